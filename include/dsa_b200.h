@@ -19,6 +19,15 @@
  *                           states and the query latent; keys written into the cache
  *   dsa_indexer_key_append  the key-cache write alone, for keys already projected
  *
+ * Beside the path, for layers and models that attend densely with grouped
+ * heads, and for whoever keeps a paged cache:
+ *
+ *   gqa_prompt_attention    causal attention over whole prompts, packed
+ *   gqa_decode_attention    attention of single query rows over a paged key-value cache
+ *   kv_cache_append         new tokens' keys and values written into their pages
+ *   kv_pages_extend, kv_pages_free, kv_pages_fork, kv_pages_copy, kv_pages_compact
+ *                           the pool of pages: handing out, taking back, sharing, moving
+ *
  * Conventions shared by every entry point
  *   - Every data pointer is a DEVICE pointer owned by the caller.  The library
  *     never allocates or frees device memory; scratch space, where a step
@@ -66,7 +75,8 @@ typedef enum {
     DSA_ERR_INVALID_ARG = 1,    /* null pointer, bad size, misaligned pointer ... */
     DSA_ERR_UNSUPPORTED = 2,    /* valid, but no kernel is built for this shape/type */
     DSA_ERR_CUDA = 3,           /* a CUDA runtime call or launch failed */
-    DSA_ERR_DEVICE_TIMEOUT = 4  /* a kernel gave up a bounded wait (see dsa_get_device_error) */
+    DSA_ERR_DEVICE_TIMEOUT = 4, /* a kernel gave up a bounded wait (see dsa_get_device_error) */
+    DSA_ERR_OUT_OF_PAGES = 5    /* a sequence found too few free pages (see dsa_get_device_error) */
 } dsa_status_t;
 
 typedef enum {
@@ -378,12 +388,196 @@ DSA_API dsa_status_t dsa_indexer_key_append(const void* k, dsa_dtype_t k_in_dtyp
                                             dsa_dtype_t k_dtype, float* k_scale, int64_t cache_rows, void* stream);
 
 /*
+ * The paged key-value cache of grouped-query attention.
+ *
+ *   k_cache, v_cache  [num_pages, n_kv_heads, page_size, head_dim] of kv_dtype (DSA_BF16,
+ *                     DSA_FP32 or DSA_FP8_E4M3), 16-byte aligned
+ *   k_scale, v_scale  [num_pages, n_kv_heads, page_size] fp32, one dequantisation scale per
+ *                     fp8 row (value = code * scale); NULL unless the cache is fp8
+ *   page_table        [batch, max_pages] int32: token s of sequence b lies in page
+ *                     page_table[b, s / page_size], at place s % page_size; -1 = no page
+ * head_dim is 64 or 128; page_size is any number >= 1.  At most 2^31 - 2
+ * cache rows (num_pages * n_kv_heads * page_size), table entries and
+ * positions per sequence.  A page may be in several sequences' rows.
+ */
+
+/*
+ * kv_cache_append -- keys and values of n new tokens into their pages: row r
+ * goes to token row_pos[r] of sequence row_batch[r].
+ *   k, v       [n, n_kv_heads, head_dim] of dtype (DSA_BF16 or DSA_FP32), rows ld_k /
+ *              ld_v elements apart (views of a fused projection's output), 16-byte
+ *              aligned rows
+ *   row_batch  [n] int32 in [0, batch);  row_pos [n] int32, < 0: the row is not stored
+ * A bf16 cache takes fp32 rows rounded to nearest even; an fp32 cache takes
+ * fp32 rows only; an fp8 cache takes finite rows, each (row, head) vector with
+ * its own scale = amax / 448 (1 for an all-zero vector), code = the nearest
+ * code of value / scale, ties to even, saturating: every operation in
+ * binary32, as in the indexer's key cache.  No two rows may name the same
+ * token (the token would hold a mixture).  A row whose sequence, position or
+ * page is out of range is skipped and reported by dsa_get_device_error.
+ */
+DSA_API dsa_status_t kv_cache_append(const void* k, int64_t ld_k, const void* v, int64_t ld_v, dsa_dtype_t dtype,
+                             const int32_t* row_batch, const int32_t* row_pos, int n, const int32_t* page_table,
+                             int batch, int max_pages, int page_size, int num_pages, int n_kv_heads, int head_dim,
+                             void* k_cache, void* v_cache, dsa_dtype_t kv_dtype, float* k_scale, float* v_scale,
+                             void* stream);
+
+/* Workspace bytes gqa_decode_attention needs for these sizes on the current
+ * device.  It grows with rows and with the GPU's size, not with lengths. */
+DSA_API size_t gqa_decode_attention_workspace_size(int rows, int n_heads, int n_kv_heads, int head_dim,
+                                           dsa_dtype_t kv_dtype);
+
+/*
+ * gqa_decode_attention -- attention of single query rows over the paged
+ * cache: row t attends to tokens 0 .. row_pos[t] of sequence row_batch[t],
+ *   z_s        = scale * q[t, h, :] . k_s[h / (n_heads / n_kv_heads), :]
+ *   out[t,h,:] = sum_s softmax_s(z) * v_s[h / (n_heads / n_kv_heads), :]
+ *   lse[t,h]   = log sum_s exp(z_s)
+ * One row per sequence decodes one token; several rows of a sequence (at
+ * successive positions) verify several tokens or run a piece of a prompt.
+ *   q          [rows, n_heads, head_dim] of dtype, rows ld_q elements apart, 16-byte
+ *              aligned rows; n_heads a multiple of n_kv_heads
+ *   row_pos    [rows] int32: last visible token; < 0: none (out = 0, lse = -inf), as
+ *              for the padding rows of a captured batch
+ *   out        [rows, n_heads, head_dim] of dtype;  lse [rows, n_heads] fp32
+ *   workspace  gqa_decode_attention_workspace_size() bytes, 256-byte aligned; needs to
+ *              hold nothing on entry
+ * Types (dtype, kv_dtype): bf16 queries over a bf16 or an fp8 cache, fp32 over
+ * fp32.  fp8 codes must be finite.  Places of a page behind the sequence's
+ * last token are not read into the result, whatever they hold.  A row whose
+ * sequence is out of range has no visible token; tokens past the table's
+ * width (row_pos >= max_pages * page_size) or in a page out of range are left
+ * out; each is reported by dsa_get_device_error.  Sums are fp32; results do
+ * not depend on the order in which blocks run.
+ */
+DSA_API dsa_status_t gqa_decode_attention(const void* q, int64_t ld_q, dsa_dtype_t dtype, const void* k_cache,
+                                  const void* v_cache, dsa_dtype_t kv_dtype, const float* k_scale,
+                                  const float* v_scale, const int32_t* page_table, int batch, int max_pages,
+                                  int page_size, int num_pages, const int32_t* row_batch, const int32_t* row_pos,
+                                  int rows, int n_heads, int n_kv_heads, int head_dim, float scale, void* out,
+                                  float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes gqa_prompt_attention needs for these sizes (0 = none). */
+DSA_API size_t gqa_prompt_attention_workspace_size(int total, int n_seqs, int n_heads, int head_dim,
+                                           dsa_dtype_t dtype);
+
+/*
+ * gqa_prompt_attention -- causal attention over whole prompts, packed one
+ * behind the other: prompt p is rows cu_seqlens[p] .. cu_seqlens[p + 1] - 1, and
+ * its row i attends to its rows j <= i,
+ *   z_j        = scale * q[i, h, :] . k[j, h / (n_heads / n_kv_heads), :]
+ *   out[i,h,:] = sum_j softmax_j(z) * v[j, h / (n_heads / n_kv_heads), :]
+ *   lse[i,h]   = log sum_j exp(z_j)
+ *   q           [total, n_heads, head_dim] of dtype (DSA_BF16 or DSA_FP32), rows ld_q
+ *               elements apart; k, v [total, n_kv_heads, head_dim], rows ld_k / ld_v
+ *               apart; 16-byte aligned rows; n_heads a multiple of n_kv_heads;
+ *               head_dim 64 or 128
+ *   cu_seqlens  [n_seqs + 1] int32, ascending from >= 0 to <= total, on the device;
+ *               empty prompts are allowed.  Rows outside every prompt are neither
+ *               read nor written.
+ *   out         [total, n_heads, head_dim] of dtype;  lse [total, n_heads] fp32
+ *   workspace   gqa_prompt_attention_workspace_size() bytes, 256-byte aligned; needs to
+ *               hold nothing on entry
+ * k and v must be finite within a prompt (a later row's infinity or NaN may
+ * reach earlier rows of its own prompt); prompts never reach one another.  A
+ * prompt whose bounds descend or leave [0, total] is skipped and reported by
+ * dsa_get_device_error.  bf16 runs on the tensor cores (P is rounded to bf16),
+ * fp32 on the CUDA cores; sums are fp32.
+ */
+DSA_API dsa_status_t gqa_prompt_attention(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
+                                  int64_t ld_v, dsa_dtype_t dtype, const int32_t* cu_seqlens, int n_seqs, int total,
+                                  int n_heads, int n_kv_heads, int head_dim, float scale, void* out, float* lse,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The pool of pages, kept on the device so that a loop that admits, branches
+ * and drops sequences needs no host read and can be captured:
+ *   page_table  [batch, max_pages] int32, the first ceil(seq_len / page_size) entries of a
+ *               row in use
+ *   seq_len     [batch] int32, tokens of each sequence (0 = empty)
+ *   ref_count   [num_pages] int32, table entries that name each page (0 = free)
+ * An empty pool is ref_count = 0, seq_len = 0, page_table = -1.  Lists hold n
+ * sequence numbers each, -1 = unused entry; a sequence listed twice counts at
+ * its first place.  Fresh pages are the lowest-numbered free ones, in the
+ * list's order, so results are deterministic.  An entry that cannot be served
+ * changes nothing and is reported by dsa_get_device_error: DSA_ERR_INVALID_ARG for
+ * a sequence, length or page out of range or listed twice, DSA_ERR_OUT_OF_PAGES
+ * for want of free pages.  Calls on one pool must be in order on one stream.
+ * The functions serve any paged cache of the library, the latent cache of
+ * dsa_sparse_mla among them: a cache is a pointer and the bytes of its pages.
+ */
+#define DSA_KV_PAGES_MAX_LIST 4096          /* list entries per call (kv_pages_copy: any number) */
+#define DSA_KV_PAGES_MAX_POOL (1 << 22)     /* pages of a pool */
+
+/*
+ * kv_pages_extend -- room for add[i] more tokens in sequence seqs[i]: fresh
+ * pages (each with count 1) until the new length fits, seq_len += add.  An
+ * entry is served when the pages asked for up to and with it are free.  A
+ * sequence that would pass max_pages * page_size tokens is refused.
+ */
+DSA_API dsa_status_t kv_pages_extend(int32_t* page_table, int batch, int max_pages, int page_size, int32_t* seq_len,
+                             int32_t* ref_count, int num_pages, const int32_t* seqs, const int32_t* add, int n,
+                             void* stream);
+
+/*
+ * kv_pages_free -- sequences seqs[i] are dropped: their pages' counts go down by
+ * one (a page is free at 0), their table entries in use to -1, their lengths to 0.
+ */
+DSA_API dsa_status_t kv_pages_free(int32_t* page_table, int batch, int max_pages, int page_size, int32_t* seq_len,
+                           int32_t* ref_count, int num_pages, const int32_t* seqs, int n, void* stream);
+
+/* Workspace bytes kv_pages_fork needs for a list of n entries. */
+DSA_API size_t kv_pages_fork_workspace_size(int n);
+
+/*
+ * kv_pages_fork -- empty sequence children[i] becomes a branch of parents[i]: full pages
+ * are shared (counts + 1); a last page that is not full gets a fresh page
+ * whose bytes are copied from the parent's in every listed cache, so that
+ * parent and branch can both grow.  Several branches of one parent are
+ * allowed; a child that is not empty is refused.
+ *   caches      host array of n_caches device pointers, 16-byte aligned (all layers' key
+ *               and value caches, fp8 scales among them); n_caches may be 0
+ *   page_bytes  host array: bytes of one page of each cache, a multiple of 16
+ *   workspace   kv_pages_fork_workspace_size(n) bytes, 16-byte aligned
+ */
+DSA_API dsa_status_t kv_pages_fork(int32_t* page_table, int batch, int max_pages, int page_size, int32_t* seq_len,
+                           int32_t* ref_count, int num_pages, const int32_t* parents, const int32_t* children, int n,
+                           void* const* caches, const size_t* page_bytes, int n_caches, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * kv_pages_copy -- page src[i] over page dst[i] in every listed cache, for n pairs
+ * (device arrays; a pair with a -1, or with src = dst, is skipped; a page out
+ * of range is skipped and reported).  No page may be written by two pairs, nor
+ * be written by one and read by another.
+ */
+DSA_API dsa_status_t kv_pages_copy(void* const* caches, const size_t* page_bytes, int n_caches, int num_pages,
+                           const int32_t* src, const int32_t* dst, int n, void* stream);
+
+/* Workspace bytes kv_pages_compact needs for a pool of num_pages. */
+DSA_API size_t kv_pages_compact_workspace_size(int num_pages);
+
+/*
+ * kv_pages_compact -- the pages in use drawn together to ids 0 .. n_live - 1: those at or
+ * above n_live (the number of pages with a positive count) move to the free places below it,
+ * both in ascending order, in every listed cache (caches, page_bytes as in kv_pages_fork); every
+ * table entry follows.  table_out and ref_out take the new table and counts; each may be
+ * its input itself.  Pages at n_live and above are free afterwards.
+ *   workspace   kv_pages_compact_workspace_size(num_pages) bytes, 16-byte aligned
+ */
+DSA_API dsa_status_t kv_pages_compact(const int32_t* page_table, int batch, int max_pages, const int32_t* ref_count,
+                              int num_pages, void* const* caches, const size_t* page_bytes, int n_caches,
+                              int32_t* table_out, int32_t* ref_out, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/*
  * dsa_get_device_error -- synchronizes `stream`, then reads and clears the
  * library's device error word on the current device.  Returns DSA_OK when
  * no kernel recorded an error, DSA_ERR_DEVICE_TIMEOUT when a kernel gave up
  * a bounded wait, DSA_ERR_INVALID_ARG when a kernel met an index, position
- * or slot out of range and skipped it, DSA_ERR_CUDA when the synchronization
- * itself failed.
+ * or slot out of range and skipped it, DSA_ERR_OUT_OF_PAGES when that did not
+ * happen but kv_pages_extend or kv_pages_fork left a sequence as it was for
+ * want of free pages, DSA_ERR_CUDA when the synchronization itself failed.
  */
 DSA_API dsa_status_t dsa_get_device_error(void* stream);
 

@@ -29,11 +29,11 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_CUDA, DSA_ERR_DEVICE_TIMEOUT = range(5)
+DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_CUDA, DSA_ERR_DEVICE_TIMEOUT, DSA_ERR_OUT_OF_PAGES = range(6)
 DSA_FP32, DSA_BF16, DSA_FP8_E4M3, DSA_FP4_E2M1 = 0, 1, 2, 3
 
 _STATUS_NAMES = {0: "DSA_OK", 1: "DSA_ERR_INVALID_ARG", 2: "DSA_ERR_UNSUPPORTED", 3: "DSA_ERR_CUDA",
-                 4: "DSA_ERR_DEVICE_TIMEOUT"}
+                 4: "DSA_ERR_DEVICE_TIMEOUT", 5: "DSA_ERR_OUT_OF_PAGES"}
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
 _f32 = ctypes.c_float
@@ -61,6 +61,21 @@ _SIGS = {
                                    _i32, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _i64, _vp, _sz, _vp]),
     "dsa_indexer_key_append": (_i32, [_vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _i64,
                                       _vp]),
+    "kv_cache_append": (_i32, [_vp, _i64, _vp, _i64, _i32, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp,
+                               _vp, _i32, _vp, _vp, _vp]),
+    "gqa_decode_attention_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+    "gqa_decode_attention": (_i32, [_vp, _i64, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp,
+                                    _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp, _sz, _vp]),
+    "gqa_prompt_attention_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+    "gqa_prompt_attention": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _f32, _vp,
+                                    _vp, _vp, _sz, _vp]),
+    "kv_pages_extend": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _vp]),
+    "kv_pages_free": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp, _i32, _vp, _i32, _vp]),
+    "kv_pages_fork_workspace_size": (_sz, [_i32]),
+    "kv_pages_fork": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _sz, _vp]),
+    "kv_pages_copy": (_i32, [_vp, _vp, _i32, _i32, _vp, _vp, _i32, _vp]),
+    "kv_pages_compact_workspace_size": (_sz, [_i32]),
+    "kv_pages_compact": (_i32, [_vp, _i32, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _sz, _vp]),
     "dsa_get_device_error": (_i32, [_vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -372,6 +387,259 @@ def indexer_key_append(k: torch.Tensor, slot: torch.Tensor, k_cache: torch.Tenso
         _check(_lib.dsa_indexer_key_append(_ptr(k), _dt(k), _ptr(rope_cos), _ptr(rope_sin), max_pos, d_rope,
                                            _ptr(pos), _ptr(slot), n, head_dim, _ptr(k_cache), fmt, _ptr(k_scale),
                                            rows, _stream(dev)), "dsa_indexer_key_append")
+
+
+# ---- grouped-query attention and its paged key-value cache -------------------
+
+def _int32(*named) -> None:
+    for name, t in named:
+        if t is not None and t.dtype != torch.int32:
+            raise TypeError(f"{name} must be int32")
+
+
+def _rows(name: str, t: torch.Tensor, dev: torch.device) -> int:
+    """Distance between the rows of a [rows, heads, dim] operand, in elements:
+    rows may be strided (views of a fused projection), heads and dims dense."""
+    if t.device != dev:
+        raise ValueError("tensors on different devices")
+    n, heads, dim = t.shape
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name}: the heads and dims of a row must be contiguous")
+    return t.stride(0) if n > 1 else heads * dim
+
+
+def _paged_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale, v_scale) -> int:
+    """Checks a cache pair's shapes; its type code."""
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise ValueError("k_cache and v_cache must be [num_pages, n_kv_heads, page_size, head_dim] of one type")
+    for s in (k_scale, v_scale):
+        if s is not None and (s.dtype != torch.float32 or s.shape != k_cache.shape[:3]):
+            raise ValueError("scales must be fp32 [num_pages, n_kv_heads, page_size]")
+    return _dt(k_cache)
+
+
+def kv_cache_append(k: torch.Tensor, v: torch.Tensor, row_batch: torch.Tensor, row_pos: torch.Tensor,
+                    page_table: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None) -> None:
+    """Write keys and values k, v [n, n_kv_heads, head_dim] (rows may be
+    strided) to token row_pos[r] of sequence row_batch[r] of the paged caches
+    [num_pages, n_kv_heads, page_size, head_dim] (row_pos < 0: not stored).
+    fp8 caches (float8_e4m3fn or uint8) take scales [num_pages, n_kv_heads, page_size]."""
+    dev = _dev(row_batch, row_pos, page_table, k_cache, v_cache, k_scale, v_scale)
+    _int32(("row_batch", row_batch), ("row_pos", row_pos), ("page_table", page_table))
+    kv = _paged_kv(k_cache, v_cache, k_scale, v_scale)
+    pages, hkv, page, d = k_cache.shape
+    n = k.shape[0]
+    if k.shape != (n, hkv, d) or v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must be [n, n_kv_heads, head_dim] of one type")
+    if row_batch.shape != (n,) or row_pos.shape != (n,):
+        raise ValueError("row_batch and row_pos must be [n]")
+    ld_k, ld_v = _rows("k", k, dev), _rows("v", v, dev)
+    with torch.cuda.device(dev):
+        _check(_lib.kv_cache_append(k.data_ptr(), ld_k, v.data_ptr(), ld_v, _dt(k), row_batch.data_ptr(),
+                                    row_pos.data_ptr(), n, page_table.data_ptr(), page_table.shape[0],
+                                    page_table.shape[1], page, pages, hkv, d, k_cache.data_ptr(), v_cache.data_ptr(),
+                                    kv, _ptr(k_scale), _ptr(v_scale), _stream(dev)), "kv_cache_append")
+
+
+def gqa_decode_attention_workspace_size(rows: int, n_heads: int, n_kv_heads: int, head_dim: int,
+                                        kv_dtype: torch.dtype) -> int:
+    dt = {torch.float32: DSA_FP32, torch.bfloat16: DSA_BF16}.get(kv_dtype, DSA_FP8_E4M3)
+    return int(_lib.gqa_decode_attention_workspace_size(rows, n_heads, n_kv_heads, head_dim, dt))
+
+
+def gqa_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                         row_batch: torch.Tensor, row_pos: torch.Tensor, scale: float,
+                         k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                         out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of query rows q [rows, n_heads, head_dim] (rows may be
+    strided) over tokens 0 .. row_pos[t] of sequence row_batch[t] of the paged
+    caches: (out [rows, n_heads, head_dim], lse [rows, n_heads] fp32).
+    row_pos < 0: nothing visible (out = 0, lse = -inf)."""
+    dev = _dev(k_cache, v_cache, page_table, row_batch, row_pos, k_scale, v_scale, out, lse, workspace)
+    _int32(("page_table", page_table), ("row_batch", row_batch), ("row_pos", row_pos))
+    kv = _paged_kv(k_cache, v_cache, k_scale, v_scale)
+    pages, hkv, page, d = k_cache.shape
+    rows, H, d_q = q.shape
+    if d_q != d:
+        raise ValueError("q and the caches differ in head_dim")
+    if row_batch.shape != (rows,) or row_pos.shape != (rows,):
+        raise ValueError("row_batch and row_pos must be [rows]")
+    ld_q = _rows("q", q, dev)
+    if out is None:
+        out = torch.empty((rows, H, d), dtype=q.dtype, device=dev)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must be [rows, n_heads, head_dim] of q's type")
+    if lse is None:
+        lse = torch.empty((rows, H), dtype=torch.float32, device=dev)
+    elif lse.shape != (rows, H) or lse.dtype != torch.float32:
+        raise ValueError("lse must be fp32 [rows, n_heads]")
+    with torch.cuda.device(dev):
+        if workspace is None:
+            need = _lib.gqa_decode_attention_workspace_size(rows, H, hkv, d, kv)
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        wsb = workspace.numel() * workspace.element_size()
+        _check(_lib.gqa_decode_attention(q.data_ptr(), ld_q, _dt(q), k_cache.data_ptr(), v_cache.data_ptr(), kv,
+                                         _ptr(k_scale), _ptr(v_scale), page_table.data_ptr(), page_table.shape[0],
+                                         page_table.shape[1], page, pages, row_batch.data_ptr(), row_pos.data_ptr(),
+                                         rows, H, hkv, d, float(scale), out.data_ptr(), lse.data_ptr(),
+                                         workspace.data_ptr(), wsb, _stream(dev)), "gqa_decode_attention")
+    return out, lse
+
+
+def gqa_prompt_attention_workspace_size(total: int, n_seqs: int, n_heads: int, head_dim: int,
+                                        dtype: torch.dtype) -> int:
+    dt = DSA_FP32 if dtype == torch.float32 else DSA_BF16
+    return int(_lib.gqa_prompt_attention_workspace_size(total, n_seqs, n_heads, head_dim, dt))
+
+
+def gqa_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, scale: float,
+                         out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Causal attention within each prompt of a packed batch: q [total,
+    n_heads, head_dim], k and v [total, n_kv_heads, head_dim] (rows may be
+    strided), cu_seqlens int32 [n_seqs + 1]: (out [total, n_heads, head_dim],
+    lse [total, n_heads] fp32).  Rows outside every prompt are left as they
+    were in out and lse (undefined when these are allocated here)."""
+    dev = _dev(cu_seqlens, out, lse, workspace)
+    _int32(("cu_seqlens", cu_seqlens))
+    T, H, d = q.shape
+    hkv = k.shape[1]
+    if k.shape != (T, hkv, d) or v.shape != k.shape or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("k and v must be [total, n_kv_heads, head_dim] of q's type")
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be [n_seqs + 1]")
+    n_seqs = cu_seqlens.shape[0] - 1
+    ld_q, ld_k, ld_v = _rows("q", q, dev), _rows("k", k, dev), _rows("v", v, dev)
+    if out is None:
+        out = torch.empty((T, H, d), dtype=q.dtype, device=dev)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must be [total, n_heads, head_dim] of q's type")
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    elif lse.shape != (T, H) or lse.dtype != torch.float32:
+        raise ValueError("lse must be fp32 [total, n_heads]")
+    dt = _dt(q)
+    with torch.cuda.device(dev):
+        if workspace is None:
+            need = _lib.gqa_prompt_attention_workspace_size(T, n_seqs, H, d, dt)
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        wsb = workspace.numel() * workspace.element_size()
+        _check(_lib.gqa_prompt_attention(q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v, dt,
+                                         cu_seqlens.data_ptr(), n_seqs, T, H, hkv, d, float(scale), out.data_ptr(),
+                                         lse.data_ptr(), workspace.data_ptr(), wsb, _stream(dev)),
+               "gqa_prompt_attention")
+    return out, lse
+
+
+def _books(page_table: torch.Tensor, seq_len: torch.Tensor, ref_count: torch.Tensor, *lists) -> Tuple[torch.device, int]:
+    """Checks a pool's books and lists: (device, list entries)."""
+    dev = _dev(page_table, seq_len, ref_count, *lists)
+    for t in (page_table, seq_len, ref_count, *lists):
+        if t.dtype != torch.int32:
+            raise TypeError("page tables, lengths, counts and lists must be int32")
+    if page_table.dim() != 2 or seq_len.shape != (page_table.shape[0],) or ref_count.dim() != 1:
+        raise ValueError("page_table [batch, max_pages], seq_len [batch] and ref_count [num_pages] are needed")
+    n = lists[0].numel() if lists else 0
+    for t in lists:
+        if t.shape != (n,):
+            raise ValueError("lists must be [n], of one length")
+    return dev, n
+
+
+def _cache_list(caches, num_pages: int, dev: torch.device):
+    """A list of caches [num_pages, ...] as C arrays: (pointers, page bytes, count)."""
+    n = len(caches)
+    ptrs, sizes = (_vp * n)(), (_sz * n)()
+    for i, c in enumerate(caches):
+        if c.device != dev or not c.is_contiguous() or c.dim() < 1 or c.shape[0] != num_pages:
+            raise ValueError("caches must be contiguous [num_pages, ...] tensors on the pool's device")
+        ptrs[i] = c.data_ptr()
+        sizes[i] = c.numel() // num_pages * c.element_size() if num_pages else 0
+    return ptrs, sizes, n
+
+
+def kv_pages_extend(page_table: torch.Tensor, seq_len: torch.Tensor, ref_count: torch.Tensor, seqs: torch.Tensor,
+                    add: torch.Tensor, page_size: int) -> None:
+    """Room for add[i] more tokens in sequence seqs[i]: fresh pages (lowest
+    free ids first) and seq_len grown, in place."""
+    dev, n = _books(page_table, seq_len, ref_count, seqs, add)
+    with torch.cuda.device(dev):
+        _check(_lib.kv_pages_extend(page_table.data_ptr(), page_table.shape[0], page_table.shape[1], page_size,
+                                    seq_len.data_ptr(), ref_count.data_ptr(), ref_count.shape[0], seqs.data_ptr(),
+                                    add.data_ptr(), n, _stream(dev)), "kv_pages_extend")
+
+
+def kv_pages_free(page_table: torch.Tensor, seq_len: torch.Tensor, ref_count: torch.Tensor, seqs: torch.Tensor,
+                  page_size: int) -> None:
+    """Drop sequences seqs[i]: their pages' counts go down, their table rows
+    and lengths are cleared, in place."""
+    dev, n = _books(page_table, seq_len, ref_count, seqs)
+    with torch.cuda.device(dev):
+        _check(_lib.kv_pages_free(page_table.data_ptr(), page_table.shape[0], page_table.shape[1], page_size,
+                                  seq_len.data_ptr(), ref_count.data_ptr(), ref_count.shape[0], seqs.data_ptr(), n,
+                                  _stream(dev)), "kv_pages_free")
+
+
+def kv_pages_fork(page_table: torch.Tensor, seq_len: torch.Tensor, ref_count: torch.Tensor, parents: torch.Tensor,
+                  children: torch.Tensor, page_size: int, caches=(), workspace: Optional[torch.Tensor] = None) -> None:
+    """Empty sequence children[i] becomes a branch of parents[i]: full pages
+    shared, a last page that is not full copied to a fresh page in every
+    cache of `caches` ([num_pages, ...] tensors), in place."""
+    dev, n = _books(page_table, seq_len, ref_count, parents, children)
+    ptrs, sizes, n_caches = _cache_list(caches, ref_count.shape[0], dev)
+    if workspace is None:
+        workspace = torch.empty(max(8 * n, 1), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the pool's device")
+    with torch.cuda.device(dev):
+        _check(_lib.kv_pages_fork(page_table.data_ptr(), page_table.shape[0], page_table.shape[1], page_size,
+                                  seq_len.data_ptr(), ref_count.data_ptr(), ref_count.shape[0], parents.data_ptr(),
+                                  children.data_ptr(), n, ptrs, sizes, n_caches, workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), _stream(dev)), "kv_pages_fork")
+
+
+def kv_pages_copy(caches, src: torch.Tensor, dst: torch.Tensor) -> None:
+    """Copy page src[i] over page dst[i] in every cache of `caches` ([num_pages,
+    ...] tensors); pairs with a -1 are skipped."""
+    dev = _dev(src, dst)
+    _int32(("src", src), ("dst", dst))
+    if src.dim() != 1 or src.shape != dst.shape:
+        raise ValueError("src and dst must be [n]")
+    if not caches:
+        return
+    pages = caches[0].shape[0]
+    ptrs, sizes, n_caches = _cache_list(caches, pages, dev)
+    with torch.cuda.device(dev):
+        _check(_lib.kv_pages_copy(ptrs, sizes, n_caches, pages, src.data_ptr(), dst.data_ptr(), src.shape[0],
+                                  _stream(dev)), "kv_pages_copy")
+
+
+def kv_pages_compact(page_table: torch.Tensor, ref_count: torch.Tensor, caches=(),
+                     table_out: Optional[torch.Tensor] = None, ref_out: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Draw the pages in use together at the pool's lowest ids, moving the
+    fewest pages in every cache of `caches`: (new table, new counts), written
+    to table_out / ref_out (which may be the inputs) when given."""
+    dev = _dev(page_table, ref_count, table_out, ref_out, workspace)
+    _int32(("page_table", page_table), ("ref_count", ref_count), ("table_out", table_out), ("ref_out", ref_out))
+    if page_table.dim() != 2 or ref_count.dim() != 1:
+        raise ValueError("page_table [batch, max_pages] and ref_count [num_pages] are needed")
+    table_out = torch.empty_like(page_table) if table_out is None else table_out
+    ref_out = torch.empty_like(ref_count) if ref_out is None else ref_out
+    if table_out.shape != page_table.shape or ref_out.shape != ref_count.shape:
+        raise ValueError("table_out and ref_out must have their inputs' shapes")
+    pages = ref_count.shape[0]
+    ptrs, sizes, n_caches = _cache_list(caches, pages, dev)
+    if workspace is None:
+        workspace = torch.empty(_lib.kv_pages_compact_workspace_size(pages), dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        _check(_lib.kv_pages_compact(page_table.data_ptr(), page_table.shape[0], page_table.shape[1],
+                                     ref_count.data_ptr(), pages, ptrs, sizes, n_caches, table_out.data_ptr(),
+                                     ref_out.data_ptr(), workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), _stream(dev)), "kv_pages_compact")
+    return table_out, ref_out
 
 
 def get_device_error(device: Optional[torch.device] = None) -> int:

@@ -438,6 +438,317 @@ dsa_status_t dsa_sparse_mla_noalloc(const void* q, const void* kv, dsa_dtype_t d
                           n_heads, d_qk, d_v, scale, out, lse, scratch, scratch ? kMlaScratchBytes : 0, stream);
 }
 
+namespace {
+
+bool kv_head_dim(int d) { return d == 64 || d == 128; }
+
+// Cache geometry shared by kv_cache_append and gqa_decode_attention.
+dsa_status_t check_paged_kv(const char* name, const int32_t* page_table, int batch, int max_pages, int page_size,
+                            int num_pages, int n_kv_heads, int head_dim, const void* k_cache, const void* v_cache,
+                            dsa_dtype_t kv_dtype, const float* k_scale, const float* v_scale) {
+    if (batch <= 0 || max_pages <= 0 || page_size <= 0 || num_pages <= 0 || n_kv_heads <= 0 || head_dim <= 0)
+        return fail(DSA_ERR_INVALID_ARG, "%s: bad sizes", name);
+    if (!page_table || !k_cache || !v_cache) return fail(DSA_ERR_INVALID_ARG, "%s: null pointer", name);
+    if (kv_dtype != DSA_BF16 && kv_dtype != DSA_FP32 && kv_dtype != DSA_FP8_E4M3)
+        return fail(DSA_ERR_UNSUPPORTED, "%s: the cache must be bf16, fp32 or fp8", name);
+    if ((kv_dtype == DSA_FP8_E4M3) != (k_scale != nullptr) || (k_scale != nullptr) != (v_scale != nullptr))
+        return fail(DSA_ERR_INVALID_ARG, "%s: k_scale and v_scale must be given exactly when the cache is fp8", name);
+    if (!kv_head_dim(head_dim)) return fail(DSA_ERR_UNSUPPORTED, "%s: head_dim must be 64 or 128", name);
+    if (n_kv_heads > 1024) return fail(DSA_ERR_UNSUPPORTED, "%s: n_kv_heads > 1024", name);
+    const int64_t lim = ((int64_t)1 << 31) - 2;
+    if ((int64_t)num_pages * page_size > lim || (int64_t)num_pages * page_size * n_kv_heads > lim ||
+        (int64_t)batch * max_pages > lim || (int64_t)max_pages * page_size > lim)
+        return fail(DSA_ERR_UNSUPPORTED, "%s: more than 2^31 - 2 cache rows, table entries or positions", name);
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16))
+        return fail(DSA_ERR_INVALID_ARG, "%s: the caches must be 16-byte aligned", name);
+    return DSA_OK;
+}
+
+// A [rows, heads, head_dim] operand whose rows are `ld` elements apart.
+dsa_status_t check_rows(const char* name, const char* what, const void* p, int64_t ld, int heads, int head_dim,
+                        dsa_dtype_t t) {
+    if (!p) return fail(DSA_ERR_INVALID_ARG, "%s: null pointer (%s)", name, what);
+    if (ld < (int64_t)heads * head_dim) return fail(DSA_ERR_INVALID_ARG, "%s: rows of %s overlap", name, what);
+    if (!aligned(p, 16) || (ld * dtype_size(t)) % 16)
+        return fail(DSA_ERR_INVALID_ARG, "%s: %s and its row stride must be 16-byte aligned", name, what);
+    return DSA_OK;
+}
+
+// The pool's books.
+dsa_status_t check_books(const char* name, const int32_t* page_table, int batch, int max_pages, int page_size,
+                         const int32_t* seq_len, const int32_t* ref_count, int num_pages, int n) {
+    if (batch <= 0 || max_pages <= 0 || page_size <= 0 || num_pages <= 0 || n < 0)
+        return fail(DSA_ERR_INVALID_ARG, "%s: bad sizes", name);
+    if (n > DSA_KV_PAGES_MAX_LIST) return fail(DSA_ERR_UNSUPPORTED, "%s: more than %d list entries", name, DSA_KV_PAGES_MAX_LIST);
+    if (num_pages > DSA_KV_PAGES_MAX_POOL) return fail(DSA_ERR_UNSUPPORTED, "%s: more than %d pages", name, DSA_KV_PAGES_MAX_POOL);
+    const int64_t lim = ((int64_t)1 << 31) - 2;
+    if ((int64_t)batch * max_pages > lim || (int64_t)n * max_pages > lim)
+        return fail(DSA_ERR_UNSUPPORTED, "%s: more than 2^31 - 2 table entries", name);
+    if (!page_table || !seq_len || !ref_count) return fail(DSA_ERR_INVALID_ARG, "%s: null pointer", name);
+    return DSA_OK;
+}
+
+dsa_status_t check_caches(const char* name, void* const* caches, const size_t* page_bytes, int n_caches) {
+    if (n_caches < 0 || (n_caches > 0 && (!caches || !page_bytes)))
+        return fail(DSA_ERR_INVALID_ARG, "%s: bad cache list", name);
+    for (int i = 0; i < n_caches; ++i) {
+        if (!caches[i] || !aligned(caches[i], 16))
+            return fail(DSA_ERR_INVALID_ARG, "%s: cache %d is null or not 16-byte aligned", name, i);
+        if (page_bytes[i] == 0 || page_bytes[i] % 16 || page_bytes[i] > ((size_t)1 << 30))
+            return fail(DSA_ERR_UNSUPPORTED, "%s: the page bytes of cache %d must be a multiple of 16, at most 2^30", name, i);
+    }
+    return DSA_OK;
+}
+
+}  // namespace
+
+dsa_status_t kv_cache_append(const void* k, int64_t ld_k, const void* v, int64_t ld_v, dsa_dtype_t dtype,
+                             const int32_t* row_batch, const int32_t* row_pos, int n, const int32_t* page_table,
+                             int batch, int max_pages, int page_size, int num_pages, int n_kv_heads, int head_dim,
+                             void* k_cache, void* v_cache, dsa_dtype_t kv_dtype, float* k_scale, float* v_scale,
+                             void* stream) {
+    const char* name = "kv_cache_append";
+    if (n < 0) return fail(DSA_ERR_INVALID_ARG, "%s: bad sizes", name);
+    if (n == 0) return DSA_OK;
+    dsa_status_t st = check_paged_kv(name, page_table, batch, max_pages, page_size, num_pages, n_kv_heads, head_dim,
+                                     k_cache, v_cache, kv_dtype, k_scale, v_scale);
+    if (st != DSA_OK) return st;
+    if (dtype != DSA_BF16 && dtype != DSA_FP32) return fail(DSA_ERR_UNSUPPORTED, "%s: k and v must be bf16 or fp32", name);
+    if (kv_dtype == DSA_FP32 && dtype != DSA_FP32)
+        return fail(DSA_ERR_UNSUPPORTED, "%s: an fp32 cache takes fp32 keys and values", name);
+    if (!row_batch || !row_pos) return fail(DSA_ERR_INVALID_ARG, "%s: null pointer", name);
+    if ((st = check_rows(name, "k", k, ld_k, n_kv_heads, head_dim, dtype)) != DSA_OK) return st;
+    if ((st = check_rows(name, "v", v, ld_v, n_kv_heads, head_dim, dtype)) != DSA_OK) return st;
+    dsa::Launch L;
+    if ((st = make_launch(stream, &L)) != DSA_OK) return st;
+    dsa::AppendArgs a;
+    a.k = k;
+    a.v = v;
+    a.ld_k = ld_k;
+    a.ld_v = ld_v;
+    a.row_batch = row_batch;
+    a.row_pos = row_pos;
+    a.n = n;
+    a.n_kv_heads = n_kv_heads;
+    a.page_table = page_table;
+    a.batch = batch;
+    a.max_pages = max_pages;
+    a.page_size = page_size;
+    a.num_pages = num_pages;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.err = L.err;
+    return cuda_status(dsa::launch_kv_append(L, a, dtype, kv_dtype, head_dim), "kv_cache_append launch");
+}
+
+size_t gqa_decode_attention_workspace_size(int rows, int n_heads, int n_kv_heads, int head_dim, dsa_dtype_t kv_dtype) {
+    if (rows <= 0 || n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads || !kv_head_dim(head_dim)) return 0;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        sms = 1024;  // no device: size for a large GPU
+    return dsa::gqa_decode_workspace_bytes(rows, n_heads, n_kv_heads, head_dim, kv_dtype, sms);
+}
+
+dsa_status_t gqa_decode_attention(const void* q, int64_t ld_q, dsa_dtype_t dtype, const void* k_cache,
+                                  const void* v_cache, dsa_dtype_t kv_dtype, const float* k_scale,
+                                  const float* v_scale, const int32_t* page_table, int batch, int max_pages,
+                                  int page_size, int num_pages, const int32_t* row_batch, const int32_t* row_pos,
+                                  int rows, int n_heads, int n_kv_heads, int head_dim, float scale, void* out,
+                                  float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    const char* name = "gqa_decode_attention";
+    if (rows < 0) return fail(DSA_ERR_INVALID_ARG, "%s: bad sizes", name);
+    if (rows == 0) return DSA_OK;
+    dsa_status_t st = check_paged_kv(name, page_table, batch, max_pages, page_size, num_pages, n_kv_heads, head_dim,
+                                     k_cache, v_cache, kv_dtype, k_scale, v_scale);
+    if (st != DSA_OK) return st;
+    if (!(dtype == DSA_FP32 && kv_dtype == DSA_FP32) &&
+        !(dtype == DSA_BF16 && (kv_dtype == DSA_BF16 || kv_dtype == DSA_FP8_E4M3)))
+        return fail(DSA_ERR_UNSUPPORTED, "%s: unsupported query / cache type pair", name);
+    if (n_heads <= 0 || n_heads % n_kv_heads)
+        return fail(DSA_ERR_INVALID_ARG, "%s: n_heads must be a multiple of n_kv_heads", name);
+    if (!row_batch || !row_pos || !out || !lse) return fail(DSA_ERR_INVALID_ARG, "%s: null pointer", name);
+    if ((st = check_rows(name, "q", q, ld_q, n_heads, head_dim, dtype)) != DSA_OK) return st;
+    if (!aligned(out, 16)) return fail(DSA_ERR_INVALID_ARG, "%s: out must be 16-byte aligned", name);
+    if (!(scale > 0.f) || !(scale < 1e30f)) return fail(DSA_ERR_INVALID_ARG, "%s: scale must be positive and finite", name);
+    const int64_t units = ((int64_t)max_pages * page_size - 1) / 64 + 1, lim = ((int64_t)1 << 31) - 2;
+    if ((int64_t)rows * units > lim || units * n_heads > lim || (int64_t)rows * n_heads > lim)
+        return fail(DSA_ERR_UNSUPPORTED, "%s: too many rows, heads or positions", name);
+    dsa::Launch L;
+    if ((st = make_launch(stream, &L)) != DSA_OK) return st;
+    const size_t need = dsa::gqa_decode_workspace_bytes(rows, n_heads, n_kv_heads, head_dim, kv_dtype, L.num_sms);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 256))
+        return fail(DSA_ERR_INVALID_ARG, "%s: a 256-byte aligned workspace of %zu bytes is needed", name, need);
+    dsa::DecodeArgs a;
+    a.q = q;
+    a.ld_q = ld_q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.page_table = page_table;
+    a.batch = batch;
+    a.max_pages = max_pages;
+    a.page_size = page_size;
+    a.num_pages = num_pages;
+    a.row_batch = row_batch;
+    a.row_pos = row_pos;
+    a.rows = rows;
+    a.n_heads = n_heads;
+    a.n_kv_heads = n_kv_heads;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.out = out;
+    a.lse = lse;
+    a.err = L.err;
+    return cuda_status(dsa::launch_gqa_decode(L, a, kv_dtype, head_dim, workspace), "gqa_decode_attention launch");
+}
+
+size_t gqa_prompt_attention_workspace_size(int total, int n_seqs, int n_heads, int head_dim, dsa_dtype_t dtype) {
+    if (total <= 0 || n_seqs <= 0 || n_heads <= 0 || !kv_head_dim(head_dim)) return 0;
+    return dsa::gqa_prompt_workspace_bytes(total, n_seqs, dtype);
+}
+
+dsa_status_t gqa_prompt_attention(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
+                                  int64_t ld_v, dsa_dtype_t dtype, const int32_t* cu_seqlens, int n_seqs, int total,
+                                  int n_heads, int n_kv_heads, int head_dim, float scale, void* out, float* lse,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+    const char* name = "gqa_prompt_attention";
+    if (n_seqs < 0 || total < 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0)
+        return fail(DSA_ERR_INVALID_ARG, "%s: bad sizes", name);
+    if (n_heads % n_kv_heads) return fail(DSA_ERR_INVALID_ARG, "%s: n_heads must be a multiple of n_kv_heads", name);
+    if (n_seqs == 0 || total == 0) return DSA_OK;
+    if (dtype != DSA_BF16 && dtype != DSA_FP32) return fail(DSA_ERR_UNSUPPORTED, "%s: dtype must be bf16 or fp32", name);
+    if (!kv_head_dim(head_dim)) return fail(DSA_ERR_UNSUPPORTED, "%s: head_dim must be 64 or 128", name);
+    if (!cu_seqlens || !out || !lse) return fail(DSA_ERR_INVALID_ARG, "%s: null pointer", name);
+    dsa_status_t st = check_rows(name, "q", q, ld_q, n_heads, head_dim, dtype);
+    if (st != DSA_OK) return st;
+    if ((st = check_rows(name, "k", k, ld_k, n_kv_heads, head_dim, dtype)) != DSA_OK) return st;
+    if ((st = check_rows(name, "v", v, ld_v, n_kv_heads, head_dim, dtype)) != DSA_OK) return st;
+    if (!aligned(out, 16)) return fail(DSA_ERR_INVALID_ARG, "%s: out must be 16-byte aligned", name);
+    if (!(scale > 0.f) || !(scale < 1e30f)) return fail(DSA_ERR_INVALID_ARG, "%s: scale must be positive and finite", name);
+    const int64_t tiles = (int64_t)total / 64 + (n_seqs < total ? n_seqs : total);
+    if (tiles * n_heads > ((int64_t)1 << 31) - 2) return fail(DSA_ERR_UNSUPPORTED, "%s: too many rows and heads", name);
+    dsa::Launch L;
+    if ((st = make_launch(stream, &L)) != DSA_OK) return st;
+    const size_t need = dsa::gqa_prompt_workspace_bytes(total, n_seqs, dtype);
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+        return fail(DSA_ERR_INVALID_ARG, "%s: a 256-byte aligned workspace of %zu bytes is needed", name, need);
+    dsa::PromptArgs a;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.ld_q = ld_q;
+    a.ld_k = ld_k;
+    a.ld_v = ld_v;
+    a.cu_seqlens = cu_seqlens;
+    a.n_seqs = n_seqs;
+    a.total = total;
+    a.n_heads = n_heads;
+    a.n_kv_heads = n_kv_heads;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.out = out;
+    a.lse = lse;
+    a.err = L.err;
+    return cuda_status(dsa::launch_gqa_prompt_simt(L, a, dtype, head_dim), "gqa_prompt_attention launch");
+}
+
+dsa_status_t kv_pages_copy(void* const* caches, const size_t* page_bytes, int n_caches, int num_pages,
+                           const int32_t* src, const int32_t* dst, int n, void* stream) {
+    const char* name = "kv_pages_copy";
+    if (n < 0 || num_pages <= 0) return fail(DSA_ERR_INVALID_ARG, "%s: bad sizes", name);
+    dsa_status_t st = check_caches(name, caches, page_bytes, n_caches);
+    if (st != DSA_OK) return st;
+    if (n == 0 || n_caches == 0) return DSA_OK;
+    if (!src || !dst) return fail(DSA_ERR_INVALID_ARG, "%s: null pointer", name);
+    dsa::Launch L;
+    if ((st = make_launch(stream, &L)) != DSA_OK) return st;
+    const dsa::CacheList l = {caches, page_bytes, n_caches, num_pages};
+    return cuda_status(dsa::launch_kv_copy(L, l, src, dst, n), "kv_pages_copy launch");
+}
+
+dsa_status_t kv_pages_extend(int32_t* page_table, int batch, int max_pages, int page_size, int32_t* seq_len,
+                             int32_t* ref_count, int num_pages, const int32_t* seqs, const int32_t* add, int n,
+                             void* stream) {
+    const char* name = "kv_pages_extend";
+    dsa_status_t st = check_books(name, page_table, batch, max_pages, page_size, seq_len, ref_count, num_pages, n);
+    if (st != DSA_OK) return st;
+    if (n == 0) return DSA_OK;
+    if (!seqs || !add) return fail(DSA_ERR_INVALID_ARG, "%s: null pointer", name);
+    dsa::Launch L;
+    if ((st = make_launch(stream, &L)) != DSA_OK) return st;
+    dsa::BooksArgs a = {page_table, seq_len, ref_count, batch, max_pages, page_size, num_pages, seqs, add,
+                        nullptr, nullptr, n, nullptr, nullptr, L.err};
+    return cuda_status(dsa::launch_kv_extend(L, a), "kv_pages_extend launch");
+}
+
+dsa_status_t kv_pages_free(int32_t* page_table, int batch, int max_pages, int page_size, int32_t* seq_len,
+                           int32_t* ref_count, int num_pages, const int32_t* seqs, int n, void* stream) {
+    const char* name = "kv_pages_free";
+    dsa_status_t st = check_books(name, page_table, batch, max_pages, page_size, seq_len, ref_count, num_pages, n);
+    if (st != DSA_OK) return st;
+    if (n == 0) return DSA_OK;
+    if (!seqs) return fail(DSA_ERR_INVALID_ARG, "%s: null pointer", name);
+    dsa::Launch L;
+    if ((st = make_launch(stream, &L)) != DSA_OK) return st;
+    dsa::BooksArgs a = {page_table, seq_len, ref_count, batch, max_pages, page_size, num_pages, seqs, nullptr,
+                        nullptr, nullptr, n, nullptr, nullptr, L.err};
+    return cuda_status(dsa::launch_kv_free(L, a), "kv_pages_free launch");
+}
+
+size_t kv_pages_fork_workspace_size(int n) { return n > 0 ? dsa::kv_fork_workspace_bytes(n) : 0; }
+
+dsa_status_t kv_pages_fork(int32_t* page_table, int batch, int max_pages, int page_size, int32_t* seq_len,
+                           int32_t* ref_count, int num_pages, const int32_t* parents, const int32_t* children, int n,
+                           void* const* caches, const size_t* page_bytes, int n_caches, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+    const char* name = "kv_pages_fork";
+    dsa_status_t st = check_books(name, page_table, batch, max_pages, page_size, seq_len, ref_count, num_pages, n);
+    if (st != DSA_OK) return st;
+    if ((st = check_caches(name, caches, page_bytes, n_caches)) != DSA_OK) return st;
+    if (n == 0) return DSA_OK;
+    if (!parents || !children) return fail(DSA_ERR_INVALID_ARG, "%s: null pointer", name);
+    const size_t need = dsa::kv_fork_workspace_bytes(n);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
+        return fail(DSA_ERR_INVALID_ARG, "%s: a 16-byte aligned workspace of %zu bytes is needed", name, need);
+    dsa::Launch L;
+    if ((st = make_launch(stream, &L)) != DSA_OK) return st;
+    dsa::BooksArgs a = {page_table, seq_len, ref_count, batch, max_pages, page_size, num_pages, nullptr, nullptr,
+                        parents, children, n, nullptr, nullptr, L.err};
+    const dsa::CacheList l = {caches, page_bytes, n_caches, num_pages};
+    return cuda_status(dsa::launch_kv_fork(L, a, l, workspace), "kv_pages_fork launch");
+}
+
+size_t kv_pages_compact_workspace_size(int num_pages) {
+    return num_pages > 0 ? dsa::kv_compact_workspace_bytes(num_pages) : 0;
+}
+
+dsa_status_t kv_pages_compact(const int32_t* page_table, int batch, int max_pages, const int32_t* ref_count,
+                              int num_pages, void* const* caches, const size_t* page_bytes, int n_caches,
+                              int32_t* table_out, int32_t* ref_out, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+    const char* name = "kv_pages_compact";
+    if (!table_out || !ref_out) return fail(DSA_ERR_INVALID_ARG, "%s: null pointer", name);
+    dsa_status_t st = check_books(name, page_table, batch, max_pages, 1, ref_count, ref_count, num_pages, 0);
+    if (st != DSA_OK) return st;
+    if ((st = check_caches(name, caches, page_bytes, n_caches)) != DSA_OK) return st;
+    const size_t table_bytes = (size_t)batch * max_pages * 4, ref_bytes = (size_t)num_pages * 4;
+    auto overlap = [](const void* x, const void* y, size_t n) {
+        return x != y && (const char*)x < (const char*)y + n && (const char*)y < (const char*)x + n;
+    };
+    if (overlap(page_table, table_out, table_bytes) || overlap(ref_count, ref_out, ref_bytes))
+        return fail(DSA_ERR_INVALID_ARG, "%s: an output overlaps its input without being it", name);
+    const size_t need = dsa::kv_compact_workspace_bytes(num_pages);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
+        return fail(DSA_ERR_INVALID_ARG, "%s: a 16-byte aligned workspace of %zu bytes is needed", name, need);
+    dsa::Launch L;
+    if ((st = make_launch(stream, &L)) != DSA_OK) return st;
+    dsa::CompactArgs a = {page_table, ref_count, table_out, ref_out, batch, max_pages, num_pages,
+                          nullptr, nullptr, nullptr, nullptr, nullptr, L.err};
+    const dsa::CacheList l = {caches, page_bytes, n_caches, num_pages};
+    return cuda_status(dsa::launch_kv_compact(L, a, l, workspace), "kv_pages_compact launch");
+}
+
 dsa_status_t dsa_get_device_error(void* stream) {
     dsa::Launch L;
     dsa_status_t st = make_launch(stream, &L);
@@ -453,7 +764,9 @@ dsa_status_t dsa_get_device_error(void* stream) {
     if (e != cudaSuccess) return cuda_status(e, "dsa_get_device_error: clear");
     if (word & (dsa::DEV_ERR_TIMEOUT_TMA | dsa::DEV_ERR_TIMEOUT_MMA | dsa::DEV_ERR_TIMEOUT_PEER))
         return fail(DSA_ERR_DEVICE_TIMEOUT, "a kernel gave up a bounded wait (device error word 0x%x)", word);
-    return fail(DSA_ERR_INVALID_ARG, "a kernel met an out-of-range index and skipped it (device error word 0x%x)", word);
+    if (word & dsa::DEV_ERR_BAD_INDEX)
+        return fail(DSA_ERR_INVALID_ARG, "a kernel met an out-of-range index and skipped it (device error word 0x%x)", word);
+    return fail(DSA_ERR_OUT_OF_PAGES, "a sequence found too few free pages and was left as it was (device error word 0x%x)", word);
 }
 
 }  // extern "C"

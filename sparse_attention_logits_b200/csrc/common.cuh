@@ -21,6 +21,7 @@ enum : unsigned {
     DEV_ERR_TIMEOUT_MMA = 2u,      // a wait for a tensor-core commit ran out
     DEV_ERR_TIMEOUT_PEER = 4u,     // a wait on a partner CTA of the cluster ran out
     DEV_ERR_BAD_INDEX = 8u,        // an index outside [0, ctx_len) was met and skipped
+    DEV_ERR_NO_PAGES = 16u,        // a sequence found too few free pages and was left as it was
 };
 
 constexpr int kMaxDevices = 64;

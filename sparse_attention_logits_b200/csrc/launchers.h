@@ -83,4 +83,104 @@ cudaError_t launch_indexer_prepare(const Launch& L, const PrepareArgs& a, void* 
 cudaError_t launch_key_append(const Launch& L, const void* k, dsa_dtype_t k_in, int n, const int32_t* pos,
                               const int64_t* slot, const float* rope_cos, const float* rope_sin, int max_pos,
                               int d_rope, void* cache, dsa_dtype_t fmt, float* k_scale, int64_t cache_rows);
+
+// Paged key-value cache (validated arguments of kv_cache_append).
+struct AppendArgs {
+    const void* k;              // [n, n_kv_heads, head_dim], rows ld_k / ld_v elements apart
+    const void* v;
+    int64_t ld_k, ld_v;
+    const int32_t* row_batch;   // [n]
+    const int32_t* row_pos;     // [n]
+    int n, n_kv_heads;
+    const int32_t* page_table;  // [batch, max_pages]
+    int batch, max_pages, page_size, num_pages;
+    void* k_cache;              // [num_pages, n_kv_heads, page_size, head_dim]
+    void* v_cache;
+    float* k_scale;             // [num_pages, n_kv_heads, page_size] (fp8)
+    float* v_scale;
+    unsigned* err;
+};
+cudaError_t launch_kv_append(const Launch& L, const AppendArgs& a, dsa_dtype_t in, dsa_dtype_t fmt, int head_dim);
+
+// The pool's books (kv_pages_extend, kv_pages_free, kv_pages_fork).
+struct BooksArgs {
+    int32_t* page_table;        // [batch, max_pages]
+    int32_t* seq_len;           // [batch]
+    int32_t* ref_count;         // [num_pages]
+    int batch, max_pages, page_size, num_pages;
+    const int32_t* seqs;        // [n] extend, free
+    const int32_t* add;         // [n] extend
+    const int32_t* parents;     // [n] fork
+    const int32_t* children;    // [n] fork
+    int n;
+    int32_t* pair_src;          // [n] fork: last pages to copy
+    int32_t* pair_dst;
+    unsigned* err;
+};
+
+struct CompactArgs {
+    const int32_t* page_table;  // [batch, max_pages]
+    const int32_t* ref_count;   // [num_pages]
+    int32_t* table_out;         // may be page_table
+    int32_t* ref_out;           // may be ref_count
+    int batch, max_pages, num_pages;
+    int* state;                 // workspace: moves, live pages
+    int32_t* to;
+    int32_t* pair_src;
+    int32_t* pair_dst;
+    int32_t* moved_ref;
+    unsigned* err;
+};
+
+constexpr int kMaxCopyCaches = 96;      // caches per copy launch (a kernel parameter of 1.6 KB)
+struct CacheList {                      // host arrays of the caller
+    void* const* caches;
+    const size_t* page_bytes;
+    int n_caches, num_pages;
+};
+cudaError_t launch_kv_copy(const Launch& L, const CacheList& l, const int32_t* src, const int32_t* dst, int n);
+cudaError_t launch_kv_free(const Launch& L, const BooksArgs& a);
+size_t kv_books_smem(int num_pages, int n);
+cudaError_t launch_kv_extend(const Launch& L, const BooksArgs& a);
+size_t kv_fork_workspace_bytes(int n);
+cudaError_t launch_kv_fork(const Launch& L, BooksArgs a, const CacheList& l, void* workspace);
+size_t kv_compact_workspace_bytes(int num_pages);
+cudaError_t launch_kv_compact(const Launch& L, CompactArgs a, const CacheList& l, void* workspace);
+
+// Grouped-query attention of single rows over the paged cache.
+struct DecodeArgs {
+    const void* q;              // [rows, n_heads, head_dim], rows ld_q elements apart
+    int64_t ld_q;
+    const void* k_cache;
+    const void* v_cache;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* page_table;
+    int batch, max_pages, page_size, num_pages;
+    const int32_t* row_batch;
+    const int32_t* row_pos;
+    int rows, n_heads, n_kv_heads;
+    float scale_log2;
+    void* out;                  // [rows, n_heads, head_dim]
+    float* lse;                 // [rows, n_heads]
+    unsigned* err;
+};
+size_t gqa_decode_workspace_bytes(int rows, int n_heads, int n_kv_heads, int head_dim, dsa_dtype_t kv, int num_sms);
+cudaError_t launch_gqa_decode(const Launch& L, const DecodeArgs& a, dsa_dtype_t kv, int head_dim, void* workspace);
+
+// Causal grouped-query attention of packed prompts.
+struct PromptArgs {
+    const void* q;              // [total, n_heads, head_dim], rows ld_q / ld_k / ld_v elements apart
+    const void* k;              // [total, n_kv_heads, head_dim]
+    const void* v;
+    int64_t ld_q, ld_k, ld_v;
+    const int32_t* cu_seqlens;  // [n_seqs + 1]
+    int n_seqs, total, n_heads, n_kv_heads;
+    float scale_log2;
+    void* out;                  // [total, n_heads, head_dim]
+    float* lse;                 // [total, n_heads]
+    unsigned* err;
+};
+size_t gqa_prompt_workspace_bytes(int total, int n_seqs, dsa_dtype_t dtype);
+cudaError_t launch_gqa_prompt_simt(const Launch& L, const PromptArgs& a, dsa_dtype_t dtype, int head_dim);
 }  // namespace dsa

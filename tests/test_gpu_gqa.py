@@ -1,0 +1,428 @@
+"""Grouped-query attention over whole prompts and over the paged cache, and
+the cache's writer, on the GPU through the public binding, against plain
+64-bit forms (bounds: see gqa_reference)."""
+import math
+
+import pytest
+import torch
+
+from gqa_reference import U, attend, check, e4m3_rows
+
+dsa = pytest.importorskip("sparse_attention_logits_b200")
+
+pytestmark = pytest.mark.gpu
+
+NAN = float("nan")
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _randn(shape, g, dtype=torch.float32):
+    return torch.randn(shape, generator=g, device="cuda").to(dtype)
+
+
+# ------------------------------------------------------------------ prompt --
+
+# (prompt lengths, rows before the first prompt, rows behind the last, heads, kv heads, dim, dtype)
+PROMPTS = {
+    "one_token": ([1], 0, 0, 4, 4, 128, "bf16"),
+    "one_token_d64": ([1], 0, 0, 2, 1, 64, "bf16"),
+    "tile_edges": ([127, 128, 129, 1, 64], 0, 0, 8, 2, 128, "bf16"),
+    "tile_edges_d64": ([255, 256, 257, 63, 65], 0, 0, 4, 2, 64, "bf16"),
+    "empty_prompts": ([0, 0, 5, 0, 130, 0], 0, 0, 4, 2, 128, "bf16"),
+    "rows_around": ([33, 70, 200], 19, 45, 4, 2, 128, "bf16"),
+    "odd_group_of_3": ([300, 141, 17], 0, 0, 6, 2, 128, "bf16"),
+    "mha_odd_heads": ([300, 141, 17], 0, 3, 3, 3, 128, "bf16"),
+    "mqa_one_kv_head": ([500, 20], 0, 0, 16, 1, 64, "bf16"),
+    "group_of_5_d64": ([400, 90], 5, 0, 5, 1, 64, "bf16"),
+    "one_long": ([2049], 0, 0, 4, 1, 128, "bf16"),
+    "long_and_short": ([1500, 3, 900, 1, 1, 1], 0, 0, 4, 2, 64, "bf16"),
+    "many_short": ([(7 * i) % 23 for i in range(150)], 0, 0, 2, 2, 128, "bf16"),
+    "fp32": ([1, 63, 64, 65, 0, 300], 2, 3, 6, 2, 64, "fp32"),
+    "fp32_d128": ([200, 31], 0, 0, 4, 4, 128, "fp32"),
+}
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+def _prompt_inputs(case, seed=3):
+    lens, before, behind, H, Hkv, D, dt = PROMPTS[case]
+    total = before + sum(lens) + behind
+    g = _gen(seed)
+    # views of one fused projection's rows
+    qkv = _randn((total, H + 2 * Hkv, D), g, DT[dt])
+    cu = [before]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    # rows outside the prompts hold NaN: none may reach a prompt
+    qkv[:before] = NAN
+    qkv[cu[-1]:] = NAN
+    return qkv[:, :H], qkv[:, H:H + Hkv], qkv[:, H + Hkv:], cu
+
+
+def _prompt_check(out, lse, q, k, v, cu, scale, a, b):
+    n = b - a
+    mask = torch.ones(n, n, dtype=torch.bool, device="cuda").tril()
+    ref, ref_lse, A, d = attend(q[a:b].transpose(0, 1), k[a:b].transpose(0, 1), v[a:b].transpose(0, 1), scale, mask)
+    check(out[a:b].transpose(0, 1), lse[a:b].transpose(0, 1), ref, ref_lse, A, d, n, U[out.dtype])
+
+
+@pytest.mark.parametrize("case", list(PROMPTS))
+def test_prompt_attention(cuda_device, case):
+    q, k, v, cu = _prompt_inputs(case)
+    T, H, D = q.shape
+    scale = 1.0 / math.sqrt(D)
+    out = torch.full((T, H, D), 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full((T, H), 7.0, device="cuda")
+    dsa.gqa_prompt_attention(q, k, v, torch.tensor(cu, dtype=torch.int32, device="cuda"), scale, out=out, lse=lse)
+    assert dsa.get_device_error(cuda_device) == dsa.DSA_OK
+    for a, b in zip(cu, cu[1:]):
+        if b > a:
+            _prompt_check(out, lse, q, k, v, cu, scale, a, b)
+    # rows outside every prompt are left as they were
+    for part in (slice(0, cu[0]), slice(cu[-1], T)):
+        assert bool((out[part] == 7).all()) and bool((lse[part] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_prompt_large_and_peaked_scores(cuda_device, dtype):
+    """Scores of a few hundred, falling and rising along the keys: the running maximum moves all the time."""
+    g = _gen(5)
+    n, D = 700, 128
+    q, k, v = (_randn((n, 2, D), g, DT[dtype]) for _ in range(3))
+    k *= torch.linspace(0.1, 6.0, n, device="cuda")[:, None, None].to(DT[dtype])
+    q[::3] *= -3
+    out, lse = dsa.gqa_prompt_attention(q, k, v, torch.tensor([0, n], dtype=torch.int32, device="cuda"), 0.3)
+    _prompt_check(out, lse, q, k, v, [0, n], 0.3, 0, n)
+
+
+def test_prompt_bad_bounds_are_reported_and_skipped(cuda_device):
+    g = _gen(6)
+    q, k, v = (_randn((200, 2, 128), g, torch.bfloat16) for _ in range(3))
+    for bounds in ([0, 100, 60, 200], [0, 100, 300], [-5, 100]):
+        out = torch.zeros_like(q)
+        lse = torch.zeros(200, 2, device="cuda")
+        dsa.gqa_prompt_attention(q, k, v, torch.tensor(bounds, dtype=torch.int32, device="cuda"), 0.1, out=out, lse=lse)
+        with pytest.raises(dsa.DSAError) as e:
+            dsa.get_device_error(cuda_device)
+        assert e.value.status == dsa.DSA_ERR_INVALID_ARG
+        if bounds[0] == 0:
+            _prompt_check(out, lse, q, k, v, bounds, 0.1, 0, 100 if bounds[2] != 60 else 60)
+    assert dsa.get_device_error(cuda_device) == dsa.DSA_OK
+
+
+# ------------------------------------------------------------------ decode --
+
+class Paged:
+    """A paged cache with every place that no sequence uses set to NaN."""
+
+    def __init__(self, lens, hkv, D, page, kind, seed, spare=3):
+        g = _gen(seed)
+        self.page, self.kind = page, kind
+        per = [-(-n // page) for n in lens]
+        pages = sum(per) + spare
+        width = max(max(per), 1) + 1
+        ids = torch.randperm(pages, generator=g, device="cuda").tolist()
+        table = torch.full((len(lens), width), -1, dtype=torch.int32)
+        used = torch.zeros(pages, page, dtype=torch.bool)
+        for b, n in enumerate(lens):
+            for j in range(per[b]):
+                table[b, j] = ids.pop()
+                used[table[b, j], :min(page, n - j * page)] = True
+        self.table = table.cuda()
+        used = used.cuda()[:, None, :, None].expand(pages, hkv, page, D)
+        out = []
+        for _ in range(2):
+            x = _randn((pages, hkv, page, D), g)
+            if kind == "fp8":
+                codes, scale = e4m3_rows(x * (0.05 + 4 * torch.rand((pages, hkv, page, 1), generator=g, device="cuda")))
+                codes.view(torch.uint8).masked_fill_(~used, 0x7F)
+                scale.masked_fill_(~used[..., 0], NAN)
+                out += [codes, scale, codes.double() * scale.double()[..., None]]
+            else:
+                x = x.to(DT[kind]).masked_fill_(~used, NAN)
+                out += [x, None, x.double()]
+        self.k, self.k_scale, self.k64, self.v, self.v_scale, self.v64 = out
+
+    def rows64(self, which, b, n):
+        x = which[self.table[b, :-(-n // self.page)].long()]          # [pages, hkv, page, D]
+        return x.transpose(0, 1).flatten(1, 2)[:, :n]
+
+
+# (sequence lengths, rows per sequence, heads, kv heads, dim, page, cache)
+DECODES = {
+    "one_key": ([1], 1, 4, 1, 128, 16, "bf16"),
+    "lengths_at_the_tile": ([63, 64, 65, 127, 128, 129], 1, 8, 2, 128, 64, "bf16"),
+    "page_of_1": ([5, 40, 77], 1, 4, 2, 64, 1, "bf16"),
+    "page_of_7": ([5, 40, 300], 1, 6, 2, 128, 7, "bf16"),
+    "page_of_256": ([255, 700, 3], 1, 4, 4, 64, 256, "bf16"),
+    "mha": ([100, 3, 1000], 1, 3, 3, 128, 16, "bf16"),
+    "group_16": ([900, 33], 1, 32, 2, 128, 32, "bf16"),
+    "group_17": ([500, 65], 1, 17, 1, 64, 32, "bf16"),
+    "group_40": ([600, 5], 1, 40, 1, 128, 32, "bf16"),
+    "group_5_rows_3": ([37, 2, 200], 3, 10, 2, 64, 16, "bf16"),
+    "one_long_row": ([20011], 1, 8, 1, 128, 64, "bf16"),
+    "many_rows": ([1 + (37 * i) % 190 for i in range(300)], 1, 8, 2, 64, 16, "bf16"),
+    "ragged": ([4000, 1, 17, 2500, 600], 1, 16, 4, 128, 64, "bf16"),
+    "fp8": ([63, 64, 65, 1, 1000], 1, 8, 2, 128, 64, "fp8"),
+    "fp8_d64_odd_pages": ([400, 7, 33], 2, 6, 2, 64, 11, "fp8"),
+    "fp8_group_17": ([500, 65], 1, 17, 1, 128, 16, "fp8"),
+    "fp8_group_12": ([3000, 65], 1, 24, 2, 64, 16, "fp8"),
+    "fp8_long": ([9001, 12], 1, 16, 2, 128, 64, "fp8"),
+    "fp32": ([63, 64, 65, 1, 1000], 1, 8, 2, 128, 64, "fp32"),
+    "fp32_d64_odd_pages": ([400, 7, 33], 2, 15, 3, 64, 5, "fp32"),
+    "fp32_group_9": ([500, 65], 1, 9, 1, 128, 16, "fp32"),
+}
+U_P = {"bf16": U[torch.bfloat16], "fp8": U[torch.float16] + 2.0 ** -20, "fp32": U[torch.float32]}
+
+
+def _decode_check(c, q, out, lse, batch, pos, scale):
+    for r, (b, p) in enumerate(zip(batch, pos)):
+        if p < 0:
+            assert bool((out[r] == 0).all()) and bool(torch.isneginf(lse[r]).all())
+            continue
+        n = p + 1
+        ref, ref_lse, A, d = attend(q[r][:, None], c.rows64(c.k64, b, n), c.rows64(c.v64, b, n), scale,
+                                    torch.ones(1, n, dtype=torch.bool, device="cuda"))
+        check(out[r][:, None], lse[r][:, None], ref, ref_lse, A, d, n, U_P[c.kind])
+
+
+def _decode_case(case, seed=11):
+    lens, per, H, Hkv, D, page, kind = DECODES[case]
+    c = Paged(lens, Hkv, D, page, kind, seed)
+    batch = [b for b in range(len(lens)) for _ in range(per)]
+    pos = [max(-1, n - per + i) for n in lens for i in range(per)]
+    g = _gen(seed + 1)
+    fused = _randn((len(pos), H + 3, D), g, torch.float32 if kind == "fp32" else torch.bfloat16)
+    return c, fused[:, 1:H + 1], batch, pos, 1.0 / math.sqrt(D)
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("case", list(DECODES))
+def test_decode_attention(cuda_device, case):
+    c, q, batch, pos, scale = _decode_case(case)
+    out, lse = dsa.gqa_decode_attention(q, c.k, c.v, c.table, _i32(batch), _i32(pos), scale, c.k_scale, c.v_scale)
+    assert dsa.get_device_error(cuda_device) == dsa.DSA_OK
+    _decode_check(c, q, out, lse, batch, pos, scale)
+    # the same call again gives the same bits (blocks' order does not matter)
+    again = dsa.gqa_decode_attention(q, c.k, c.v, c.table, _i32(batch), _i32(pos), scale, c.k_scale, c.v_scale)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp32"])
+def test_decode_empty_rows_and_shuffled_batch(cuda_device, kind):
+    """Padding rows anywhere, rows in any order of the sequences, one sequence twice."""
+    lens = [130, 5, 900, 64]
+    c = Paged(lens, 2, 128, 16, kind, 21)
+    batch, pos = [2, 0, 0, 3, 1, 2, 0], [899, -1, 129, 63, 4, 500, -1]
+    q = _randn((7, 6, 128), _gen(22), torch.float32 if kind == "fp32" else torch.bfloat16)
+    out, lse = dsa.gqa_decode_attention(q, c.k, c.v, c.table, _i32(batch), _i32(pos), 0.2, c.k_scale, c.v_scale)
+    assert dsa.get_device_error(cuda_device) == dsa.DSA_OK
+    _decode_check(c, q, out, lse, batch, pos, 0.2)
+    # all rows empty
+    out, lse = dsa.gqa_decode_attention(q, c.k, c.v, c.table, _i32(batch), _i32([-1] * 7), 0.2, c.k_scale, c.v_scale)
+    _decode_check(c, q, out, lse, batch, [-1] * 7, 0.2)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp32"])
+def test_decode_large_scores(cuda_device, kind):
+    """Scores of a few hundred that grow along the sequence: every slice moves the maximum."""
+    c = Paged([3000], 1, 128, 64, kind, 31)
+    q = 4 * _randn((1, 8, 128), _gen(32), torch.float32 if kind == "fp32" else torch.bfloat16)
+    if kind == "fp8":
+        c.k_scale *= torch.linspace(0.2, 3, c.k_scale.numel(), device="cuda").reshape(c.k_scale.shape)
+        c.k64 = c.k.double() * c.k_scale.double()[..., None]
+    out, lse = dsa.gqa_decode_attention(q, c.k, c.v, c.table, _i32([0]), _i32([2999]), 1.0, c.k_scale, c.v_scale)
+    _decode_check(c, q, out, lse, [0], [2999], 1.0)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp32"])
+def test_decode_bad_indexes_are_reported(cuda_device, kind):
+    lens = [200, 100]
+    c = Paged(lens, 2, 64, 16, kind, 41)
+    q = _randn((3, 4, 64), _gen(42), torch.float32 if kind == "fp32" else torch.bfloat16)
+
+    def run(batch, pos, table=c.table):
+        out, lse = dsa.gqa_decode_attention(q, c.k, c.v, table, _i32(batch), _i32(pos), 0.1, c.k_scale, c.v_scale)
+        with pytest.raises(dsa.DSAError) as e:
+            dsa.get_device_error(cuda_device)
+        assert e.value.status == dsa.DSA_ERR_INVALID_ARG
+        return out, lse
+    # a sequence out of range: as an empty row; the others stand
+    out, lse = run([0, 7, 1], [199, 5, 99])
+    _decode_check(c, q, out, lse, [0, 0, 1], [199, -1, 99], 0.1)
+    out, lse = run([0, -1, 1], [199, 5, 99])
+    _decode_check(c, q, out, lse, [0, 0, 1], [199, -1, 99], 0.1)
+    # a position past the table's width, and a page out of range: left out
+    for table, batch, pos in ((c.table, [0, 1, 1], [199, 10 ** 6, 99]), (c.table.clone(), [0, 1, 1], [199, 50, 99])):
+        if pos[1] == 50:
+            table[0, 3] = 10 ** 6
+        out, lse = run(batch, pos, table)
+        assert bool(torch.isfinite(lse[::2]).all())         # (row 1 of the first names places that hold NaN)
+        _decode_check(c, q[2:], out[2:], lse[2:], [1], [99], 0.1)
+    assert dsa.get_device_error(cuda_device) == dsa.DSA_OK
+
+
+def test_decode_side_stream_and_caller_buffers(cuda_device):
+    c, q, batch, pos, scale = _decode_case("ragged")
+    b, p = _i32(batch), _i32(pos)
+    ref = dsa.gqa_decode_attention(q, c.k, c.v, c.table, b, p, scale)
+    need = dsa.gqa_decode_attention_workspace_size(q.shape[0], q.shape[1], c.k.shape[1], q.shape[2], c.k.dtype)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")     # NaN everywhere: nothing of it is read first
+    out, lse = torch.empty_like(ref[0]), torch.empty_like(ref[1])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        dsa.gqa_decode_attention(q, c.k, c.v, c.table, b, p, scale, out=out, lse=lse, workspace=ws)
+    s.synchronize()
+    assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+
+
+def test_captured_decode_follows_growing_lengths(cuda_device):
+    """One captured step (append, then attention) replayed while its position and input buffers change; a second
+    graph that shares the workspace runs in between."""
+    c = Paged([400, 400], 2, 128, 16, "bf16", 51)
+    c.k[:] = _randn(c.k.shape, _gen(52), torch.bfloat16)
+    c.v[:] = _randn(c.v.shape, _gen(53), torch.bfloat16)
+    g = _gen(54)
+    b, p = _i32([0, 1]), _i32([10, 10])
+    qkv = _randn((2, 8 + 4, 128), g, torch.bfloat16)
+    q, k, v = qkv[:, :8], qkv[:, 8:10], qkv[:, 10:]
+    need = dsa.gqa_decode_attention_workspace_size(2, 8, 2, 128, torch.bfloat16)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    outs = [(torch.empty(2, 8, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(2, 8, device="cuda")) for _ in "ab"]
+
+    def step(o):
+        dsa.kv_cache_append(k, v, b, p, c.table, c.k, c.v)
+        dsa.gqa_decode_attention(q, c.k, c.v, c.table, b, p, 0.1, out=o[0], lse=o[1], workspace=ws)
+    graphs = []
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(outs[0])
+    torch.cuda.current_stream().wait_stream(side)
+    for o in outs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step(o)
+        graphs.append(graph)
+    for i, at in enumerate((11, 250, 12, 399, 64)):
+        p.copy_(_i32([at, max(0, at - 5)]))
+        qkv.copy_(_randn(qkv.shape, g, torch.bfloat16))
+        graphs[i % 2].replay()
+        torch.cuda.synchronize()
+        c.k64, c.v64 = c.k.double(), c.v.double()
+        pos = p.tolist()
+        for r in range(2):
+            assert torch.equal(c.rows64(c.k64, r, pos[r] + 1)[:, -1], k[r].double())
+        _decode_check(c, q, *outs[i % 2], [0, 1], pos, 0.1)
+    assert dsa.get_device_error(cuda_device) == dsa.DSA_OK
+
+
+# ------------------------------------------------------------------ append --
+
+@pytest.mark.parametrize("kind,src,D,page,hkv", [
+    ("bf16", "bf16", 128, 64, 8), ("bf16", "fp32", 64, 16, 3), ("fp32", "fp32", 128, 7, 2), ("fp32", "fp32", 64, 1, 1),
+    ("fp8", "bf16", 128, 64, 4), ("fp8", "fp32", 64, 5, 3), ("fp8", "bf16", 64, 16, 1)])
+@pytest.mark.parametrize("n", [1, 2, 67, 1500])
+def test_append(cuda_device, kind, src, D, page, hkv, n):
+    """Rows land whole in their places, rounded once by the cache's rule, and nothing else changes."""
+    g = _gen(61)
+    B, width = 5, -(-400 // page)
+    pages = B * width + 3
+    table = torch.randperm(pages, generator=g, device="cuda")[:B * width].reshape(B, width).to(torch.int32)
+    where = torch.randperm(B * 400, generator=g, device="cuda")[:n]
+    batch, pos = (where // 400).to(torch.int32), (where % 400).to(torch.int32)
+    if n > 2:
+        pos[1] = -1                                                    # not stored
+    x = _randn((n, 2 + 2 * hkv, D), g, DT[src])
+    if n > 2:
+        x[2] = 0                                                       # all-zero rows: scale 1
+        x[3] *= 1e-3
+        x[4, :, 5] = 300
+    k, v = x[:, 1:1 + hkv], x[:, 1 + hkv:1 + 2 * hkv]
+    dt = {"fp8": torch.float8_e4m3fn, **DT}[kind]
+    before = [torch.randint(0, 120, (pages, hkv, page, D * dt.itemsize), generator=g, device="cuda").to(torch.uint8).view(dt)
+              for _ in "kv"]
+    scales = [torch.rand((pages, hkv, page), generator=g, device="cuda") for _ in "kv"] if kind == "fp8" else [None, None]
+    caches, sc = [t.clone() for t in before], [None if t is None else t.clone() for t in scales]
+    dsa.kv_cache_append(k, v, batch, pos, table, caches[0], caches[1], sc[0], sc[1])
+    assert dsa.get_device_error(cuda_device) == dsa.DSA_OK
+    keep = pos >= 0
+    pg = table[batch[keep].long(), (pos[keep] // page).long()].long()
+    sl = (pos[keep] % page).long()
+    for new, old, s_new, s_old, rows in zip(caches, before, sc, scales, (k, v)):
+        rows = rows[keep]
+        if kind == "fp8":
+            codes, s = e4m3_rows(rows.float())
+            s_old[pg, :, sl] = s
+            assert torch.equal(s_new, s_old)
+            old.view(torch.uint8)[pg, :, sl] = codes.view(torch.uint8)
+        else:
+            old[pg, :, sl] = rows.to(dt)
+        assert torch.equal(new.view(torch.uint8), old.view(torch.uint8))
+
+
+def test_append_bad_indexes_are_reported_and_skipped(cuda_device):
+    k_cache = torch.zeros(4, 1, 16, 64, dtype=torch.bfloat16, device="cuda")
+    v_cache = torch.zeros_like(k_cache)
+    table = _i32([[0, 1], [9, -1]])
+    x = torch.ones(5, 1, 64, dtype=torch.bfloat16, device="cuda")
+    # good; page out of range; no page; past the table; no such sequence
+    dsa.kv_cache_append(x, x, _i32([0, 1, 1, 0, 2]), _i32([17, 3, 20, 32, 0]), table, k_cache, v_cache)
+    with pytest.raises(dsa.DSAError):
+        dsa.get_device_error(cuda_device)
+    assert bool((k_cache[1, 0, 1] == 1).all()) and float(k_cache.sum()) == 64 and float(v_cache.sum()) == 64
+
+
+# ---------------------------------------------------------------- together --
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_prompt_then_decode_over_the_cache(cuda_device, kind):
+    """A serving run: room for two prompts, their keys and values stored, the prompts' attention; then one token at a
+    time.  The cache's attention at the prompts' rows agrees with the prompts' own, and each new token with the
+    64-bit form over all tokens so far; a branch and its parent go on apart; drawing the pool together changes nothing."""
+    dt, D, H, Hkv, page, g = DT[kind], 64, 6, 2, 16, _gen(71)
+    lens, B, width, pages = [37, 90], 3, 10, 40
+    table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+    length, count = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(pages, dtype=torch.int32, device="cuda")
+    k_cache = torch.full((pages, Hkv, page, D), NAN, dtype=dt, device="cuda")
+    v_cache = torch.full_like(k_cache, NAN)
+    u, scale = U[dt], 0.2
+    count[:5] = 1                                                       # pages held by someone else
+    dsa.kv_pages_extend(table, length, count, _i32([0, 2]), _i32(lens), page)
+    total = sum(lens)
+    qkv = _randn((total, H + 2 * Hkv, D), g, dt)
+    q, k, v = qkv[:, :H], qkv[:, H:H + Hkv], qkv[:, H + Hkv:]
+    batch = _i32([0] * lens[0] + [2] * lens[1])
+    pos = torch.cat([torch.arange(n, device="cuda", dtype=torch.int32) for n in lens])
+    dsa.kv_cache_append(k, v, batch, pos, table, k_cache, v_cache)
+    out, lse = dsa.gqa_prompt_attention(q, k, v, _i32([0, lens[0], total]), scale)
+    out2, lse2 = dsa.gqa_decode_attention(q, k_cache, v_cache, table, batch, pos, scale)
+    for a, b in ((0, lens[0]), (lens[0], total)):
+        _prompt_check(out, lse, q, k, v, None, scale, a, b)
+        _prompt_check(out2, lse2, q, k, v, None, scale, a, b)
+    # sequence 1 branches off sequence 2; then all three take new tokens
+    dsa.kv_pages_fork(table, length, count, _i32([2]), _i32([1]), page, [k_cache, v_cache])
+    story = {0: (k[:lens[0]], v[:lens[0]]), 1: (k[lens[0]:], v[lens[0]:]), 2: (k[lens[0]:], v[lens[0]:])}
+    rows = _i32([0, 1, 2])
+    for step in range(20):
+        if step == 10:
+            dsa.kv_pages_compact(table, count, [k_cache, v_cache], table_out=table, ref_out=count)
+            assert int((count > 0).sum()) == int((count[:int((count > 0).sum())] > 0).sum())
+        dsa.kv_pages_extend(table, length, count, rows, _i32([1, 1, 1]), page)
+        new = _randn((3, H + 2 * Hkv, D), g, dt)
+        dsa.kv_cache_append(new[:, H:H + Hkv], new[:, H + Hkv:], rows, length - 1, table, k_cache, v_cache)
+        o, l = dsa.gqa_decode_attention(new[:, :H], k_cache, v_cache, table, rows, length - 1, scale)
+        for b in range(3):
+            story[b] = (torch.cat([story[b][0], new[b:b + 1, H:H + Hkv]]), torch.cat([story[b][1], new[b:b + 1, H + Hkv:]]))
+            n = story[b][0].shape[0]
+            ref, ref_lse, A, d = attend(new[b, :H][:, None], story[b][0].transpose(0, 1), story[b][1].transpose(0, 1), scale,
+                                        torch.ones(1, n, dtype=torch.bool, device="cuda"))
+            check(o[b][:, None], l[b][:, None], ref, ref_lse, A, d, n, u)
+    assert dsa.get_device_error(cuda_device) == dsa.DSA_OK
+    assert length.tolist() == [57, 110, 110]
