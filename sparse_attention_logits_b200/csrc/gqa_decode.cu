@@ -147,54 +147,26 @@ __device__ __forceinline__ int cache_row(const DecodeArgs& a, const Walk& w, int
 
 // ------------------------------------------------------------ CUDA cores --
 //
-// fp32 caches (and any type, in fp32 arithmetic).  A warp takes 4 keys at a
+// fp32 caches.  A warp takes 4 keys at a
 // time for 8 heads: every lane holds D/32 dims of the queries, keys and
 // outputs, the 32 partial dot products per lane are summed over the lanes by
 // one transposing butterfly (31 shuffles for 32 sums), after which lane l
 // holds the score of key l / 8 and head l % 8.
-template <typename T, int VEC> __device__ __forceinline__ void load_vec(const T* p, float (&x)[VEC]);
-template <> __device__ __forceinline__ void load_vec<float, 4>(const float* p, float (&x)[4]) {
+template <int VEC> __device__ __forceinline__ void load_vec(const float* p, float (&x)[VEC]);
+template <> __device__ __forceinline__ void load_vec<4>(const float* p, float (&x)[4]) {
     const float4 v = __ldg((const float4*)p);
     x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
 }
-template <> __device__ __forceinline__ void load_vec<float, 2>(const float* p, float (&x)[2]) {
+template <> __device__ __forceinline__ void load_vec<2>(const float* p, float (&x)[2]) {
     const float2 v = __ldg((const float2*)p);
     x[0] = v.x; x[1] = v.y;
 }
-template <> __device__ __forceinline__ void load_vec<__nv_bfloat16, 4>(const __nv_bfloat16* p, float (&x)[4]) {
-    const uint2 v = __ldg((const uint2*)p);
-    x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xFFFF0000u);
-    x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xFFFF0000u);
-}
-template <> __device__ __forceinline__ void load_vec<__nv_bfloat16, 2>(const __nv_bfloat16* p, float (&x)[2]) {
-    const uint32_t v = __ldg((const uint32_t*)p);
-    x[0] = __uint_as_float(v << 16); x[1] = __uint_as_float(v & 0xFFFF0000u);
-}
-template <> __device__ __forceinline__ void load_vec<__nv_fp8_e4m3, 4>(const __nv_fp8_e4m3* p, float (&x)[4]) {
-    const uint32_t v = __ldg((const uint32_t*)p);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        __nv_fp8_e4m3 c;
-        c.__x = (__nv_fp8_storage_t)(v >> (8 * e));
-        x[e] = (float)c;
-    }
-}
-template <> __device__ __forceinline__ void load_vec<__nv_fp8_e4m3, 2>(const __nv_fp8_e4m3* p, float (&x)[2]) {
-    const uint16_t v = __ldg((const uint16_t*)p);
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        __nv_fp8_e4m3 c;
-        c.__x = (__nv_fp8_storage_t)(v >> (8 * e));
-        x[e] = (float)c;
-    }
-}
 
-template <typename Q, typename KV, int D>
+template <int D>
 __global__ void __launch_bounds__(THREADS) gqa_decode_simt_kernel(const DecodeArgs a, const Parts parts) {
     pdl_wait();
     pdl_launch_dependents();
     constexpr int GT = 8, VEC = D / 32;
-    constexpr bool SCALED = sizeof(KV) == 1;
     __shared__ LocateShared sh;
     __shared__ float s_o[WARPS][GT][D];
     __shared__ float s_m[WARPS][GT], s_l[WARPS][GT];
@@ -203,8 +175,8 @@ __global__ void __launch_bounds__(THREADS) gqa_decode_simt_kernel(const DecodeAr
     Walk w;
     int64_t begin, end, stretch;
     locate(a, hvs, 2, sh, w, begin, end, stretch);
-    const KV* kc = (const KV*)a.k_cache;
-    const KV* vc = (const KV*)a.v_cache;
+    const float* kc = (const float*)a.k_cache;
+    const float* vc = (const float*)a.v_cache;
     for (int64_t at = begin; at < end;) {
         const int kvh = w.hv / tiles, h0 = kvh * group + (w.hv - kvh * tiles) * GT;
         const int heads = min(GT, (kvh + 1) * group - h0);
@@ -220,9 +192,7 @@ __global__ void __launch_bounds__(THREADS) gqa_decode_simt_kernel(const DecodeAr
         for (int h = 0; h < GT; ++h) {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                q[h][v] = h < heads ? to_f32(((const Q*)a.q)[(int64_t)w.row * a.ld_q + (h0 + h) * D + lane * VEC + v]) *
-                                          a.scale_log2
-                                    : 0.f;
+                q[h][v] = h < heads ? ((const float*)a.q)[(int64_t)w.row * a.ld_q + (h0 + h) * D + lane * VEC + v] * a.scale_log2 : 0.f;
                 acc[h][v] = 0.f;
             }
         }
@@ -238,8 +208,8 @@ __global__ void __launch_bounds__(THREADS) gqa_decode_simt_kernel(const DecodeAr
                 for (int k = 0; k < 4; ++k) {
                     row[k] = __shfl_sync(0xffffffffu, my_row, k0 + k);
                     if (row[k] >= 0) {
-                        load_vec<KV, VEC>(kc + (int64_t)row[k] * D + lane * VEC, kx[k]);
-                        load_vec<KV, VEC>(vc + (int64_t)row[k] * D + lane * VEC, vx[k]);
+                        load_vec<VEC>(kc + (int64_t)row[k] * D + lane * VEC, kx[k]);
+                        load_vec<VEC>(vc + (int64_t)row[k] * D + lane * VEC, vx[k]);
                     } else {
 #pragma unroll
                         for (int v = 0; v < VEC; ++v) kx[k][v] = vx[k][v] = 0.f;
@@ -248,11 +218,6 @@ __global__ void __launch_bounds__(THREADS) gqa_decode_simt_kernel(const DecodeAr
                 if (row[0] < 0 && row[1] < 0 && row[2] < 0 && row[3] < 0) continue;
                 const int mine = lane >> 3;
                 const int mrow = mine == 0 ? row[0] : mine == 1 ? row[1] : mine == 2 ? row[2] : row[3];
-                float ks = 1.f, vs = 1.f;
-                if (SCALED && mrow >= 0) {
-                    ks = __ldg(a.k_scale + mrow);
-                    vs = __ldg(a.v_scale + mrow);
-                }
                 float s[32];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -273,7 +238,7 @@ __global__ void __launch_bounds__(THREADS) gqa_decode_simt_kernel(const DecodeAr
                         s[i] = keep + __shfl_xor_sync(0xffffffffu, give, half);
                     }
                 }
-                const float z = mrow >= 0 ? s[0] * ks : -INFINITY;
+                const float z = mrow >= 0 ? s[0] : -INFINITY;
                 float top = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 8));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
                 const float m_new = fmaxf(m, top);
@@ -290,12 +255,11 @@ __global__ void __launch_bounds__(THREADS) gqa_decode_simt_kernel(const DecodeAr
                 }
                 const float p = mrow >= 0 && m > -INFINITY ? fast_exp2(z - m) : 0.f;
                 l += p;
-                const float pv = SCALED ? p * vs : p;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
                     for (int h = 0; h < GT; ++h) {
-                        const float ph = __shfl_sync(0xffffffffu, pv, k * GT + h);
+                        const float ph = __shfl_sync(0xffffffffu, p, k * GT + h);
 #pragma unroll
                         for (int v = 0; v < VEC; ++v) acc[h][v] = fmaf(ph, vx[k][v], acc[h][v]);
                     }
@@ -331,9 +295,9 @@ __global__ void __launch_bounds__(THREADS) gqa_decode_simt_kernel(const DecodeAr
             }
             if (begins && ends) {
                 const float inv = ll == 0.f ? 0.f : 1.f / ll;
-                Q* out = (Q*)a.out + ((int64_t)w.row * a.n_heads + h0 + h) * D + lane * VEC;
+                float* out = (float*)a.out + ((int64_t)w.row * a.n_heads + h0 + h) * D + lane * VEC;
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) store_out(out + v, o[v] * inv);
+                for (int v = 0; v < VEC; ++v) out[v] = o[v] * inv;
                 if (lane == 0)
                     a.lse[(int64_t)w.row * a.n_heads + h0 + h] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * LN2;
             } else {
@@ -352,6 +316,417 @@ __global__ void __launch_bounds__(THREADS) gqa_decode_simt_kernel(const DecodeAr
         w.unit += n - 1;
         w.next(a, hvs);
     }
+}
+
+// ---------------------------------------------------------- tensor cores --
+//
+// bf16 and fp8 caches.  The work is bound by the cache's bytes, so the kernel
+// is built around its loads: each warp owns 16 keys of a unit and streams
+// their K and V rows through a ring of its own (cp.async, 16 bytes per lane,
+// rows of unused places zero-filled), never waiting for another warp while a
+// pair lasts.  With up to 16 heads of a group as the M of mma.m16n8k16, one
+// slice costs a warp 2 D/16 + D/8 products and one softmax step in registers:
+// about a tenth of an SM's issue slots at the HBM rate, which is why the
+// products need no more than the warp-level tensor instruction (M = 128 of
+// tcgen05 would be filled to an eighth).
+//
+// fp8: codes are widened to f16 (exact) on the way into the product.  Which 16
+// dims a k-step holds is free as long as Q and K agree, and which d a column
+// of the output holds is free altogether; both are chosen so that a lane
+// reads its keys as 16-byte (V, D = 64: 8-byte) pieces.  The query row is
+// first brought to [1, 2) by a power of two, so that f16 holds it (a value
+// below 2^-14 of the row's largest loses bits below 2^-25 of it); P is taken
+// times the value scale relative to the largest scale met so far, which the
+// output carries like the running maximum.
+template <typename KV> struct MmaCfg;
+template <> struct MmaCfg<__nv_bfloat16> { static constexpr int STAGES = 3, BLOCKS = 2; };
+template <> struct MmaCfg<__nv_fp8_e4m3> { static constexpr int STAGES = 4, BLOCKS = 3; };
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (F16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <bool F16> __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    if (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Two e4m3 codes (the low half of v) to two f16.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ void cp_async_4(void* dst, const void* src, uint32_t src_bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(src_bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Shared-memory place of 16-byte piece c of key r, within a slice of 16 rows
+// of RB bytes (swizzled so that the reads below meet no bank twice).
+template <bool FP8, int RB, bool IS_V> __device__ __forceinline__ uint32_t piece_at(int r, int c) {
+    if (!FP8) return r * RB + ((c ^ (r & 7)) << 4);
+    if (IS_V) {                     // lines of 128 bytes
+        const int lin = r * (RB / 16) + c;
+        return (lin >> 3) * 128 + (((lin & 7) ^ (((r >> 1) & 3) << 1)) << 4);
+    }
+    return r * RB + ((RB == 128 ? c ^ ((r & 1) << 2) : c) << 4);
+}
+
+// Place (in floats) of dim d of row r in the exchange buffer of the warps'
+// outputs: 16-byte pieces swizzled among the eight of a 128-byte line.
+template <int D> __device__ __forceinline__ int exch_at(int r, int d) {
+    const int g = d >> 2;
+    return r * D + (((g ^ (((g >> 3) & 3) | ((r & 1) << 2)))) << 2) + (d & 3);
+}
+
+template <typename KV, int D, int GT>
+__global__ void __launch_bounds__(THREADS, MmaCfg<KV>::BLOCKS) gqa_decode_mma_kernel(const DecodeArgs a, const Parts parts) {
+    pdl_wait();
+    pdl_launch_dependents();
+    constexpr bool FP8 = sizeof(KV) == 1;
+    constexpr int RB = D * (int)sizeof(KV);         // bytes of a row
+    constexpr int PIECES = RB / 16;
+    constexpr int SLICE = WK * RB;                  // K (or V) bytes of a warp's slice
+    constexpr int STAGES = MmaCfg<KV>::STAGES;
+    constexpr int SLOT = 2 * SLICE + (FP8 ? 2 * WK * 4 : 0) + 16;   // K, V, scales, the mask of valid keys
+    constexpr int KS = D / 16, NT = D / 8;
+    static_assert(2 * SLICE >= 8 * D * 4, "the outputs of 8 heads are exchanged in a slot");
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ LocateShared sh;
+    __shared__ float2 s_ml[WARPS][16];
+    const int group = a.n_heads / a.n_kv_heads, tiles = ceil_div(group, GT), hvs = a.n_kv_heads * tiles;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int r4 = lane >> 2, c4 = lane & 3;        // fragment row / column group
+    uint8_t* ring = smem + warp * STAGES * SLOT;
+    Walk w;
+    int64_t begin, end, stretch;
+    locate(a, hvs, 2, sh, w, begin, end, stretch);
+    if (begin >= end) return;
+    const uint8_t* kc = (const uint8_t*)a.k_cache;
+    const uint8_t* vc = (const uint8_t*)a.v_cache;
+
+    // the loads' walk runs STAGES units ahead of the products'; the page
+    // of a slice is looked up one unit before its rows are requested
+    Walk lw = w;
+    int64_t to_load = end - begin;
+    auto look = [&]() -> int {
+        return to_load > 0 ? cache_row(a, lw, lw.hv / tiles, lw.unit * KT + warp * WK + (lane & (WK - 1))) : -1;
+    };
+    int row = look();
+    auto request = [&](int st) {
+        if (to_load > 0) {
+            uint8_t* slot = ring + st * SLOT;
+#pragma unroll
+            for (int i = 0; i < WK * PIECES / 32; ++i) {
+                const int r = (i * 32 + lane) / PIECES, c = (i * 32 + lane) % PIECES;
+                const int from = __shfl_sync(0xffffffffu, row, r);
+                const int64_t off = from >= 0 ? (int64_t)from * RB + c * 16 : 0;
+                const uint32_t n = from >= 0 ? 16u : 0u;
+                cp_async_16(slot + piece_at<FP8, RB, false>(r, c), kc + off, n);
+                cp_async_16(slot + SLICE + piece_at<FP8, RB, true>(r, c), vc + off, n);
+            }
+            if (FP8)
+                cp_async_4(slot + 2 * SLICE + lane * 4, (lane < WK ? a.k_scale : a.v_scale) + (row >= 0 ? row : 0),
+                           row >= 0 ? 4u : 0u);
+            const uint32_t valid = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
+            if (lane == 0) *(uint32_t*)(slot + SLOT - 16) = valid;
+            lw.next(a, hvs);
+            --to_load;
+            row = look();
+        }
+        cp_async_commit();
+    };
+#pragma unroll 1
+    for (int st = 0; st < STAGES; ++st) request(st);
+
+    int st = 0;
+    for (int64_t at = begin; at < end;) {
+        const int kvh = w.hv / tiles, h0 = kvh * group + (w.hv - kvh * tiles) * GT;
+        const int heads = min(GT, (kvh + 1) * group - h0);
+        const int n = (int)min((int64_t)(w.units - w.unit), end - at);
+        if (w.unit == 0 && w.hv == 0 && tid == 0 &&
+            (w.batch < 0 || w.batch >= a.batch || __ldg(a.row_pos + w.row) >= (int64_t)a.max_pages * a.page_size))
+            record_error(a.err, DEV_ERR_BAD_INDEX);     // reported once per row, by the block that begins it
+        // Q fragments: rows r4 and r4 + 8 (heads); k-step kk holds dims
+        // 16 kk + {2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9} (bf16), or
+        // 64 (kk / 4) + 16 c4 + 4 (kk % 4) + {0, 1, 2, 3} (fp8)
+        uint32_t qf[KS][4];
+        float zs[2] = {a.scale_log2, a.scale_log2};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const bool on = (half == 0 || GT > 8) && r4 + 8 * half < heads;
+            const __nv_bfloat16* q = (const __nv_bfloat16*)a.q + (int64_t)w.row * a.ld_q +
+                                     (h0 + (on ? r4 + 8 * half : 0)) * D;
+            if (!FP8) {
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk) {
+                    qf[kk][half] = on ? __ldg((const uint32_t*)(q + 16 * kk + 2 * c4)) : 0u;
+                    qf[kk][half + 2] = on ? __ldg((const uint32_t*)(q + 16 * kk + 2 * c4 + 8)) : 0u;
+                }
+            } else {
+                uint32_t raw[KS][2];
+                float top = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk) {
+                    const uint2 x = on ? __ldg((const uint2*)(q + 64 * (kk / 4) + 16 * c4 + 4 * (kk % 4))) : make_uint2(0u, 0u);
+                    raw[kk][0] = x.x;
+                    raw[kk][1] = x.y;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(raw[kk][e] << 16)),
+                                               fabsf(__uint_as_float(raw[kk][e] & 0xFFFF0000u))));
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // 2^e <= top < 2^(e + 1), e kept where 2^-e is a normal number
+                const int e = min(max((int)(__float_as_uint(top) >> 23), 1), 253) - 127;
+                const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+                zs[half] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+                    for (int e2 = 0; e2 < 2; ++e2)
+                        qf[kk][half + 2 * e2] = pack2<true>(__uint_as_float(raw[kk][e2] << 16) * down,
+                                                            __uint_as_float(raw[kk][e2] & 0xFFFF0000u) * down);
+            }
+        }
+        float o[NT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, vref = 0.f, vinv = 0.f;
+
+        for (int u = 0; u < n; ++u) {
+            cp_async_wait<STAGES - 1>();
+            __syncwarp();
+            const uint8_t* slot = ring + st * SLOT;
+            const uint32_t kb = smem_u32(slot), vb = kb + SLICE;
+            const uint32_t valid = *(const uint32_t*)(slot + SLOT - 16);
+            if (valid) {
+                // S = Q K^T: two tiles of 8 keys; lane: rows r4 / r4 + 8, keys 8 t + 2 c4 + {0, 1}
+                float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                if (!FP8) {
+#pragma unroll
+                    for (int kk = 0; kk < KS; ++kk) {
+                        uint32_t b[4];
+                        ldmatrix_x4(b, kb + piece_at<FP8, RB, false>((lane >> 4) * 8 + (lane & 7), kk * 2 + ((lane >> 3) & 1)));
+                        mma16816<FP8>(s[0], qf[kk], b[0], b[1]);
+                        mma16816<FP8>(s[1], qf[kk], b[2], b[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const uint4 x = ld_shared_v4(slot + piece_at<FP8, RB, false>(t * 8 + r4, 4 * i + c4));
+                            const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                mma16816<FP8>(s[t], qf[4 * i + j], e4m3x2_f16x2(wd[j]), e4m3x2_f16x2(wd[j] >> 16));
+                        }
+                }
+                float2 vs2[2];
+                if (FP8) {
+                    const float* ks = (const float*)(slot + 2 * SLICE);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const float2 k2 = *(const float2*)(ks + t * 8 + 2 * c4);
+                        vs2[t] = *(const float2*)(ks + WK + t * 8 + 2 * c4);
+                        s[t][0] *= k2.x; s[t][1] *= k2.y; s[t][2] *= k2.x; s[t][3] *= k2.y;
+                    }
+                }
+                // running maximum, and the output brought to it
+                float f[2] = {1.f, 1.f};
+                bool moved = false;
+#pragma unroll
+                for (int half = 0; half < (GT > 8 ? 2 : 1); ++half) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float& z = s[t][2 * half + e];
+                            z *= zs[half];
+                            if (valid != 0xffffu && !((valid >> (t * 8 + 2 * c4 + e)) & 1u)) z = -INFINITY;
+                            top = fmaxf(top, z);
+                        }
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    if (top > m[half]) {
+                        f[half] = fast_exp2(m[half] - top);
+                        m[half] = top;
+                        l[half] *= f[half];
+                        moved = true;
+                    }
+                }
+                float vmove = 1.f;
+                if (FP8) {
+                    float top = fmaxf(fmaxf(fabsf(vs2[0].x), fabsf(vs2[0].y)), fmaxf(fabsf(vs2[1].x), fabsf(vs2[1].y)));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)), 1e-30f);   // its reciprocal is finite
+                    if (top > vref) {
+                        vmove = vref / top;
+                        vref = top;
+                        vinv = 1.f / top;
+                        moved = true;
+                    }
+                }
+                if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        o[t][0] *= f[0] * vmove; o[t][1] *= f[0] * vmove;
+                        if (GT > 8) { o[t][2] *= f[1] * vmove; o[t][3] *= f[1] * vmove; }
+                    }
+                }
+                // P, and O += P V
+                uint32_t pf[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int half = 0; half < (GT > 8 ? 2 : 1); ++half) {
+                    const float base = m[half] > -INFINITY ? m[half] : 0.f;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        float p0 = fast_exp2(s[t][2 * half] - base), p1 = fast_exp2(s[t][2 * half + 1] - base);
+                        l[half] += p0 + p1;
+                        if (FP8) {
+                            p0 *= vs2[t].x * vinv;
+                            p1 *= vs2[t].y * vinv;
+                        }
+                        pf[half + 2 * t] = pack2<FP8>(p0, p1);
+                    }
+                }
+                if (!FP8) {
+#pragma unroll
+                    for (int t = 0; t < NT; t += 2) {
+                        uint32_t b[4];
+                        ldmatrix_x4_t(b, vb + piece_at<FP8, RB, true>(((lane >> 3) & 1) * 8 + (lane & 7), t + (lane >> 4)));
+                        mma16816<FP8>(o[t], pf, b[0], b[1]);
+                        mma16816<FP8>(o[t + 1], pf, b[2], b[3]);
+                    }
+                } else {
+                    // column r4 of tile t is dim (D / 8) r4 + t; keys 2 c4 + {0, 1, 8, 9}
+                    constexpr int RUN = D / 8;
+                    uint32_t x[4][RUN / 4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int key = 2 * c4 + (k & 1) + 8 * (k >> 1);
+                        const uint8_t* src = slot + SLICE + piece_at<FP8, RB, true>(key, r4 * RUN / 16) + (r4 * RUN) % 16;
+                        if (RUN == 16) {
+                            const uint4 v = ld_shared_v4(src);
+                            x[k][0] = v.x; x[k][1] = v.y; x[k][RUN / 4 - 2] = v.z; x[k][RUN / 4 - 1] = v.w;
+                        } else {
+                            const uint2 v = *(const uint2*)src;
+                            x[k][0] = v.x; x[k][1] = v.y;
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < RUN / 4; ++j) {
+                        const uint32_t a0 = __byte_perm(x[0][j], x[1][j], 0x5140), a1 = __byte_perm(x[0][j], x[1][j], 0x7362);
+                        const uint32_t b0 = __byte_perm(x[2][j], x[3][j], 0x5140), b1 = __byte_perm(x[2][j], x[3][j], 0x7362);
+                        mma16816<FP8>(o[4 * j], pf, e4m3x2_f16x2(a0), e4m3x2_f16x2(b0));
+                        mma16816<FP8>(o[4 * j + 1], pf, e4m3x2_f16x2(a0 >> 16), e4m3x2_f16x2(b0 >> 16));
+                        mma16816<FP8>(o[4 * j + 2], pf, e4m3x2_f16x2(a1), e4m3x2_f16x2(b1));
+                        mma16816<FP8>(o[4 * j + 3], pf, e4m3x2_f16x2(a1 >> 16), e4m3x2_f16x2(b1 >> 16));
+                    }
+                }
+            }
+            __syncwarp();
+            if (u + 1 < n) {
+                request(st);
+                st = st + 1 == STAGES ? 0 : st + 1;
+            }
+        }
+        // the four warps' shares of the pair, joined through the slots whose
+        // slices were just used (their next loads are requested afterwards)
+#pragma unroll
+        for (int half = 0; half < (GT > 8 ? 2 : 1); ++half) {
+            l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
+            l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
+            if (c4 == 0) s_ml[warp][r4 + 8 * half] = make_float2(m[half], l[half]);
+        }
+        const bool begins = w.unit == 0, ends = w.unit + n == w.units;
+        const int place = 2 * blockIdx.x + (begins ? 1 : 0);
+        const float carry = FP8 ? vref : 1.f;
+        float* mine = (float*)(ring + st * SLOT);
+#pragma unroll
+        for (int half = 0; half < (GT > 8 ? 2 : 1); ++half) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (!FP8) {
+                    *(float2*)(mine + exch_at<D>(r4, 8 * t + 2 * c4)) = make_float2(o[t][2 * half], o[t][2 * half + 1]);
+                } else if ((t & 3) == 0) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        *(float4*)(mine + exch_at<D>(r4, (D / 8) * (2 * c4 + e) + t)) =
+                            make_float4(o[t][2 * half + e] * carry, o[t + 1][2 * half + e] * carry,
+                                        o[t + 2][2 * half + e] * carry, o[t + 3][2 * half + e] * carry);
+                }
+            }
+            __syncthreads();
+            constexpr int VEC = D / 32;
+            for (int r = warp; r < 8 && r + 8 * half < heads; r += WARPS) {
+                const int h = r + 8 * half;
+                float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+                for (int i = 0; i < WARPS; ++i) mm = fmaxf(mm, s_ml[i][h].x);
+                float acc[VEC];
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) acc[v] = 0.f;
+#pragma unroll
+                for (int i = 0; i < WARPS; ++i) {
+                    const float2 ml = s_ml[i][h];
+                    const float g = mm == -INFINITY ? 0.f : fast_exp2(ml.x - mm);
+                    ll += g * ml.y;
+                    const float* from = (const float*)(smem + (i * STAGES + st) * SLOT) + exch_at<D>(r, lane * VEC);
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) acc[v] = fmaf(g, from[v], acc[v]);
+                }
+                if (begins && ends) {
+                    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+                    __nv_bfloat16* out = (__nv_bfloat16*)a.out + ((int64_t)w.row * a.n_heads + h0 + h) * D + lane * VEC;
+#pragma unroll
+                    for (int v = 0; v < VEC; v += 2)
+                        *(uint32_t*)(out + v) = pack2<false>(acc[v] * inv, acc[v + 1] * inv);
+                    if (lane == 0)
+                        a.lse[(int64_t)w.row * a.n_heads + h0 + h] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * LN2;
+                } else {
+                    float* po = parts.o + ((int64_t)place * GT + h) * D + lane * VEC;
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) po[v] = acc[v];
+                    if (lane == 0) parts.ml[place * GT + h] = make_float2(mm, ll);
+                }
+            }
+            __syncthreads();
+        }
+        if (begins && tid == 0) {
+            const int64_t last = (at + w.units - 1) / stretch;      // block of the pair's last unit
+            parts.meta[(int64_t)w.row * hvs + w.hv] = make_int2(blockIdx.x, (int)(last - blockIdx.x) + 1);
+        }
+        request(st);
+        st = st + 1 == STAGES ? 0 : st + 1;
+        at += n;
+        w.unit += n - 1;
+        w.next(a, hvs);
+    }
+    cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------- joining --
@@ -397,52 +772,74 @@ __global__ void __launch_bounds__(128) gqa_combine_kernel(const DecodeArgs a, co
     if (lane == 0) a.lse[item] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
 }
 
-constexpr int BLOCKS_PER_SM = 4;
-constexpr int GT_SIMT = 8;
-
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-template <typename Q, typename KV, int D>
-cudaError_t launch_decode(const Launch& L, const DecodeArgs& a, void* workspace) {
-    constexpr int GT = GT_SIMT;
-    const int grid = L.num_sms * BLOCKS_PER_SM;
+// Heads per pair: 8 on the CUDA cores; on the tensor cores as many rows of
+// the product as the group fills (16, or 8 when the upper half would be idle).
+int head_tile(dsa_dtype_t kv, int group) { return kv == DSA_FP32 || group <= 8 ? 8 : 16; }
+int blocks_per_sm(dsa_dtype_t kv) {
+    return kv == DSA_FP32 ? 4 : kv == DSA_BF16 ? MmaCfg<__nv_bfloat16>::BLOCKS : MmaCfg<__nv_fp8_e4m3>::BLOCKS;
+}
+
+template <typename Q, int D, int GT, class Kern>
+cudaError_t launch_decode(const Launch& L, const DecodeArgs& a, Kern kern, int smem, int per_sm, void* workspace) {
+    const int grid = L.num_sms * per_sm;
     Parts p;
     p.o = (float*)workspace;
     p.ml = (float2*)((char*)workspace + up256((size_t)2 * grid * GT * D * 4));
     p.meta = (int2*)((char*)p.ml + up256((size_t)2 * grid * GT * 8));
+    cudaError_t e = cudaSuccess;
+    if (smem > 0) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1] = {pdl_attr()};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = L.stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, gqa_decode_simt_kernel<Q, KV, D>, a, p);
+    e = cudaLaunchKernelEx(&cfg, kern, a, p);
     count_launch();
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)(((int64_t)a.rows * a.n_heads + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, gqa_combine_kernel<Q, D, GT>, a, p);
     count_launch();
     return e;
 }
 
+template <typename KV, int D>
+cudaError_t launch_mma(const Launch& L, const DecodeArgs& a, void* workspace) {
+    constexpr bool FP8 = sizeof(KV) == 1;
+    constexpr int slot = 2 * WK * D * (int)sizeof(KV) + (FP8 ? 2 * WK * 4 : 0) + 16;
+    constexpr int smem = WARPS * MmaCfg<KV>::STAGES * slot, per_sm = MmaCfg<KV>::BLOCKS;
+    if (a.n_heads / a.n_kv_heads <= 8)
+        return launch_decode<__nv_bfloat16, D, 8>(L, a, gqa_decode_mma_kernel<KV, D, 8>, smem, per_sm, workspace);
+    return launch_decode<__nv_bfloat16, D, 16>(L, a, gqa_decode_mma_kernel<KV, D, 16>, smem, per_sm, workspace);
+}
+
 }  // namespace
 
 size_t gqa_decode_workspace_bytes(int rows, int n_heads, int n_kv_heads, int head_dim, dsa_dtype_t kv, int num_sms) {
-    const size_t grid = (size_t)num_sms * BLOCKS_PER_SM, gt = GT_SIMT;
-    const size_t pairs = (size_t)rows * n_kv_heads * ceil_div(n_heads / n_kv_heads, (int)gt);
+    const int group = n_heads / n_kv_heads;
+    const size_t grid = (size_t)num_sms * blocks_per_sm(kv), gt = head_tile(kv, group);
+    const size_t pairs = (size_t)rows * n_kv_heads * ceil_div(group, (int)gt);
     return up256(2 * grid * gt * head_dim * 4) + up256(2 * grid * gt * 8) + pairs * 8;
 }
 
 cudaError_t launch_gqa_decode(const Launch& L, const DecodeArgs& a, dsa_dtype_t kv, int head_dim, void* workspace) {
+    const int per_sm = blocks_per_sm(DSA_FP32);
     if (kv == DSA_FP32)
-        return head_dim == 64 ? launch_decode<float, float, 64>(L, a, workspace)
-                              : launch_decode<float, float, 128>(L, a, workspace);
+        return head_dim == 64
+                   ? launch_decode<float, 64, 8>(L, a, gqa_decode_simt_kernel<64>, 0, per_sm, workspace)
+                   : launch_decode<float, 128, 8>(L, a, gqa_decode_simt_kernel<128>, 0, per_sm, workspace);
     if (kv == DSA_BF16)
-        return head_dim == 64 ? launch_decode<__nv_bfloat16, __nv_bfloat16, 64>(L, a, workspace)
-                              : launch_decode<__nv_bfloat16, __nv_bfloat16, 128>(L, a, workspace);
-    return head_dim == 64 ? launch_decode<__nv_bfloat16, __nv_fp8_e4m3, 64>(L, a, workspace)
-                          : launch_decode<__nv_bfloat16, __nv_fp8_e4m3, 128>(L, a, workspace);
+        return head_dim == 64 ? launch_mma<__nv_bfloat16, 64>(L, a, workspace)
+                              : launch_mma<__nv_bfloat16, 128>(L, a, workspace);
+    return head_dim == 64 ? launch_mma<__nv_fp8_e4m3, 64>(L, a, workspace)
+                          : launch_mma<__nv_fp8_e4m3, 128>(L, a, workspace);
 }
 
 }  // namespace dsa
