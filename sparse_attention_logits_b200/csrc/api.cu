@@ -650,7 +650,9 @@ dsa_status_t gqa_prompt_attention(const void* q, int64_t ld_q, const void* k, in
     a.out = out;
     a.lse = lse;
     a.err = L.err;
-    return cuda_status(dsa::launch_gqa_prompt_simt(L, a, dtype, head_dim), "gqa_prompt_attention launch");
+    return cuda_status(dtype == DSA_BF16 ? dsa::launch_gqa_prompt_tc(L, a, head_dim, workspace)
+                                         : dsa::launch_gqa_prompt_simt(L, a, head_dim),
+                       "gqa_prompt_attention launch");
 }
 
 dsa_status_t kv_pages_copy(void* const* caches, const size_t* page_bytes, int n_caches, int num_pages,

@@ -63,15 +63,7 @@ __device__ __forceinline__ bool find_tile(const PromptArgs& a, int t, Tile& w, i
     return sh[3] > 0;
 }
 
-template <typename T> __device__ __forceinline__ float4 load4(const T* p);
-template <> __device__ __forceinline__ float4 load4<float>(const float* p) { return __ldg((const float4*)p); }
-template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-    const uint2 v = __ldg((const uint2*)p);
-    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
-                       __uint_as_float(v.y & 0xFFFF0000u));
-}
-
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(THREADS) gqa_prompt_simt_kernel(const PromptArgs a) {
     pdl_wait();
     pdl_launch_dependents();
@@ -88,11 +80,11 @@ __global__ void __launch_bounds__(THREADS) gqa_prompt_simt_kernel(const PromptAr
     const int head = blockIdx.x - tile * a.n_heads, kvh = head / (a.n_heads / a.n_kv_heads);
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int rows = min(BM, w.len - w.row0);
-    const T* q = (const T*)a.q + (int64_t)(w.first + w.row0) * a.ld_q + head * D;
+    const float* q = (const float*)a.q + (int64_t)(w.first + w.row0) * a.ld_q + head * D;
     for (int i = tid; i < BM * (D / 4); i += THREADS) {
         const int r = i / (D / 4), c = i % (D / 4);
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < rows) x = load4<T>(q + r * a.ld_q + c * 4);
+        if (r < rows) x = __ldg((const float4*)(q + r * a.ld_q + c * 4));
         *(float4*)(sq + r * LD + c * 4) =
             make_float4(x.x * a.scale_log2, x.y * a.scale_log2, x.z * a.scale_log2, x.w * a.scale_log2);
     }
@@ -106,16 +98,16 @@ __global__ void __launch_bounds__(THREADS) gqa_prompt_simt_kernel(const PromptAr
         for (int v = 0; v < OV; ++v) o[i][v] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     const int keys = w.row0 + rows;             // the tile's last row sees this many
-    const T* kb = (const T*)a.k + (int64_t)w.first * a.ld_k + kvh * D;
-    const T* vb = (const T*)a.v + (int64_t)w.first * a.ld_v + kvh * D;
+    const float* kb = (const float*)a.k + (int64_t)w.first * a.ld_k + kvh * D;
+    const float* vb = (const float*)a.v + (int64_t)w.first * a.ld_v + kvh * D;
     for (int k0 = 0; k0 < keys; k0 += BN) {
         __syncthreads();
         for (int i = tid; i < BN * (D / 4); i += THREADS) {
             const int r = i / (D / 4), c = i % (D / 4);
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
             if (k0 + r < keys) {
-                x = load4<T>(kb + (k0 + r) * a.ld_k + c * 4);
-                y = load4<T>(vb + (k0 + r) * a.ld_v + c * 4);
+                x = __ldg((const float4*)(kb + (k0 + r) * a.ld_k + c * 4));
+                y = __ldg((const float4*)(vb + (k0 + r) * a.ld_v + c * 4));
             }
             *(float4*)(sk + r * LD + c * 4) = x;
             *(float4*)(sv + r * D + c * 4) = y;
@@ -201,21 +193,19 @@ __global__ void __launch_bounds__(THREADS) gqa_prompt_simt_kernel(const PromptAr
         if (r >= rows) continue;
         const int64_t row = w.first + w.row0 + r;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        T* out = (T*)a.out + (row * a.n_heads + head) * D;
+        float* out = (float*)a.out + (row * a.n_heads + head) * D;
 #pragma unroll
-        for (int v = 0; v < OV; ++v) {
-            const float x[4] = {o[i][v].x, o[i][v].y, o[i][v].z, o[i][v].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) store_out(out + v * 64 + tx * 4 + e, x[e] * inv);
-        }
+        for (int v = 0; v < OV; ++v)
+            *(float4*)(out + v * 64 + tx * 4) =
+                make_float4(o[i][v].x * inv, o[i][v].y * inv, o[i][v].z * inv, o[i][v].w * inv);
         if (tx == 0) a.lse[row * a.n_heads + head] = sum == 0.f ? -INFINITY : (m[i] + log2f(sum)) * LN2;
     }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch(const Launch& L, const PromptArgs& a) {
     const int smem = (BM * (D + 4) + BN * (D + 4) + BN * D + BM * (BN + 4)) * 4;
-    cudaError_t e = cudaFuncSetAttribute(gqa_prompt_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(gqa_prompt_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1] = {pdl_attr()};
@@ -226,18 +216,15 @@ cudaError_t launch(const Launch& L, const PromptArgs& a) {
     cfg.stream = L.stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, gqa_prompt_simt_kernel<T, D>, a);
+    e = cudaLaunchKernelEx(&cfg, gqa_prompt_simt_kernel<D>, a);
     count_launch();
     return e;
 }
 
 }  // namespace
 
-size_t gqa_prompt_workspace_bytes(int total, int n_seqs, dsa_dtype_t dtype) { return 0; }
-
-cudaError_t launch_gqa_prompt_simt(const Launch& L, const PromptArgs& a, dsa_dtype_t dtype, int head_dim) {
-    if (dtype == DSA_FP32) return head_dim == 64 ? launch<float, 64>(L, a) : launch<float, 128>(L, a);
-    return head_dim == 64 ? launch<__nv_bfloat16, 64>(L, a) : launch<__nv_bfloat16, 128>(L, a);
+cudaError_t launch_gqa_prompt_simt(const Launch& L, const PromptArgs& a, int head_dim) {
+    return head_dim == 64 ? launch<64>(L, a) : launch<128>(L, a);
 }
 
 }  // namespace dsa

@@ -1,0 +1,576 @@
+// Causal grouped-query attention over whole prompts, packed one behind the
+// other, bf16 on the 5th-generation tensor cores:
+//   out[i,h] = sum_{j <= i} softmax_j(scale q_i . k_j) v_j   within each prompt.
+//
+// A persistent block per SM works on items of two query tiles of 128 rows that
+// share their keys: two heads of one group over the same rows (even groups),
+// or two neighbouring row tiles of one head (odd groups).  Per 128 keys:
+//   S_t = Q_t K^T      tcgen05, [128 x 128 x D] into tensor memory
+//   P_t = softmax part one thread per row: the row's 128 scores are read into
+//                      registers, brought to base 2 and rounded to bf16 over the
+//                      scores' own place in tensor memory
+//   O_t += P_t V       tcgen05 with P from tensor memory
+// The products alternate between the tiles (O_0, S_0', O_1, S_1'), so that
+// one tile's exponentials run under the other tile's products.  The running
+// maximum is lazy: O is rescaled only when a row's maximum grows by more than
+// 2^8, by the row's own thread, which knows from S's arrival that all earlier
+// products have finished (products complete in order).
+//
+// Warps 0-3 / 4-7: softmax and epilogue of tile 0 / 1; 8: products, tensor
+// memory; 9: TMA loads; 10: zeroes the rows of a last V tile that lie behind
+// the prompt (they belong to other prompts, and 0 times their infinities
+// would not be 0).  Items are taken longest first.
+#include "common.cuh"
+#include "launchers.h"
+#include "sm100.cuh"
+#include "tensor_map.h"
+
+namespace dsa {
+
+using namespace sm100;
+
+namespace {
+
+constexpr int BM = 128, BN = 128;
+constexpr int MMA_WARP = 8, LOAD_WARP = 9, ZERO_WARP = 10;
+constexpr int THREADS = 384;
+// registers: launched at 168 x 384; the softmax warps take what the others give back
+constexpr int REGS_SOFTMAX = 216, REGS_REST = 72;
+static_assert(256 * REGS_SOFTMAX + 128 * REGS_REST <= 168 * THREADS, "register split exceeds launch");
+constexpr int TMEM_COLS = 512;
+constexpr int INLINE_SEQS = 32;     // prompts that a warp schedules without a list
+constexpr float RESCALE_LOG2 = 8.f;
+constexpr float LN2 = 0.6931471805599453f;
+
+template <int D> struct Cfg {
+    static constexpr int TILE = 128 * D * 2;                // bytes of a Q, K or V tile
+    static constexpr int STAGES = D == 128 ? 4 : 8;         // K / V ring
+    static constexpr int SMEM = 2 * TILE + STAGES * TILE + 1024 + 1024;
+    static constexpr int O_COL = 256;                       // S_0, S_1 at 0, 128; O_0, O_1 behind
+};
+
+template <int STAGES> struct Bars {
+    uint64_t q_full, q_empty, kv_full[STAGES], kv_empty[STAGES];
+    uint64_t s_full[2], p_ready[2], o_final[2], to_zero, zeroed;
+    uint32_t tmem;
+    int abort;
+};
+
+struct Entry {
+    int seq, block;
+};
+
+struct Sched {                      // where the items come from
+    const Entry* list;              // NULL: scheduled by the warp itself
+    const int* count;
+    int pairs;                      // items per row block: head pairs (even groups) or heads
+    int rows_per_block;             // 128 (even groups) or 256
+    bool two_heads;
+};
+
+// One warp's view of the items, longest first.
+struct Items {
+    int start, len, blocks;         // of prompt `lane` (inline scheduling)
+    int entries;
+
+    __device__ __forceinline__ void init(const PromptArgs& a, const Sched& s) {
+        const int lane = threadIdx.x & 31;
+        if (s.list) {
+            entries = *s.count;
+            return;
+        }
+        start = len = 0;
+        if (lane < a.n_seqs) bounds(a, lane, start, len);
+        blocks = (len + s.rows_per_block - 1) / s.rows_per_block;
+        entries = at_least(1);
+    }
+    static __device__ __forceinline__ void bounds(const PromptArgs& a, int seq, int& start, int& len) {
+        start = a.cu_seqlens[seq];
+        len = a.cu_seqlens[seq + 1] - start;
+        if (start < 0 || len < 0 || (int64_t)start + len > a.total) {
+            record_error(a.err, DEV_ERR_BAD_INDEX);
+            start = len = 0;
+        }
+    }
+    // row blocks whose number (from 1) within their prompt is at least v
+    __device__ __forceinline__ int at_least(int v) const {
+        return (int)__reduce_add_sync(0xffffffffu, (unsigned)max(0, blocks - v + 1));
+    }
+    // Entry e: blocks in falling order of their number (their work); false past the end.
+    __device__ __forceinline__ bool get(const PromptArgs& a, const Sched& s, int e, int& first, int& n, int& row0) const {
+        if (e >= entries) return false;
+        if (s.list) {
+            const Entry x = s.list[e];
+            first = a.cu_seqlens[x.seq];
+            n = a.cu_seqlens[x.seq + 1] - first;
+            row0 = x.block * s.rows_per_block;
+            return true;
+        }
+        int lo = 1, hi = (int)__reduce_max_sync(0xffffffffu, (unsigned)blocks) + 1;
+        while (hi - lo > 1) {                   // at_least(lo) > e >= at_least(hi)
+            const int mid = (lo + hi) >> 1;
+            if (at_least(mid) > e) lo = mid;
+            else hi = mid;
+        }
+        const unsigned have = __ballot_sync(0xffffffffu, blocks >= lo);
+        const int seq = (int)__fns(have, 0, e - at_least(lo + 1) + 1);
+        first = __shfl_sync(0xffffffffu, start, seq);
+        n = __shfl_sync(0xffffffffu, len, seq);
+        row0 = (lo - 1) * s.rows_per_block;
+        return true;
+    }
+};
+
+struct Item {
+    int first, len;                 // the prompt's first packed row, and its length
+    int head[2], row0[2], n[2];     // per tile: query head, first row in the prompt, key tiles (0: no tile)
+    int kvh, n_max;
+};
+
+// The block's r-th item; odd rounds run backwards over the blocks, so that
+// neither end of the grid collects the longer ones.
+__device__ __forceinline__ bool get_item(const PromptArgs& a, const Sched& s, const Items& items, int round, Item& w) {
+    const int g = gridDim.x, b = blockIdx.x;
+    const int64_t i = (int64_t)round * g + ((round & 1) ? g - 1 - b : b);
+    const int64_t e = i / s.pairs;
+    const int p = (int)(i - e * s.pairs);
+    int row0;
+    if (e > 0x7fffffff || !items.get(a, s, (int)e, w.first, w.len, row0)) return false;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        w.head[t] = s.two_heads ? 2 * p + t : p;
+        w.row0[t] = s.two_heads ? row0 : row0 + t * BM;
+        w.n[t] = w.row0[t] < w.len ? w.row0[t] / BN + 1 : 0;
+    }
+    w.kvh = w.head[0] / (a.n_heads / a.n_kv_heads);
+    w.n_max = max(w.n[0], w.n[1]);
+    return true;
+}
+
+// 2^x on the MUFU unit: relative error ~2^-22, -inf -> +0.
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+}  // namespace
+
+// The items' list for more prompts than a warp holds: row blocks sorted by
+// their number within their prompt, falling (a counting sort in one block).
+constexpr int LIST_BINS = 4096;
+__global__ void __launch_bounds__(1024) gqa_prompt_list_kernel(const PromptArgs a, int rows_per_block, Entry* list,
+                                                               int* count, int max_entries) {
+    pdl_wait();
+    pdl_launch_dependents();
+    __shared__ int bins[LIST_BINS];
+    __shared__ int warp_sum[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < LIST_BINS; i += 1024) bins[i] = 0;
+    __syncthreads();
+    // bin 0 holds the largest numbers
+    auto bin_of = [](int block) { return LIST_BINS - 1 - min(block, LIST_BINS - 1); };
+    for (int s = warp; s < a.n_seqs; s += 32) {
+        int start, len;
+        Items::bounds(a, s, start, len);
+        const int blocks = (len + rows_per_block - 1) / rows_per_block;
+        for (int b = lane; b < blocks; b += 32) atomicAdd(&bins[bin_of(b)], 1);
+    }
+    __syncthreads();
+    // exclusive prefix sum over the bins, four per thread
+    int v[LIST_BINS / 1024], sum = 0;
+#pragma unroll
+    for (int i = 0; i < LIST_BINS / 1024; ++i) {
+        v[i] = bins[tid * (LIST_BINS / 1024) + i];
+        sum += v[i];
+    }
+    int x = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    int before = x - sum;
+    for (int i = 0; i < warp; ++i) before += warp_sum[i];
+#pragma unroll
+    for (int i = 0; i < LIST_BINS / 1024; ++i) {
+        bins[tid * (LIST_BINS / 1024) + i] = before;
+        before += v[i];
+    }
+    if (tid == 1023) *count = min(before, max_entries);
+    __syncthreads();
+    for (int s = warp; s < a.n_seqs; s += 32) {
+        int start, len;
+        Items::bounds(a, s, start, len);
+        const int blocks = (len + rows_per_block - 1) / rows_per_block;
+        for (int b = lane; b < blocks; b += 32) {
+            const int at = atomicAdd(&bins[bin_of(b)], 1);
+            if (at < max_entries) list[at] = Entry{s, b};   // (more only when prompts overlap)
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1) gqa_prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map,
+                                                                   const __grid_constant__ CUtensorMap k_map,
+                                                                   const __grid_constant__ CUtensorMap v_map,
+                                                                   const PromptArgs a, const Sched sched) {
+    using C = Cfg<D>;
+    constexpr int NS = C::STAGES, TILE = C::TILE, KBLK = D / 64, BLK = 128 * 128;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t* qbuf = smem;                               // two Q tiles: [D / 64][128 rows x 128 B], swizzled
+    uint8_t* kvbuf = smem + 2 * TILE;                   // ring of K and V tiles, same layout
+    auto* bars = (Bars<NS>*)(smem + (2 + NS) * TILE);
+    volatile int* abort_flag = &bars->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        mbar_init(&bars->q_full, 1);
+        mbar_init(&bars->q_empty, 1);
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&bars->kv_full[i], 1);
+            mbar_init(&bars->kv_empty[i], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&bars->s_full[t], 1);
+            mbar_init(&bars->p_ready[t], 4);
+            mbar_init(&bars->o_final[t], 1);
+        }
+        mbar_init(&bars->to_zero, 1);
+        mbar_init(&bars->zeroed, 1);
+        bars->abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&q_map);
+        tma_prefetch_desc(&k_map);
+        tma_prefetch_desc(&v_map);
+    }
+    if (warp == MMA_WARP) {
+        tmem_alloc(&bars->tmem, TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem;
+    pdl_wait();
+    pdl_launch_dependents();
+    Items items;
+    Item w;
+    items.init(a, sched);
+
+    if (warp < 8) {
+        regs_inc<REGS_SOFTMAX>();
+        // ------------------------------------------- softmax and epilogue ----
+        const int t = warp >> 2, r = (warp & 3) * 32 + lane;        // tile; row = tensor-memory lane
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t s_col = lane_base + t * 128, o_col = lane_base + C::O_COL + t * D;
+        uint32_t n_s = 0, n_o = 0;                                  // phases used so far
+        bool ok = true;
+        for (int round = 0; ok && get_item(a, sched, items, round, w); ++round) {
+            const int n = w.n[t];
+            if (n == 0) continue;
+            float m = -INFINITY, l = 0.f;                           // maximum in use (base 2), sum
+            for (int j = 0; j < n; ++j) {
+                ok = __all_sync(0xffffffffu,
+                                mbar_wait(&bars->s_full[t], n_s & 1, a.err, DEV_ERR_TIMEOUT_MMA, abort_flag));
+                if (!ok) break;
+                ++n_s;
+                tc_fence_after();
+                float s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(s_col + c * 32, s[c]);
+                tmem_ld_wait();
+                if (j == n - 1) {                                   // the diagonal tile: keys up to the row's own
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (c * 32 + e > r) s[c][e] = -INFINITY;
+                }
+                float mx[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mx[i] = fmaxf(s[i >> 1][(i & 1) * 16], s[i >> 1][(i & 1) * 16 + 1]);
+#pragma unroll
+                for (int e = 2; e < 16; ++e)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) mx[i] = fmaxf(mx[i], s[i >> 1][(i & 1) * 16 + e]);
+#pragma unroll
+                for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+                    for (int i = 0; i < d; ++i) mx[i] = fmaxf(mx[i], mx[i + d]);
+                const float top = mx[0] * a.scale_log2;
+                bool move = false;
+                float f = 1.f;
+                if (top > m + RESCALE_LOG2 || (m == -INFINITY && top > m)) {
+                    f = fast_exp2(m - top);                         // 0 while nothing has been summed
+                    m = top;
+                    l *= f;
+                    move = j > 0;
+                }
+                if (__any_sync(0xffffffffu, move)) {
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        float v[32];
+                        tmem_ld32(o_col + c * 32, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] *= f;
+                        tmem_st32(o_col + c * 32, v);
+                    }
+                }
+                const float base = m == -INFINITY ? 0.f : m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float p0 = fast_exp2(fmaf(s[c][2 * e], a.scale_log2, -base));
+                        const float p1 = fast_exp2(fmaf(s[c][2 * e + 1], a.scale_log2, -base));
+                        sum[e & 3] += p0 + p1;
+                        pk[e] = bf16x2_bits(p0, p1);
+                    }
+                    tmem_st16(s_col + c * 16, pk);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->p_ready[t]);
+            }
+            if (!ok) break;
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_final[t], n_o & 1, a.err, DEV_ERR_TIMEOUT_MMA, abort_flag));
+            if (!ok) break;
+            ++n_o;
+            tc_fence_after();
+            const bool mine = w.row0[t] + r < w.len;
+            const int64_t row = (int64_t)w.first + w.row0[t] + r;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            uint4* out = (uint4*)((__nv_bfloat16*)a.out + (row * a.n_heads + w.head[t]) * D);
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                float v[32];
+                tmem_ld32(o_col + c * 32, v);
+                tmem_ld_wait();
+                if (mine) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        out[c * 4 + e] = make_uint4(bf16x2_bits(v[8 * e] * inv, v[8 * e + 1] * inv),
+                                                    bf16x2_bits(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
+                                                    bf16x2_bits(v[8 * e + 4] * inv, v[8 * e + 5] * inv),
+                                                    bf16x2_bits(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
+                }
+            }
+            if (mine) a.lse[row * a.n_heads + w.head[t]] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+            tc_fence_before();          // O has been read before this tile's next P is announced
+        }
+    } else {
+        regs_dec<REGS_REST>();
+        if (warp == MMA_WARP) {
+            // ------------------------------------------------- products ----
+            constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, 0, 0), idesc_o = idesc_bf16_f32(BM, D, 0, 1);
+            const uint32_t qb = smem_u32(qbuf), kvb = smem_u32(kvbuf);
+            const bool leader = elect_one();
+            uint32_t slot = 0, n_p[2] = {0, 0}, n_z = 0;    // first ring slot of the item; phases used
+            bool ok = true;
+            auto wait_kv = [&](uint32_t i) {
+                return mbar_wait(&bars->kv_full[i % NS], (i / NS) & 1, a.err, DEV_ERR_TIMEOUT_TMA, abort_flag);
+            };
+            auto product_s = [&](int t, uint32_t kslot) {
+                const uint32_t ka = kvb + (kslot % NS) * TILE, qa = qb + t * TILE;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (uint32_t)((kk >> 2) * BLK + (kk & 3) * 32);
+                    mma_ss(tmem + t * 128, desc_sw128(qa + off, 1024), desc_sw128(ka + off, 1024), idesc_s, kk > 0);
+                }
+                mma_commit(&bars->s_full[t]);
+            };
+            for (int round = 0; get_item(a, sched, items, round, w); ++round) {
+                if (leader && ok) {
+                    ok = mbar_wait(&bars->q_full, round & 1, a.err, DEV_ERR_TIMEOUT_TMA, abort_flag) && wait_kv(slot);
+                    if (ok) {
+                        tc_fence_after();
+                        for (int t = 0; t < 2; ++t)
+                            if (w.n[t] > 0) product_s(t, slot);
+                        mma_commit(&bars->kv_empty[slot % NS]);
+                        if (w.n_max == 1) mma_commit(&bars->q_empty);
+                    }
+                    for (int j = 0; j < w.n_max && ok; ++j) {
+                        const uint32_t vslot = slot + 2 * j + 1, kslot = vslot + 1;
+                        ok = wait_kv(vslot);
+                        if (ok && (j + 1) * BN > w.len) {
+                            mbar_arrive(&bars->to_zero);        // the tile has landed
+                            ok = mbar_wait(&bars->zeroed, n_z & 1, a.err, DEV_ERR_TIMEOUT_PEER, abort_flag);
+                            ++n_z;
+                        }
+                        const int last_now = w.n[1] > j ? 1 : 0, last_next = w.n[1] > j + 1 ? 1 : 0;
+                        bool have_k = false;
+                        for (int t = 0; t < 2 && ok; ++t) {
+                            if (j >= w.n[t]) continue;
+                            ok = mbar_wait(&bars->p_ready[t], n_p[t] & 1, a.err, DEV_ERR_TIMEOUT_PEER, abort_flag);
+                            if (!ok) break;
+                            ++n_p[t];
+                            tc_fence_after();
+                            const uint32_t va = kvb + (vslot % NS) * TILE;
+#pragma unroll
+                            for (int kk = 0; kk < BN / 16; ++kk)
+                                mma_ts(tmem + C::O_COL + t * D, tmem + t * 128 + kk * 8,
+                                       desc_sw128_mn(va + kk * 16 * 128, BLK, 1024), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+                            if (j == w.n[t] - 1) mma_commit(&bars->o_final[t]);
+                            if (t == last_now) mma_commit(&bars->kv_empty[vslot % NS]);
+                            if (j + 1 < w.n[t]) {
+                                if (!have_k) ok = wait_kv(kslot);
+                                if (!ok) break;
+                                have_k = true;
+                                tc_fence_after();
+                                product_s(t, kslot);
+                                if (t == last_next) {
+                                    mma_commit(&bars->kv_empty[kslot % NS]);
+                                    if (j + 1 == w.n_max - 1) mma_commit(&bars->q_empty);
+                                }
+                            }
+                        }
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, __ffs(__ballot_sync(0xffffffffu, leader)) - 1) != 0;
+                if (!ok) break;
+                slot += 2 * w.n_max;
+            }
+        } else if (warp == LOAD_WARP) {
+            // ---------------------------------------------------- loads ----
+            const bool leader = elect_one();
+            uint32_t slot = 0;
+            bool ok = true;
+            auto load = [&](const CUtensorMap* map, int col, int row) {
+                const uint32_t st = slot % NS;
+                if (!mbar_wait(&bars->kv_empty[st], ((slot / NS) & 1) ^ 1, a.err, DEV_ERR_TIMEOUT_MMA, abort_flag)) return false;
+                mbar_arrive_expect_tx(&bars->kv_full[st], TILE);
+#pragma unroll
+                for (int b = 0; b < KBLK; ++b)
+                    tma_load_2d(kvbuf + st * TILE + b * BLK, map, col + b * 64, row, &bars->kv_full[st]);
+                ++slot;
+                return true;
+            };
+            int q_loads = 0;
+            for (int round = 0; get_item(a, sched, items, round, w); ++round) {
+                if (leader && ok) {
+                    ok = mbar_wait(&bars->q_empty, (round & 1) ^ 1, a.err, DEV_ERR_TIMEOUT_MMA, abort_flag);
+                    if (ok) {
+                        const int tiles = (w.n[0] > 0) + (w.n[1] > 0);
+                        mbar_arrive_expect_tx(&bars->q_full, tiles * TILE);
+                        for (int t = 0; t < 2; ++t)
+                            if (w.n[t] > 0)
+                                for (int b = 0; b < KBLK; ++b)
+                                    tma_load_2d(qbuf + t * TILE + b * BLK, &q_map, w.head[t] * D + b * 64,
+                                                w.first + w.row0[t], &bars->q_full);
+                        ++q_loads;
+                    }
+                    for (int j = 0; j < w.n_max && ok; ++j)
+                        ok = load(&k_map, w.kvh * D, w.first + j * BN) && load(&v_map, w.kvh * D, w.first + j * BN);
+                }
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, __ffs(__ballot_sync(0xffffffffu, leader)) - 1) != 0;
+                if (!ok) break;
+            }
+            if (leader && *abort_flag) {
+                // after an abort, tiles already requested land before the block exits
+                for (uint32_t i = slot > NS ? slot - NS : 0; i < slot; ++i)
+                    mbar_wait(&bars->kv_full[i % NS], (i / NS) & 1, a.err, DEV_ERR_TIMEOUT_TMA, nullptr);
+                if (q_loads > 0) mbar_wait(&bars->q_full, (q_loads - 1) & 1, a.err, DEV_ERR_TIMEOUT_TMA, nullptr);
+            }
+        } else if (warp == ZERO_WARP) {
+            // ----------------------------- rows of V behind a prompt's end ----
+            uint32_t slot = 0, n_z = 0;
+            for (int round = 0; get_item(a, sched, items, round, w); ++round) {
+                const int left = w.len - (w.n_max - 1) * BN;            // rows of the last key tile
+                if (left < BN) {
+                    const uint32_t i = slot + 2 * (w.n_max - 1) + 1;
+                    const bool ok = __all_sync(0xffffffffu, mbar_wait(&bars->to_zero, n_z & 1, a.err, DEV_ERR_TIMEOUT_PEER,
+                                                                      abort_flag));
+                    if (!ok) break;
+                    ++n_z;
+                    for (int b = 0; b < KBLK; ++b) {
+                        uint8_t* rows = kvbuf + (i % NS) * TILE + b * BLK;
+                        for (int o = left * 128 + lane * 16; o < BN * 128; o += 32 * 16) st_shared_v4(rows + o, 0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->zeroed);
+                }
+                slot += 2 * w.n_max;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+namespace {
+
+int max_entries(int total, int n_seqs) { return total / BM + (n_seqs < total ? n_seqs : total); }
+
+template <int D>
+cudaError_t launch(const Launch& L, const PromptArgs& a, void* workspace) {
+    using C = Cfg<D>;
+    CUtensorMap q_map, k_map, v_map;
+    const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    if (!make_map_sw128_ld(&q_map, bf, 2, a.q, (uint64_t)a.n_heads * D, a.total, (uint64_t)a.ld_q * 2, 64, BM) ||
+        !make_map_sw128_ld(&k_map, bf, 2, a.k, (uint64_t)a.n_kv_heads * D, a.total, (uint64_t)a.ld_k * 2, 64, BN) ||
+        !make_map_sw128_ld(&v_map, bf, 2, a.v, (uint64_t)a.n_kv_heads * D, a.total, (uint64_t)a.ld_v * 2, 64, BN))
+        return cudaErrorInvalidValue;
+    const int group = a.n_heads / a.n_kv_heads;
+    Sched s;
+    s.two_heads = group % 2 == 0;
+    s.pairs = s.two_heads ? a.n_heads / 2 : a.n_heads;
+    s.rows_per_block = s.two_heads ? BM : 2 * BM;
+    s.list = nullptr;
+    s.count = nullptr;
+    cudaError_t e = cudaFuncSetAttribute(gqa_prompt_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1] = {pdl_attr()};
+    cfg.stream = L.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const int most = max_entries(a.total, a.n_seqs);
+    if (a.n_seqs > INLINE_SEQS) {
+        s.count = (const int*)workspace;
+        s.list = (const Entry*)((char*)workspace + 256);
+        cfg.gridDim = dim3(1);
+        cfg.blockDim = dim3(1024);
+        e = cudaLaunchKernelEx(&cfg, gqa_prompt_list_kernel, a, s.rows_per_block, (Entry*)s.list, (int*)s.count, most);
+        count_launch();
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t items = (int64_t)most * s.pairs;
+    cfg.gridDim = dim3((unsigned)(items < L.num_sms ? items : L.num_sms));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    e = cudaLaunchKernelEx(&cfg, gqa_prompt_tc_kernel<D>, q_map, k_map, v_map, a, s);
+    count_launch();
+    return e;
+}
+
+}  // namespace
+
+size_t gqa_prompt_workspace_bytes(int total, int n_seqs, dsa_dtype_t dtype) {
+    if (dtype != DSA_BF16 || n_seqs <= INLINE_SEQS) return 0;
+    return 256 + (size_t)max_entries(total, n_seqs) * sizeof(Entry);
+}
+
+cudaError_t launch_gqa_prompt_tc(const Launch& L, const PromptArgs& a, int head_dim, void* workspace) {
+    return head_dim == 64 ? launch<64>(L, a, workspace) : launch<128>(L, a, workspace);
+}
+
+}  // namespace dsa
