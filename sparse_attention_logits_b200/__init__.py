@@ -391,6 +391,35 @@ def indexer_key_append(k: torch.Tensor, slot: torch.Tensor, k_cache: torch.Tenso
 
 # ---- grouped-query attention and its paged key-value cache -------------------
 
+# torch's current stream as a raw handle, without building a Stream object
+# (2 us a call, as much as a small kernel); the public way where it is missing.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
+def _call(name: str, dev: torch.device, *args) -> None:
+    """Entry point `name` on torch's current stream of dev; dev is made the
+    current device only when it is not."""
+    fn = getattr(_lib, name)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, _raw_stream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _raw_stream(dev.index))
+    if st != DSA_OK:
+        raise DSAError(st, name)
+
+
+def _scratch(t: torch.Tensor, dev: torch.device, size_fn, *sizes) -> torch.Tensor:
+    """A workspace of size_fn(*sizes) bytes (asked on dev), beside tensor t."""
+    if torch.cuda.current_device() == dev.index:
+        need = size_fn(*sizes)
+    else:
+        with torch.cuda.device(dev):
+            need = size_fn(*sizes)
+    return t.new_empty(need // t.element_size() + 1)
+
+
 def _int32(*named) -> None:
     for name, t in named:
         if t is not None and t.dtype != torch.int32:
@@ -435,11 +464,10 @@ def kv_cache_append(k: torch.Tensor, v: torch.Tensor, row_batch: torch.Tensor, r
     if row_batch.shape != (n,) or row_pos.shape != (n,):
         raise ValueError("row_batch and row_pos must be [n]")
     ld_k, ld_v = _rows("k", k, dev), _rows("v", v, dev)
-    with torch.cuda.device(dev):
-        _check(_lib.kv_cache_append(k.data_ptr(), ld_k, v.data_ptr(), ld_v, _dt(k), row_batch.data_ptr(),
-                                    row_pos.data_ptr(), n, page_table.data_ptr(), page_table.shape[0],
-                                    page_table.shape[1], page, pages, hkv, d, k_cache.data_ptr(), v_cache.data_ptr(),
-                                    kv, _ptr(k_scale), _ptr(v_scale), _stream(dev)), "kv_cache_append")
+    batch, width = page_table.shape
+    _call("kv_cache_append", dev, k.data_ptr(), ld_k, v.data_ptr(), ld_v, _dt(k), row_batch.data_ptr(), row_pos.data_ptr(),
+          n, page_table.data_ptr(), batch, width, page, pages, hkv, d, k_cache.data_ptr(), v_cache.data_ptr(), kv,
+          _ptr(k_scale), _ptr(v_scale))
 
 
 def gqa_decode_attention_workspace_size(rows: int, n_heads: int, n_kv_heads: int, head_dim: int,
@@ -468,23 +496,20 @@ def gqa_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
         raise ValueError("row_batch and row_pos must be [rows]")
     ld_q = _rows("q", q, dev)
     if out is None:
-        out = torch.empty((rows, H, d), dtype=q.dtype, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must be [rows, n_heads, head_dim] of q's type")
     if lse is None:
-        lse = torch.empty((rows, H), dtype=torch.float32, device=dev)
+        lse = q.new_empty((rows, H), dtype=torch.float32)
     elif lse.shape != (rows, H) or lse.dtype != torch.float32:
         raise ValueError("lse must be fp32 [rows, n_heads]")
-    with torch.cuda.device(dev):
-        if workspace is None:
-            need = _lib.gqa_decode_attention_workspace_size(rows, H, hkv, d, kv)
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-        wsb = workspace.numel() * workspace.element_size()
-        _check(_lib.gqa_decode_attention(q.data_ptr(), ld_q, _dt(q), k_cache.data_ptr(), v_cache.data_ptr(), kv,
-                                         _ptr(k_scale), _ptr(v_scale), page_table.data_ptr(), page_table.shape[0],
-                                         page_table.shape[1], page, pages, row_batch.data_ptr(), row_pos.data_ptr(),
-                                         rows, H, hkv, d, float(scale), out.data_ptr(), lse.data_ptr(),
-                                         workspace.data_ptr(), wsb, _stream(dev)), "gqa_decode_attention")
+    batch, width = page_table.shape
+    if workspace is None:
+        workspace = _scratch(q, dev, _lib.gqa_decode_attention_workspace_size, rows, H, hkv, d, kv)
+    _call("gqa_decode_attention", dev, q.data_ptr(), ld_q, _dt(q), k_cache.data_ptr(), v_cache.data_ptr(), kv,
+          _ptr(k_scale), _ptr(v_scale), page_table.data_ptr(), batch, width, page, pages, row_batch.data_ptr(),
+          row_pos.data_ptr(), rows, H, hkv, d, float(scale), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+          workspace.nbytes)
     return out, lse
 
 
@@ -513,23 +538,19 @@ def gqa_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_s
     n_seqs = cu_seqlens.shape[0] - 1
     ld_q, ld_k, ld_v = _rows("q", q, dev), _rows("k", k, dev), _rows("v", v, dev)
     if out is None:
-        out = torch.empty((T, H, d), dtype=q.dtype, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must be [total, n_heads, head_dim] of q's type")
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+        lse = q.new_empty((T, H), dtype=torch.float32)
     elif lse.shape != (T, H) or lse.dtype != torch.float32:
         raise ValueError("lse must be fp32 [total, n_heads]")
     dt = _dt(q)
-    with torch.cuda.device(dev):
-        if workspace is None:
-            need = _lib.gqa_prompt_attention_workspace_size(T, n_seqs, H, d, dt)
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-        wsb = workspace.numel() * workspace.element_size()
-        _check(_lib.gqa_prompt_attention(q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v, dt,
-                                         cu_seqlens.data_ptr(), n_seqs, T, H, hkv, d, float(scale), out.data_ptr(),
-                                         lse.data_ptr(), workspace.data_ptr(), wsb, _stream(dev)),
-               "gqa_prompt_attention")
+    if workspace is None:
+        workspace = _scratch(q, dev, _lib.gqa_prompt_attention_workspace_size, T, n_seqs, H, d, dt)
+    _call("gqa_prompt_attention", dev, q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v, dt,
+          cu_seqlens.data_ptr(), n_seqs, T, H, hkv, d, float(scale), out.data_ptr(), lse.data_ptr(),
+          workspace.data_ptr(), workspace.nbytes)
     return out, lse
 
 
@@ -565,10 +586,9 @@ def kv_pages_extend(page_table: torch.Tensor, seq_len: torch.Tensor, ref_count: 
     """Room for add[i] more tokens in sequence seqs[i]: fresh pages (lowest
     free ids first) and seq_len grown, in place."""
     dev, n = _books(page_table, seq_len, ref_count, seqs, add)
-    with torch.cuda.device(dev):
-        _check(_lib.kv_pages_extend(page_table.data_ptr(), page_table.shape[0], page_table.shape[1], page_size,
-                                    seq_len.data_ptr(), ref_count.data_ptr(), ref_count.shape[0], seqs.data_ptr(),
-                                    add.data_ptr(), n, _stream(dev)), "kv_pages_extend")
+    batch, width = page_table.shape
+    _call("kv_pages_extend", dev, page_table.data_ptr(), batch, width, page_size, seq_len.data_ptr(), ref_count.data_ptr(),
+          ref_count.shape[0], seqs.data_ptr(), add.data_ptr(), n)
 
 
 def kv_pages_free(page_table: torch.Tensor, seq_len: torch.Tensor, ref_count: torch.Tensor, seqs: torch.Tensor,
@@ -576,10 +596,9 @@ def kv_pages_free(page_table: torch.Tensor, seq_len: torch.Tensor, ref_count: to
     """Drop sequences seqs[i]: their pages' counts go down, their table rows
     and lengths are cleared, in place."""
     dev, n = _books(page_table, seq_len, ref_count, seqs)
-    with torch.cuda.device(dev):
-        _check(_lib.kv_pages_free(page_table.data_ptr(), page_table.shape[0], page_table.shape[1], page_size,
-                                  seq_len.data_ptr(), ref_count.data_ptr(), ref_count.shape[0], seqs.data_ptr(), n,
-                                  _stream(dev)), "kv_pages_free")
+    batch, width = page_table.shape
+    _call("kv_pages_free", dev, page_table.data_ptr(), batch, width, page_size, seq_len.data_ptr(), ref_count.data_ptr(),
+          ref_count.shape[0], seqs.data_ptr(), n)
 
 
 def kv_pages_fork(page_table: torch.Tensor, seq_len: torch.Tensor, ref_count: torch.Tensor, parents: torch.Tensor,
@@ -590,14 +609,13 @@ def kv_pages_fork(page_table: torch.Tensor, seq_len: torch.Tensor, ref_count: to
     dev, n = _books(page_table, seq_len, ref_count, parents, children)
     ptrs, sizes, n_caches = _cache_list(caches, ref_count.shape[0], dev)
     if workspace is None:
-        workspace = torch.empty(max(8 * n, 1), dtype=torch.uint8, device=dev)
+        workspace = parents.new_empty(_lib.kv_pages_fork_workspace_size(n) // 4 + 1)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the pool's device")
-    with torch.cuda.device(dev):
-        _check(_lib.kv_pages_fork(page_table.data_ptr(), page_table.shape[0], page_table.shape[1], page_size,
-                                  seq_len.data_ptr(), ref_count.data_ptr(), ref_count.shape[0], parents.data_ptr(),
-                                  children.data_ptr(), n, ptrs, sizes, n_caches, workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), _stream(dev)), "kv_pages_fork")
+    batch, width = page_table.shape
+    _call("kv_pages_fork", dev, page_table.data_ptr(), batch, width, page_size, seq_len.data_ptr(), ref_count.data_ptr(),
+          ref_count.shape[0], parents.data_ptr(), children.data_ptr(), n, ptrs, sizes, n_caches, workspace.data_ptr(),
+          workspace.nbytes)
 
 
 def kv_pages_copy(caches, src: torch.Tensor, dst: torch.Tensor) -> None:
@@ -611,9 +629,7 @@ def kv_pages_copy(caches, src: torch.Tensor, dst: torch.Tensor) -> None:
         return
     pages = caches[0].shape[0]
     ptrs, sizes, n_caches = _cache_list(caches, pages, dev)
-    with torch.cuda.device(dev):
-        _check(_lib.kv_pages_copy(ptrs, sizes, n_caches, pages, src.data_ptr(), dst.data_ptr(), src.shape[0],
-                                  _stream(dev)), "kv_pages_copy")
+    _call("kv_pages_copy", dev, ptrs, sizes, n_caches, pages, src.data_ptr(), dst.data_ptr(), src.shape[0])
 
 
 def kv_pages_compact(page_table: torch.Tensor, ref_count: torch.Tensor, caches=(),
@@ -633,12 +649,10 @@ def kv_pages_compact(page_table: torch.Tensor, ref_count: torch.Tensor, caches=(
     pages = ref_count.shape[0]
     ptrs, sizes, n_caches = _cache_list(caches, pages, dev)
     if workspace is None:
-        workspace = torch.empty(_lib.kv_pages_compact_workspace_size(pages), dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
-        _check(_lib.kv_pages_compact(page_table.data_ptr(), page_table.shape[0], page_table.shape[1],
-                                     ref_count.data_ptr(), pages, ptrs, sizes, n_caches, table_out.data_ptr(),
-                                     ref_out.data_ptr(), workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), _stream(dev)), "kv_pages_compact")
+        workspace = ref_count.new_empty(_lib.kv_pages_compact_workspace_size(pages) // 4 + 1)
+    batch, width = page_table.shape
+    _call("kv_pages_compact", dev, page_table.data_ptr(), batch, width, ref_count.data_ptr(), pages, ptrs, sizes, n_caches,
+          table_out.data_ptr(), ref_out.data_ptr(), workspace.data_ptr(), workspace.nbytes)
     return table_out, ref_out
 
 

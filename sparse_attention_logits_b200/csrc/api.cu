@@ -597,6 +597,12 @@ dsa_status_t gqa_decode_attention(const void* q, int64_t ld_q, dsa_dtype_t dtype
     a.rows = rows;
     a.n_heads = n_heads;
     a.n_kv_heads = n_kv_heads;
+    // with 2^b >= page_size the smallest such power, mul = floor(2^(31 + b) / page_size) + 1 < 2^32 divides
+    // every s < 2^31 exactly: mul * page_size exceeds 2^(31 + b) by at most 2^b
+    uint32_t b = 0;
+    while (((int64_t)1 << b) < page_size) ++b;
+    a.page_shift = 31 + b;
+    a.page_mul = (uint32_t)((((uint64_t)1 << a.page_shift) / (uint64_t)page_size) + 1);
     a.scale_log2 = scale * 1.4426950408889634f;
     a.out = out;
     a.lse = lse;

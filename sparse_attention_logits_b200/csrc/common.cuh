@@ -52,6 +52,16 @@ int device_cached(std::atomic<int> (&cache)[kMaxDevices], F&& compute) {
     return v > 0 ? v : 0;
 }
 
+// Allows `kern` `bytes` of dynamic shared memory on the current device, once
+// per device (`done`: one array per kernel).
+template <class K>
+cudaError_t allow_smem(std::atomic<int> (&done)[kMaxDevices], K kern, int bytes) {
+    const int ok = device_cached(done, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess ? 1 : 0;
+    });
+    return ok ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 struct Launch {
     cudaStream_t stream;
     unsigned* err;   // device error word of the current device

@@ -5,8 +5,8 @@
 // so the cache's bytes at the HBM rate are the floor.
 //
 // Work split.  A pair is (row, kv head, tile of the group's heads); its keys
-// are cut into units of 64.  All pairs' units form one line, and block i of
-// the grid takes the i-th equal stretch of it, whatever the rows' lengths:
+// are cut into units of KT (64, or 128 over an fp8 cache).  All pairs' units form
+// one line, and block i of the grid takes the i-th equal stretch of it, whatever the rows' lengths:
 // ragged batches load every SM alike, and one long row uses the whole GPU.
 // Lengths are read on the device (nothing about them is known to the host),
 // so a captured call serves growing sequences.  A stretch that holds a whole
@@ -22,10 +22,8 @@ using namespace sm100;
 
 namespace {
 
-constexpr int KT = 64;              // keys per unit
 constexpr int THREADS = 128;
 constexpr int WARPS = THREADS / 32;
-constexpr int WK = KT / WARPS;      // keys of a unit that one warp takes
 constexpr float LN2 = 0.6931471805599453f;
 
 // 2^x on the MUFU unit: relative error ~2^-22, -inf -> +0.
@@ -44,30 +42,32 @@ struct Parts {
 };
 
 // Units of a row: at least one, so that empty rows are written too.
-__device__ __forceinline__ int row_units(const DecodeArgs& a, int row) {
+template <int KT> __device__ __forceinline__ int row_units(const DecodeArgs& a, int row) {
     const int pos = __ldg(a.row_pos + row);
     const int64_t room = (int64_t)a.max_pages * a.page_size;
     return pos < 0 ? 1 : pos < room ? pos / KT + 1 : (int)((room - 1) / KT) + 1;
 }
 
 // A walk along the line of units.
-struct Walk {
-    int row, hv, unit, units;       // place: row, pair of the row, unit of the pair; the row's units
-    int batch, keys;                // the row's sequence and number of visible keys (0: nothing to read)
+template <int KT> struct Walk {
+    int row, kvh, tile, unit, units;    // place: row, kv head, tile of its heads, unit; the row's units
+    int batch, keys;                    // the row's sequence and number of visible keys (0: nothing to read)
 
     __device__ __forceinline__ void enter_row(const DecodeArgs& a) {
         if (row >= a.rows) return;
-        units = row_units(a, row);
+        units = row_units<KT>(a, row);
         batch = __ldg(a.row_batch + row);
         const int64_t room = (int64_t)a.max_pages * a.page_size;
         const int pos = __ldg(a.row_pos + row);
         keys = pos < 0 || batch < 0 || batch >= a.batch ? 0 : (int)(pos < room ? pos + 1 : room);
     }
-    __device__ __forceinline__ void next(const DecodeArgs& a, int hvs) {
+    __device__ __forceinline__ void next(const DecodeArgs& a, int tiles) {
         if (++unit < units) return;
         unit = 0;
-        if (++hv < hvs) return;
-        hv = 0;
+        if (++tile < tiles) return;
+        tile = 0;
+        if (++kvh < a.n_kv_heads) return;
+        kvh = 0;
         ++row;
         enter_row(a);
     }
@@ -82,13 +82,15 @@ struct LocateShared {
 // This block's stretch [begin, end) of the line and the walk's start.  The
 // whole block takes part.  `per_block` units at least, so that short lines
 // are not cut finer than is worth joining.
-__device__ __forceinline__ void locate(const DecodeArgs& a, int hvs, int per_block, LocateShared& sh, Walk& w,
+template <int KT>
+__device__ __forceinline__ void locate(const DecodeArgs& a, int tiles, int per_block, LocateShared& sh, Walk<KT>& w,
                                        int64_t& begin, int64_t& end, int64_t& stretch) {
+    const int hvs = a.n_kv_heads * tiles;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (a.rows + THREADS - 1) / THREADS;
     const int r0 = min(a.rows, tid * per), r1 = min(a.rows, r0 + per);
     int sum = 0;
-    for (int r = r0; r < r1; ++r) sum += row_units(a, r);
+    for (int r = r0; r < r1; ++r) sum += row_units<KT>(a, r);
     int x = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -114,7 +116,7 @@ __device__ __forceinline__ void locate(const DecodeArgs& a, int hvs, int per_blo
         if (begin >= lo && begin < hi) {
             int r = r0, u = before;
             for (; r < r1; ++r) {
-                const int n = row_units(a, r);
+                const int n = row_units<KT>(a, r);
                 if (begin < (int64_t)(u + n) * hvs) break;
                 u += n;
             }
@@ -127,22 +129,24 @@ __device__ __forceinline__ void locate(const DecodeArgs& a, int hvs, int per_blo
         w.row = sh.row;
         w.enter_row(a);
         const int in_row = (int)(begin - (int64_t)sh.units_before * hvs);
-        w.hv = in_row / w.units;
-        w.unit = in_row - w.hv * w.units;
+        const int hv = in_row / w.units;
+        w.unit = in_row - hv * w.units;
+        w.kvh = hv / tiles;
+        w.tile = hv - w.kvh * tiles;
     }
 }
 
 // Row of the cache (in head_dim vectors) that holds key s of the walk's
 // sequence, or -1: not visible, or a bad page (reported).
-__device__ __forceinline__ int cache_row(const DecodeArgs& a, const Walk& w, int kvh, int s) {
+template <int KT> __device__ __forceinline__ int cache_row(const DecodeArgs& a, const Walk<KT>& w, int s) {
     if (s >= w.keys) return -1;
-    const int pi = s / a.page_size;
+    const int pi = (int)(((uint64_t)(uint32_t)s * a.page_mul) >> a.page_shift);     // s / page_size
     const int page = __ldg(a.page_table + (int64_t)w.batch * a.max_pages + pi);
     if (page < 0 || page >= a.num_pages) {
         record_error(a.err, DEV_ERR_BAD_INDEX);
         return -1;
     }
-    return (page * a.n_kv_heads + kvh) * a.page_size + (s - pi * a.page_size);
+    return (page * a.n_kv_heads + w.kvh) * a.page_size + (s - pi * a.page_size);
 }
 
 // ------------------------------------------------------------ CUDA cores --
@@ -166,22 +170,21 @@ template <int D>
 __global__ void __launch_bounds__(THREADS) gqa_decode_simt_kernel(const DecodeArgs a, const Parts parts) {
     pdl_wait();
     pdl_launch_dependents();
-    constexpr int GT = 8, VEC = D / 32;
+    constexpr int GT = 8, VEC = D / 32, KT = 64, WK = KT / WARPS;
     __shared__ LocateShared sh;
     __shared__ float s_o[WARPS][GT][D];
     __shared__ float s_m[WARPS][GT], s_l[WARPS][GT];
-    const int group = a.n_heads / a.n_kv_heads, tiles = ceil_div(group, GT), hvs = a.n_kv_heads * tiles;
+    const int group = a.n_heads / a.n_kv_heads, tiles = ceil_div(group, GT);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    Walk w;
+    Walk<KT> w;
     int64_t begin, end, stretch;
-    locate(a, hvs, 2, sh, w, begin, end, stretch);
+    locate<KT>(a, tiles, 2, sh, w, begin, end, stretch);
     const float* kc = (const float*)a.k_cache;
     const float* vc = (const float*)a.v_cache;
     for (int64_t at = begin; at < end;) {
-        const int kvh = w.hv / tiles, h0 = kvh * group + (w.hv - kvh * tiles) * GT;
-        const int heads = min(GT, (kvh + 1) * group - h0);
+        const int h0 = w.kvh * group + w.tile * GT, heads = min(GT, group - w.tile * GT);
         const int n = (int)min((int64_t)(w.units - w.unit), end - at);
-        if (w.unit == 0 && w.hv == 0 && tid == 0) {
+        if (w.unit == 0 && w.kvh == 0 && w.tile == 0 && tid == 0) {
             // reported once per row, by the block that begins it
             const int b = w.batch;
             if (b < 0 || b >= a.batch || __ldg(a.row_pos + w.row) >= (int64_t)a.max_pages * a.page_size)
@@ -199,7 +202,7 @@ __global__ void __launch_bounds__(THREADS) gqa_decode_simt_kernel(const DecodeAr
         float m = -INFINITY, l = 0.f;       // of head lane % 8
         for (int u = w.unit; u < w.unit + n; ++u) {
             const int s0 = u * KT + warp * WK;
-            const int my_row = lane < WK ? cache_row(a, w, kvh, s0 + lane) : -1;
+            const int my_row = lane < WK ? cache_row<KT>(a, w, s0 + lane) : -1;
 #pragma unroll 1
             for (int k0 = 0; k0 < WK; k0 += 4) {
                 float kx[4][VEC], vx[4][VEC];
@@ -309,19 +312,19 @@ __global__ void __launch_bounds__(THREADS) gqa_decode_simt_kernel(const DecodeAr
         }
         if (begins && tid == 0) {
             const int64_t last = (at + w.units - 1) / stretch;      // block of the pair's last unit
-            parts.meta[(int64_t)w.row * hvs + w.hv] = make_int2(blockIdx.x, (int)(last - blockIdx.x) + 1);
+            parts.meta[((int64_t)w.row * a.n_kv_heads + w.kvh) * tiles + w.tile] = make_int2(blockIdx.x, (int)(last - blockIdx.x) + 1);
         }
         __syncthreads();
         at += n;
         w.unit += n - 1;
-        w.next(a, hvs);
+        w.next(a, tiles);
     }
 }
 
 // ---------------------------------------------------------- tensor cores --
 //
 // bf16 and fp8 caches.  The work is bound by the cache's bytes, so the kernel
-// is built around its loads: each warp owns 16 keys of a unit and streams
+// is built around its loads: each warp owns 16 (fp8: 32) keys of a unit and streams
 // their K and V rows through a ring of its own (cp.async, 16 bytes per lane,
 // rows of unused places zero-filled), never waiting for another warp while a
 // pair lasts.  With up to 16 heads of a group as the M of mma.m16n8k16, one
@@ -339,8 +342,8 @@ __global__ void __launch_bounds__(THREADS) gqa_decode_simt_kernel(const DecodeAr
 // times the value scale relative to the largest scale met so far, which the
 // output carries like the running maximum.
 template <typename KV> struct MmaCfg;
-template <> struct MmaCfg<__nv_bfloat16> { static constexpr int STAGES = 3, BLOCKS = 2; };
-template <> struct MmaCfg<__nv_fp8_e4m3> { static constexpr int STAGES = 4, BLOCKS = 3; };
+template <> struct MmaCfg<__nv_bfloat16> { static constexpr int WK = 16, STAGES = 3, BLOCKS = 2; };
+template <> struct MmaCfg<__nv_fp8_e4m3> { static constexpr int WK = 32, STAGES = 2, BLOCKS = 3; };
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -402,33 +405,36 @@ __global__ void __launch_bounds__(THREADS, MmaCfg<KV>::BLOCKS) gqa_decode_mma_ke
     pdl_wait();
     pdl_launch_dependents();
     constexpr bool FP8 = sizeof(KV) == 1;
+    constexpr int WK = MmaCfg<KV>::WK, KT = WK * WARPS;     // keys of a warp's slice, and of a unit
     constexpr int RB = D * (int)sizeof(KV);         // bytes of a row
     constexpr int PIECES = RB / 16;
     constexpr int SLICE = WK * RB;                  // K (or V) bytes of a warp's slice
     constexpr int STAGES = MmaCfg<KV>::STAGES;
+    constexpr uint32_t ALL = WK == 32 ? 0xffffffffu : 0xffffu;
     constexpr int SLOT = 2 * SLICE + (FP8 ? 2 * WK * 4 : 0) + 16;   // K, V, scales, the mask of valid keys
     constexpr int KS = D / 16, NT = D / 8;
+    static_assert(!FP8 || WK == 32, "a lane per key's scales");
     static_assert(2 * SLICE >= 8 * D * 4, "the outputs of 8 heads are exchanged in a slot");
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ LocateShared sh;
     __shared__ float2 s_ml[WARPS][16];
-    const int group = a.n_heads / a.n_kv_heads, tiles = ceil_div(group, GT), hvs = a.n_kv_heads * tiles;
+    const int group = a.n_heads / a.n_kv_heads, tiles = ceil_div(group, GT);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r4 = lane >> 2, c4 = lane & 3;        // fragment row / column group
     uint8_t* ring = smem + warp * STAGES * SLOT;
-    Walk w;
+    Walk<KT> w;
     int64_t begin, end, stretch;
-    locate(a, hvs, 2, sh, w, begin, end, stretch);
+    locate<KT>(a, tiles, 128 / KT, sh, w, begin, end, stretch);
     if (begin >= end) return;
     const uint8_t* kc = (const uint8_t*)a.k_cache;
     const uint8_t* vc = (const uint8_t*)a.v_cache;
 
     // the loads' walk runs STAGES units ahead of the products'; the page
     // of a slice is looked up one unit before its rows are requested
-    Walk lw = w;
+    Walk<KT> lw = w;
     int64_t to_load = end - begin;
     auto look = [&]() -> int {
-        return to_load > 0 ? cache_row(a, lw, lw.hv / tiles, lw.unit * KT + warp * WK + (lane & (WK - 1))) : -1;
+        return to_load > 0 ? cache_row<KT>(a, lw, lw.unit * KT + warp * WK + (lane & (WK - 1))) : -1;
     };
     int row = look();
     auto request = [&](int st) {
@@ -443,12 +449,13 @@ __global__ void __launch_bounds__(THREADS, MmaCfg<KV>::BLOCKS) gqa_decode_mma_ke
                 cp_async_16(slot + piece_at<FP8, RB, false>(r, c), kc + off, n);
                 cp_async_16(slot + SLICE + piece_at<FP8, RB, true>(r, c), vc + off, n);
             }
-            if (FP8)
-                cp_async_4(slot + 2 * SLICE + lane * 4, (lane < WK ? a.k_scale : a.v_scale) + (row >= 0 ? row : 0),
-                           row >= 0 ? 4u : 0u);
-            const uint32_t valid = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
+            if (FP8) {
+                cp_async_4(slot + 2 * SLICE + lane * 4, a.k_scale + (row >= 0 ? row : 0), row >= 0 ? 4u : 0u);
+                cp_async_4(slot + 2 * SLICE + WK * 4 + lane * 4, a.v_scale + (row >= 0 ? row : 0), row >= 0 ? 4u : 0u);
+            }
+            const uint32_t valid = __ballot_sync(0xffffffffu, row >= 0) & ALL;
             if (lane == 0) *(uint32_t*)(slot + SLOT - 16) = valid;
-            lw.next(a, hvs);
+            lw.next(a, tiles);
             --to_load;
             row = look();
         }
@@ -459,10 +466,9 @@ __global__ void __launch_bounds__(THREADS, MmaCfg<KV>::BLOCKS) gqa_decode_mma_ke
 
     int st = 0;
     for (int64_t at = begin; at < end;) {
-        const int kvh = w.hv / tiles, h0 = kvh * group + (w.hv - kvh * tiles) * GT;
-        const int heads = min(GT, (kvh + 1) * group - h0);
+        const int h0 = w.kvh * group + w.tile * GT, heads = min(GT, group - w.tile * GT);
         const int n = (int)min((int64_t)(w.units - w.unit), end - at);
-        if (w.unit == 0 && w.hv == 0 && tid == 0 &&
+        if (w.unit == 0 && w.kvh == 0 && w.tile == 0 && tid == 0 &&
             (w.batch < 0 || w.batch >= a.batch || __ldg(a.row_pos + w.row) >= (int64_t)a.max_pages * a.page_size))
             record_error(a.err, DEV_ERR_BAD_INDEX);     // reported once per row, by the block that begins it
         // Q fragments: rows r4 and r4 + 8 (heads); k-step kk holds dims
@@ -522,21 +528,28 @@ __global__ void __launch_bounds__(THREADS, MmaCfg<KV>::BLOCKS) gqa_decode_mma_ke
             const uint32_t kb = smem_u32(slot), vb = kb + SLICE;
             const uint32_t valid = *(const uint32_t*)(slot + SLOT - 16);
             if (valid) {
-                // S = Q K^T: two tiles of 8 keys; lane: rows r4 / r4 + 8, keys 8 t + 2 c4 + {0, 1}
-                float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                // S = Q K^T: tiles of 8 keys; lane: rows r4 / r4 + 8, keys 8 t + 2 c4 + {0, 1}
+                float s[WK / 8][4];
+#pragma unroll
+                for (int t = 0; t < WK / 8; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
                 if (!FP8) {
 #pragma unroll
-                    for (int kk = 0; kk < KS; ++kk) {
-                        uint32_t b[4];
-                        ldmatrix_x4(b, kb + piece_at<FP8, RB, false>((lane >> 4) * 8 + (lane & 7), kk * 2 + ((lane >> 3) & 1)));
-                        mma16816<FP8>(s[0], qf[kk], b[0], b[1]);
-                        mma16816<FP8>(s[1], qf[kk], b[2], b[3]);
-                    }
+                    for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+                        for (int t = 0; t < WK / 8; t += 2) {
+                            uint32_t b[4];
+                            ldmatrix_x4(b, kb + piece_at<FP8, RB, false>(t * 8 + (lane >> 4) * 8 + (lane & 7),
+                                                                         kk * 2 + ((lane >> 3) & 1)));
+                            mma16816<FP8>(s[t], qf[kk], b[0], b[1]);
+                            mma16816<FP8>(s[t + 1], qf[kk], b[2], b[3]);
+                        }
                 } else {
 #pragma unroll
                     for (int i = 0; i < D / 64; ++i)
 #pragma unroll
-                        for (int t = 0; t < 2; ++t) {
+                        for (int t = 0; t < WK / 8; ++t) {
                             const uint4 x = ld_shared_v4(slot + piece_at<FP8, RB, false>(t * 8 + r4, 4 * i + c4));
                             const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -544,33 +557,34 @@ __global__ void __launch_bounds__(THREADS, MmaCfg<KV>::BLOCKS) gqa_decode_mma_ke
                                 mma16816<FP8>(s[t], qf[4 * i + j], e4m3x2_f16x2(wd[j]), e4m3x2_f16x2(wd[j] >> 16));
                         }
                 }
-                float2 vs2[2];
+                float2 vs2[WK / 8];
                 if (FP8) {
                     const float* ks = (const float*)(slot + 2 * SLICE);
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
+                    for (int t = 0; t < WK / 8; ++t) {
                         const float2 k2 = *(const float2*)(ks + t * 8 + 2 * c4);
                         vs2[t] = *(const float2*)(ks + WK + t * 8 + 2 * c4);
-                        s[t][0] *= k2.x; s[t][1] *= k2.y; s[t][2] *= k2.x; s[t][3] *= k2.y;
+                        s[t][0] *= k2.x; s[t][1] *= k2.y;
+                        if (GT > 8) { s[t][2] *= k2.x; s[t][3] *= k2.y; }
                     }
                 }
-                // running maximum, and the output brought to it
+                if (valid != ALL) {
+#pragma unroll
+                    for (int t = 0; t < WK / 8; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (!((valid >> (t * 8 + 2 * c4 + (e & 1))) & 1u)) s[t][e] = -INFINITY;
+                }
+                // running maximum (scores times zs; zs > 0), and the output brought to it
                 float f[2] = {1.f, 1.f};
                 bool moved = false;
 #pragma unroll
                 for (int half = 0; half < (GT > 8 ? 2 : 1); ++half) {
-                    float top = -INFINITY;
+                    float top = fmaxf(s[0][2 * half], s[0][2 * half + 1]);
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float& z = s[t][2 * half + e];
-                            z *= zs[half];
-                            if (valid != 0xffffu && !((valid >> (t * 8 + 2 * c4 + e)) & 1u)) z = -INFINITY;
-                            top = fmaxf(top, z);
-                        }
+                    for (int t = 1; t < WK / 8; ++t) top = fmaxf(top, fmaxf(s[t][2 * half], s[t][2 * half + 1]));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) * zs[half];
                     if (top > m[half]) {
                         f[half] = fast_exp2(m[half] - top);
                         m[half] = top;
@@ -580,7 +594,9 @@ __global__ void __launch_bounds__(THREADS, MmaCfg<KV>::BLOCKS) gqa_decode_mma_ke
                 }
                 float vmove = 1.f;
                 if (FP8) {
-                    float top = fmaxf(fmaxf(fabsf(vs2[0].x), fabsf(vs2[0].y)), fmaxf(fabsf(vs2[1].x), fabsf(vs2[1].y)));
+                    float top = fmaxf(fabsf(vs2[0].x), fabsf(vs2[0].y));
+#pragma unroll
+                    for (int t = 1; t < WK / 8; ++t) top = fmaxf(top, fmaxf(fabsf(vs2[t].x), fabsf(vs2[t].y)));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)), 1e-30f);   // its reciprocal is finite
                     if (top > vref) {
@@ -597,54 +613,60 @@ __global__ void __launch_bounds__(THREADS, MmaCfg<KV>::BLOCKS) gqa_decode_mma_ke
                         if (GT > 8) { o[t][2] *= f[1] * vmove; o[t][3] *= f[1] * vmove; }
                     }
                 }
-                // P, and O += P V
-                uint32_t pf[4] = {0u, 0u, 0u, 0u};
+                // P (as the A operand, 16 keys a piece), and O += P V
+                uint32_t pf[WK / 16][4];
 #pragma unroll
-                for (int half = 0; half < (GT > 8 ? 2 : 1); ++half) {
-                    const float base = m[half] > -INFINITY ? m[half] : 0.f;
+                for (int t = 0; t < WK / 8; ++t) {
+                    pf[t / 2][2 * (t & 1) + 1] = 0u;
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        float p0 = fast_exp2(s[t][2 * half] - base), p1 = fast_exp2(s[t][2 * half + 1] - base);
+                    for (int half = 0; half < (GT > 8 ? 2 : 1); ++half) {
+                        const float base = m[half] > -INFINITY ? m[half] : 0.f;
+                        float p0 = fast_exp2(fmaf(s[t][2 * half], zs[half], -base));
+                        float p1 = fast_exp2(fmaf(s[t][2 * half + 1], zs[half], -base));
                         l[half] += p0 + p1;
                         if (FP8) {
                             p0 *= vs2[t].x * vinv;
                             p1 *= vs2[t].y * vinv;
                         }
-                        pf[half + 2 * t] = pack2<FP8>(p0, p1);
+                        pf[t / 2][half + 2 * (t & 1)] = pack2<FP8>(p0, p1);
                     }
                 }
-                if (!FP8) {
 #pragma unroll
-                    for (int t = 0; t < NT; t += 2) {
-                        uint32_t b[4];
-                        ldmatrix_x4_t(b, vb + piece_at<FP8, RB, true>(((lane >> 3) & 1) * 8 + (lane & 7), t + (lane >> 4)));
-                        mma16816<FP8>(o[t], pf, b[0], b[1]);
-                        mma16816<FP8>(o[t + 1], pf, b[2], b[3]);
-                    }
-                } else {
-                    // column r4 of tile t is dim (D / 8) r4 + t; keys 2 c4 + {0, 1, 8, 9}
-                    constexpr int RUN = D / 8;
-                    uint32_t x[4][RUN / 4];
+                for (int k16 = 0; k16 < WK / 16; ++k16) {
+                    if (!FP8) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int key = 2 * c4 + (k & 1) + 8 * (k >> 1);
-                        const uint8_t* src = slot + SLICE + piece_at<FP8, RB, true>(key, r4 * RUN / 16) + (r4 * RUN) % 16;
-                        if (RUN == 16) {
-                            const uint4 v = ld_shared_v4(src);
-                            x[k][0] = v.x; x[k][1] = v.y; x[k][RUN / 4 - 2] = v.z; x[k][RUN / 4 - 1] = v.w;
-                        } else {
-                            const uint2 v = *(const uint2*)src;
-                            x[k][0] = v.x; x[k][1] = v.y;
+                        for (int t = 0; t < NT; t += 2) {
+                            uint32_t b[4];
+                            ldmatrix_x4_t(b, vb + piece_at<FP8, RB, true>(k16 * 16 + ((lane >> 3) & 1) * 8 + (lane & 7),
+                                                                          t + (lane >> 4)));
+                            mma16816<FP8>(o[t], pf[k16], b[0], b[1]);
+                            mma16816<FP8>(o[t + 1], pf[k16], b[2], b[3]);
                         }
-                    }
+                    } else {
+                        // column r4 of tile t is dim (D / 8) r4 + t; keys 2 c4 + {0, 1, 8, 9}
+                        constexpr int RUN = D / 8;
+                        uint32_t x[4][RUN / 4];
 #pragma unroll
-                    for (int j = 0; j < RUN / 4; ++j) {
-                        const uint32_t a0 = __byte_perm(x[0][j], x[1][j], 0x5140), a1 = __byte_perm(x[0][j], x[1][j], 0x7362);
-                        const uint32_t b0 = __byte_perm(x[2][j], x[3][j], 0x5140), b1 = __byte_perm(x[2][j], x[3][j], 0x7362);
-                        mma16816<FP8>(o[4 * j], pf, e4m3x2_f16x2(a0), e4m3x2_f16x2(b0));
-                        mma16816<FP8>(o[4 * j + 1], pf, e4m3x2_f16x2(a0 >> 16), e4m3x2_f16x2(b0 >> 16));
-                        mma16816<FP8>(o[4 * j + 2], pf, e4m3x2_f16x2(a1), e4m3x2_f16x2(b1));
-                        mma16816<FP8>(o[4 * j + 3], pf, e4m3x2_f16x2(a1 >> 16), e4m3x2_f16x2(b1 >> 16));
+                        for (int k = 0; k < 4; ++k) {
+                            const int key = k16 * 16 + 2 * c4 + (k & 1) + 8 * (k >> 1);
+                            const uint8_t* src = slot + SLICE + piece_at<FP8, RB, true>(key, r4 * RUN / 16) + (r4 * RUN) % 16;
+                            if (RUN == 16) {
+                                const uint4 v = ld_shared_v4(src);
+                                x[k][0] = v.x; x[k][1] = v.y; x[k][RUN / 4 - 2] = v.z; x[k][RUN / 4 - 1] = v.w;
+                            } else {
+                                const uint2 v = *(const uint2*)src;
+                                x[k][0] = v.x; x[k][1] = v.y;
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < RUN / 4; ++j) {
+                            const uint32_t a0 = __byte_perm(x[0][j], x[1][j], 0x5140), a1 = __byte_perm(x[0][j], x[1][j], 0x7362);
+                            const uint32_t b0 = __byte_perm(x[2][j], x[3][j], 0x5140), b1 = __byte_perm(x[2][j], x[3][j], 0x7362);
+                            mma16816<FP8>(o[4 * j], pf[k16], e4m3x2_f16x2(a0), e4m3x2_f16x2(b0));
+                            mma16816<FP8>(o[4 * j + 1], pf[k16], e4m3x2_f16x2(a0 >> 16), e4m3x2_f16x2(b0 >> 16));
+                            mma16816<FP8>(o[4 * j + 2], pf[k16], e4m3x2_f16x2(a1), e4m3x2_f16x2(b1));
+                            mma16816<FP8>(o[4 * j + 3], pf[k16], e4m3x2_f16x2(a1 >> 16), e4m3x2_f16x2(b1 >> 16));
+                        }
                     }
                 }
             }
@@ -718,13 +740,13 @@ __global__ void __launch_bounds__(THREADS, MmaCfg<KV>::BLOCKS) gqa_decode_mma_ke
         }
         if (begins && tid == 0) {
             const int64_t last = (at + w.units - 1) / stretch;      // block of the pair's last unit
-            parts.meta[(int64_t)w.row * hvs + w.hv] = make_int2(blockIdx.x, (int)(last - blockIdx.x) + 1);
+            parts.meta[((int64_t)w.row * a.n_kv_heads + w.kvh) * tiles + w.tile] = make_int2(blockIdx.x, (int)(last - blockIdx.x) + 1);
         }
         request(st);
         st = st + 1 == STAGES ? 0 : st + 1;
         at += n;
         w.unit += n - 1;
-        w.next(a, hvs);
+        w.next(a, tiles);
     }
     cp_async_wait<0>();
 }
@@ -788,9 +810,7 @@ cudaError_t launch_decode(const Launch& L, const DecodeArgs& a, Kern kern, int s
     p.o = (float*)workspace;
     p.ml = (float2*)((char*)workspace + up256((size_t)2 * grid * GT * D * 4));
     p.meta = (int2*)((char*)p.ml + up256((size_t)2 * grid * GT * 8));
-    cudaError_t e = cudaSuccess;
-    if (smem > 0) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1] = {pdl_attr()};
     cfg.gridDim = dim3(grid);
@@ -813,10 +833,16 @@ cudaError_t launch_decode(const Launch& L, const DecodeArgs& a, Kern kern, int s
 template <typename KV, int D>
 cudaError_t launch_mma(const Launch& L, const DecodeArgs& a, void* workspace) {
     constexpr bool FP8 = sizeof(KV) == 1;
-    constexpr int slot = 2 * WK * D * (int)sizeof(KV) + (FP8 ? 2 * WK * 4 : 0) + 16;
+    constexpr int WK = MmaCfg<KV>::WK, slot = 2 * WK * D * (int)sizeof(KV) + (FP8 ? 2 * WK * 4 : 0) + 16;
     constexpr int smem = WARPS * MmaCfg<KV>::STAGES * slot, per_sm = MmaCfg<KV>::BLOCKS;
-    if (a.n_heads / a.n_kv_heads <= 8)
+    static std::atomic<int> done8[kMaxDevices], done16[kMaxDevices];
+    if (a.n_heads / a.n_kv_heads <= 8) {
+        const cudaError_t e = allow_smem(done8, gqa_decode_mma_kernel<KV, D, 8>, smem);
+        if (e != cudaSuccess) return e;
         return launch_decode<__nv_bfloat16, D, 8>(L, a, gqa_decode_mma_kernel<KV, D, 8>, smem, per_sm, workspace);
+    }
+    const cudaError_t e = allow_smem(done16, gqa_decode_mma_kernel<KV, D, 16>, smem);
+    if (e != cudaSuccess) return e;
     return launch_decode<__nv_bfloat16, D, 16>(L, a, gqa_decode_mma_kernel<KV, D, 16>, smem, per_sm, workspace);
 }
 

@@ -205,7 +205,8 @@ __global__ void __launch_bounds__(THREADS) gqa_prompt_simt_kernel(const PromptAr
 template <int D>
 cudaError_t launch(const Launch& L, const PromptArgs& a) {
     const int smem = (BM * (D + 4) + BN * (D + 4) + BN * D + BM * (BN + 4)) * 4;
-    cudaError_t e = cudaFuncSetAttribute(gqa_prompt_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<int> done[kMaxDevices];
+    cudaError_t e = allow_smem(done, gqa_prompt_simt_kernel<D>, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1] = {pdl_attr()};

@@ -536,7 +536,8 @@ cudaError_t launch(const Launch& L, const PromptArgs& a, void* workspace) {
     s.rows_per_block = s.two_heads ? BM : 2 * BM;
     s.list = nullptr;
     s.count = nullptr;
-    cudaError_t e = cudaFuncSetAttribute(gqa_prompt_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    static std::atomic<int> done[kMaxDevices];
+    cudaError_t e = allow_smem(done, gqa_prompt_tc_kernel<D>, C::SMEM);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1] = {pdl_attr()};

@@ -543,7 +543,10 @@ __global__ void __launch_bounds__(256) kv_compact_kernel(const __grid_constant__
     }
 }
 
-int words_per_book_cta(int num_pages) { return ceil_div(ceil_div(num_pages, 32), BOOK_CTAS); }
+constexpr int words_per_book_cta(int num_pages) { return ceil_div(ceil_div(num_pages, 32), BOOK_CTAS); }
+constexpr int books_smem(int num_pages, int n) { return (words_per_book_cta(num_pages) + 3 * n + 1) * 4; }
+constexpr int BOOK_SMEM_MAX = books_smem(DSA_KV_PAGES_MAX_POOL, DSA_KV_PAGES_MAX_LIST);
+static_assert(BOOK_SMEM_MAX <= 200 * 1024, "the books' bits and lists fit in shared memory");
 
 // Caches [c0, c0 + n) of the caller's list as a kernel parameter.
 CopyList copy_list(const CacheList& l, int c0, int n) {
@@ -611,13 +614,10 @@ cudaError_t launch_kv_copy(const Launch& L, const CacheList& l, const int32_t* s
 
 cudaError_t launch_kv_free(const Launch& L, const BooksArgs& a) { return launch(kv_free_kernel, a.n, 256, 0, L, a); }
 
-size_t kv_books_smem(int num_pages, int n) {
-    return ((size_t)words_per_book_cta(num_pages) + 3 * (size_t)n + 1) * 4;
-}
-
 cudaError_t launch_kv_extend(const Launch& L, const BooksArgs& a) {
-    const size_t smem = kv_books_smem(a.num_pages, a.n);
-    cudaError_t e = cudaFuncSetAttribute(kv_assign_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const size_t smem = books_smem(a.num_pages, a.n);
+    static std::atomic<int> done[kMaxDevices];
+    const cudaError_t e = allow_smem(done, kv_assign_kernel<false>, BOOK_SMEM_MAX);
     if (e != cudaSuccess) return e;
     return launch(kv_assign_kernel<false>, BOOK_CTAS, BOOK_THREADS, smem, L, a, words_per_book_cta(a.num_pages));
 }
@@ -627,8 +627,9 @@ size_t kv_fork_workspace_bytes(int n) { return (size_t)n * 8; }
 cudaError_t launch_kv_fork(const Launch& L, BooksArgs a, const CacheList& l, void* workspace) {
     a.pair_src = (int32_t*)workspace;
     a.pair_dst = a.pair_src + a.n;
-    const size_t smem = kv_books_smem(a.num_pages, a.n);
-    cudaError_t e = cudaFuncSetAttribute(kv_assign_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const size_t smem = books_smem(a.num_pages, a.n);
+    static std::atomic<int> done[kMaxDevices];
+    cudaError_t e = allow_smem(done, kv_assign_kernel<true>, BOOK_SMEM_MAX);
     if (e != cudaSuccess) return e;
     e = launch(kv_assign_kernel<true>, BOOK_CTAS, BOOK_THREADS, smem, L, a, words_per_book_cta(a.num_pages));
     if (e != cudaSuccess) return e;
@@ -644,7 +645,8 @@ cudaError_t launch_kv_compact(const Launch& L, CompactArgs a, const CacheList& l
     a.pair_dst = a.pair_src + a.num_pages;
     a.moved_ref = a.pair_dst + a.num_pages;
     const int words = words_per_book_cta(a.num_pages);
-    cudaError_t e = cudaFuncSetAttribute(kv_compact_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, words * 4);
+    static std::atomic<int> done[kMaxDevices];
+    cudaError_t e = allow_smem(done, kv_compact_plan_kernel, BOOK_SMEM_MAX);
     if (e != cudaSuccess) return e;
     e = launch(kv_compact_plan_kernel, BOOK_CTAS, BOOK_THREADS, (size_t)words * 4, L, a, words);
     if (e != cudaSuccess) return e;

@@ -140,7 +140,6 @@ struct CacheList {                      // host arrays of the caller
 };
 cudaError_t launch_kv_copy(const Launch& L, const CacheList& l, const int32_t* src, const int32_t* dst, int n);
 cudaError_t launch_kv_free(const Launch& L, const BooksArgs& a);
-size_t kv_books_smem(int num_pages, int n);
 cudaError_t launch_kv_extend(const Launch& L, const BooksArgs& a);
 size_t kv_fork_workspace_bytes(int n);
 cudaError_t launch_kv_fork(const Launch& L, BooksArgs a, const CacheList& l, void* workspace);
@@ -160,6 +159,7 @@ struct DecodeArgs {
     const int32_t* row_batch;
     const int32_t* row_pos;
     int rows, n_heads, n_kv_heads;
+    uint32_t page_mul, page_shift;      // s / page_size = (s * page_mul) >> page_shift for 0 <= s < 2^31
     float scale_log2;
     void* out;                  // [rows, n_heads, head_dim]
     float* lse;                 // [rows, n_heads]
