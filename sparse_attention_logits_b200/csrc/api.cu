@@ -519,6 +519,7 @@ dsa_status_t kv_cache_append(const void* k, int64_t ld_k, const void* v, int64_t
     if (!row_batch || !row_pos) return fail(DSA_ERR_INVALID_ARG, "%s: null pointer", name);
     if ((st = check_rows(name, "k", k, ld_k, n_kv_heads, head_dim, dtype)) != DSA_OK) return st;
     if ((st = check_rows(name, "v", v, ld_v, n_kv_heads, head_dim, dtype)) != DSA_OK) return st;
+    if ((int64_t)n * 2 * n_kv_heads > ((int64_t)1 << 31) - 2) return fail(DSA_ERR_UNSUPPORTED, "%s: too many rows and heads", name);
     dsa::Launch L;
     if ((st = make_launch(stream, &L)) != DSA_OK) return st;
     dsa::AppendArgs a;
@@ -539,6 +540,8 @@ dsa_status_t kv_cache_append(const void* k, int64_t ld_k, const void* v, int64_t
     a.v_cache = v_cache;
     a.k_scale = k_scale;
     a.v_scale = v_scale;
+    a.by_page = dsa::fast_div(page_size);
+    a.by_head = dsa::fast_div(n_kv_heads);
     a.err = L.err;
     return cuda_status(dsa::launch_kv_append(L, a, dtype, kv_dtype, head_dim), "kv_cache_append launch");
 }
@@ -597,12 +600,7 @@ dsa_status_t gqa_decode_attention(const void* q, int64_t ld_q, dsa_dtype_t dtype
     a.rows = rows;
     a.n_heads = n_heads;
     a.n_kv_heads = n_kv_heads;
-    // with 2^b >= page_size the smallest such power, mul = floor(2^(31 + b) / page_size) + 1 < 2^32 divides
-    // every s < 2^31 exactly: mul * page_size exceeds 2^(31 + b) by at most 2^b
-    uint32_t b = 0;
-    while (((int64_t)1 << b) < page_size) ++b;
-    a.page_shift = 31 + b;
-    a.page_mul = (uint32_t)((((uint64_t)1 << a.page_shift) / (uint64_t)page_size) + 1);
+    a.by_page = dsa::fast_div(page_size);
     a.scale_log2 = scale * 1.4426950408889634f;
     a.out = out;
     a.lse = lse;

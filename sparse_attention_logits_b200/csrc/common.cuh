@@ -103,6 +103,21 @@ __device__ __forceinline__ uint32_t score_key(float f) {
 
 __host__ __device__ constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+// Division of 0 <= s < 2^31 by a number known to the host.  With 2^b the
+// smallest power >= d, mul = floor(2^(31 + b) / d) + 1 < 2^32 exceeds the true
+// reciprocal by so little (mul * d - 2^(31 + b) <= 2^b) that the quotient is
+// exact for every s < 2^31.
+struct FastDiv {
+    uint32_t mul, shift;
+    int d;
+    __host__ __device__ __forceinline__ int div(int s) const { return (int)(((uint64_t)(uint32_t)s * mul) >> shift); }
+};
+inline FastDiv fast_div(int d) {
+    uint32_t b = 0;
+    while (((int64_t)1 << b) < d) ++b;
+    return FastDiv{(uint32_t)((((uint64_t)1 << (31 + b)) / (uint64_t)d) + 1), 31 + b, d};
+}
+
 // Programmatic dependent launch.  The step's kernels are launched with the
 // programmatic-serialisation attribute, so the next kernel of the stream may
 // be scheduled while this one drains.  pdl_wait() blocks until every kernel

@@ -140,7 +140,7 @@ __device__ __forceinline__ void locate(const DecodeArgs& a, int tiles, int per_b
 // sequence, or -1: not visible, or a bad page (reported).
 template <int KT> __device__ __forceinline__ int cache_row(const DecodeArgs& a, const Walk<KT>& w, int s) {
     if (s >= w.keys) return -1;
-    const int pi = (int)(((uint64_t)(uint32_t)s * a.page_mul) >> a.page_shift);     // s / page_size
+    const int pi = a.by_page.div(s);
     const int page = __ldg(a.page_table + (int64_t)w.batch * a.max_pages + pi);
     if (page < 0 || page >= a.num_pages) {
         record_error(a.err, DEV_ERR_BAD_INDEX);

@@ -30,89 +30,141 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
 
 // ---------------------------------------------------------------- append --
 //
-// A group of D/8 lanes moves one (row, head) vector of K or V, eight elements
-// per lane, so a group's loads and stores are whole contiguous vectors.  fp8:
-// the group's amax by shuffles, scale = amax / 448 (1 for an all-zero row),
-// code = nearest even of value / scale, every operation in binary32 rounded
-// on its own (the indexer key cache's rule).  Bandwidth bound: each element
-// is read once and written once.
+// A group of D/16 lanes moves one (row, head) vector of K or V, sixteen
+// elements per lane.  fp8: the group's amax by shuffles, scale = amax / 448 (1
+// for an all-zero row), code = nearest even of value / scale, every operation
+// in binary32 rounded on its own (the indexer key cache's rule).
+//
+// Bandwidth bound, but behind a chain of dependent loads (position and
+// sequence, page, then the stores).  A block takes a run of rows: one thread
+// per row walks the chain, while all groups already load the data of their
+// first vectors, which does not depend on it.
+constexpr int APPEND_ROWS = 32, APPEND_UNROLL = 2;
+
+// Codes of sixteen values over their scale.  All share the divisor, so its
+// reciprocal r is rounded once and each quotient is corrected twice with the
+// exact remainder, q <- q + r (x - q sc): by P. Markstein's theorem
+// ("Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990) the second correction of a quotient within one unit gives
+// the correctly rounded one.  Five multiply-adds a value against about twelve
+// instructions of a division, which made the kernel issue-bound (52 us where
+// the loads and stores take 20).  Bits matter here: bf16 rows hold values that
+// fall exactly between two codes, about one in a hundred.  Below 2^-60 the
+// remainders might not be exact: scales that small divide.
+__device__ __forceinline__ uint4 e4m3_codes(const float (&x)[16], float sc) {
+    float q[16];
+    if (sc >= 0x1p-60f) {
+        const float r = __frcp_rn(sc);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            float y = x[e] * r;
+            y = fmaf(r, fmaf(-y, sc, x[e]), y);
+            q[e] = fmaf(r, fmaf(-y, sc, x[e]), y);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) q[e] = __fdiv_rn(x[e], sc);
+    }
+    uint32_t c[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = e4m3x2(q[4 * e], q[4 * e + 1]) | (e4m3x2(q[4 * e + 2], q[4 * e + 3]) << 16);
+    return make_uint4(c[0], c[1], c[2], c[3]);
+}
+
 template <int D, bool F32_IN, int FMT>     // FMT: DSA_FP32, DSA_BF16, DSA_FP8_E4M3
 __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
     pdl_wait();
     pdl_launch_dependents();
-    constexpr int LANES = D / 8;
-    const int sub = threadIdx.x % LANES;
-    const int64_t tasks = (int64_t)a.n * 2 * a.n_kv_heads;
-    const int64_t first = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) / LANES;
-    const int64_t step = (int64_t)gridDim.x * blockDim.x / LANES;
-    const unsigned group = LANES == 16 ? 0xffffu << (threadIdx.x & 16) : 0xffu << (threadIdx.x & 24);
-    for (int64_t t = first; t < tasks; t += step) {
-        // head innermost, then K / V, then row
-        const int64_t rs = t / a.n_kv_heads;
-        const int head = (int)(t - rs * a.n_kv_heads);
-        const int64_t row = rs >> 1;
-        const bool is_v = rs & 1;
-        const int pos = __ldg(a.row_pos + row);
-        if (pos < 0) continue;                              // not stored
-        const int b = __ldg(a.row_batch + row);
-        const int pi = pos / a.page_size;
-        int page = -1;
-        if (b >= 0 && b < a.batch && pi < a.max_pages) page = __ldg(a.page_table + (int64_t)b * a.max_pages + pi);
-        if (page < 0 || page >= a.num_pages) {
-            if (sub == 0) record_error(a.err, DEV_ERR_BAD_INDEX);
-            continue;
+    constexpr int LANES = D / 16, GROUPS = 256 / LANES, U = APPEND_UNROLL, W = F32_IN ? 4 : 2;
+    __shared__ int2 place[APPEND_ROWS];         // page (-1: not stored) and place in it
+    const int sub = threadIdx.x % LANES, grp = threadIdx.x / LANES;
+    const unsigned group = (LANES == 8 ? 0xffu : 0xfu) << (threadIdx.x & 31 & ~(LANES - 1));
+    const int rpb = min(APPEND_ROWS, (a.n + gridDim.x - 1) / (int)gridDim.x);
+    for (int r0 = blockIdx.x * rpb; r0 < a.n; r0 += gridDim.x * rpb) {
+        const int rows = min(rpb, a.n - r0), tasks = rows * 2 * a.n_kv_heads;
+        int pos = -1, seq = -1;
+        if (threadIdx.x < rows) {
+            pos = __ldg(a.row_pos + r0 + threadIdx.x);
+            seq = __ldg(a.row_batch + r0 + threadIdx.x);
         }
-        const int64_t dst_row = ((int64_t)page * a.n_kv_heads + head) * a.page_size + (pos - pi * a.page_size);
-        const int64_t src = row * (is_v ? a.ld_v : a.ld_k) + head * D + sub * 8;
-        uint4 lo, hi;
-        if (F32_IN) {
-            const uint4* s = (const uint4*)((const float*)(is_v ? a.v : a.k) + src);
-            lo = __ldg(s);
-            hi = __ldg(s + 1);
-        } else {
-            lo = __ldg((const uint4*)((const __nv_bfloat16*)(is_v ? a.v : a.k) + src));
-            hi = lo;
-        }
-        void* cache = is_v ? a.v_cache : a.k_cache;
-        if (FMT == DSA_FP32) {
-            uint4* d = (uint4*)((float*)cache + dst_row * D + sub * 8);
-            d[0] = lo;
-            d[1] = hi;
-        } else if (FMT == DSA_BF16 && !F32_IN) {
-            *(uint4*)((__nv_bfloat16*)cache + dst_row * D + sub * 8) = lo;
-        } else {
-            float x[8];
-            if (F32_IN) {
-                const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        for (int t0 = grp; t0 - grp < tasks; t0 += U * GROUPS) {        // (every group passes the barrier below)
+            // head innermost, then K / V, then row
+            uint4 x[U][W];
+            int rs[U], head[U];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(w[e]);
-            } else {
-                const uint32_t w[4] = {lo.x, lo.y, lo.z, lo.w};
+            for (int u = 0; u < U; ++u) {
+                const int t = t0 + u * GROUPS;
+                if (t >= tasks) continue;
+                rs[u] = a.by_head.div(t);
+                head[u] = t - rs[u] * a.n_kv_heads;
+                const int64_t src = (int64_t)(r0 + (rs[u] >> 1)) * ((rs[u] & 1) ? a.ld_v : a.ld_k) + head[u] * D + sub * 16;
+                const uint4* s = (const uint4*)((const char*)((rs[u] & 1) ? a.v : a.k) + src * (F32_IN ? 4 : 2));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[2 * e] = __uint_as_float(w[e] << 16);
-                    x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+                for (int i = 0; i < W; ++i) x[u][i] = __ldcs(s + i);
+            }
+            if (t0 == grp) {
+                if (threadIdx.x < rows) {
+                    int page = -1, slot = 0;
+                    if (pos >= 0) {                                     // (< 0: not stored)
+                        const int pi = a.by_page.div(pos);
+                        if (seq >= 0 && seq < a.batch && pi < a.max_pages)
+                            page = __ldg(a.page_table + (int64_t)seq * a.max_pages + pi);
+                        slot = pos - pi * a.page_size;
+                        if (page < 0 || page >= a.num_pages) {
+                            record_error(a.err, DEV_ERR_BAD_INDEX);
+                            page = -1;
+                        }
+                    }
+                    place[threadIdx.x] = make_int2(page, slot);
+                }
+                __syncthreads();
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (t0 + u * GROUPS >= tasks) continue;
+                const bool is_v = rs[u] & 1;
+                const int2 at = place[rs[u] >> 1];
+                if (at.x < 0) continue;
+                const int64_t dst_row = ((int64_t)at.x * a.n_kv_heads + head[u]) * a.page_size + at.y;
+                constexpr int ES = FMT == DSA_FP32 ? 4 : FMT == DSA_BF16 ? 2 : 1;
+                uint4* dst = (uint4*)((char*)(is_v ? a.v_cache : a.k_cache) + (dst_row * D + sub * 16) * ES);
+                if constexpr (FMT == DSA_FP32 || (FMT == DSA_BF16 && !F32_IN)) {
+#pragma unroll
+                    for (int i = 0; i < W; ++i) dst[i] = x[u][i];
+                } else {
+                    float f[16];
+#pragma unroll
+                    for (int i = 0; i < W; ++i) {
+                        const uint32_t w[4] = {x[u][i].x, x[u][i].y, x[u][i].z, x[u][i].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (F32_IN) {
+                                f[(4 * i + e) & 15] = __uint_as_float(w[e]);
+                            } else {
+                                f[(8 * i + 2 * e) & 15] = __uint_as_float(w[e] << 16);
+                                f[(8 * i + 2 * e + 1) & 15] = __uint_as_float(w[e] & 0xFFFF0000u);
+                            }
+                        }
+                    }
+                    if (FMT == DSA_BF16) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            dst[i] = make_uint4(bf16x2_bits(f[8 * i], f[8 * i + 1]), bf16x2_bits(f[8 * i + 2], f[8 * i + 3]),
+                                                bf16x2_bits(f[8 * i + 4], f[8 * i + 5]), bf16x2_bits(f[8 * i + 6], f[8 * i + 7]));
+                    } else {
+                        float amax = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(f[e]));
+#pragma unroll
+                        for (int m = LANES / 2; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(group, amax, m));
+                        const float sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+                        *dst = e4m3_codes(f, sc);
+                        if (sub == 0) (is_v ? a.v_scale : a.k_scale)[dst_row] = sc;
+                    }
                 }
             }
-            if (FMT == DSA_BF16) {
-                *(uint4*)((__nv_bfloat16*)cache + dst_row * D + sub * 8) =
-                    make_uint4(bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3]), bf16x2_bits(x[4], x[5]),
-                               bf16x2_bits(x[6], x[7]));
-            } else {
-                float amax = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
-#pragma unroll
-                for (int m = LANES / 2; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(group, amax, m));
-                const float sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = __fdiv_rn(x[e], sc);
-                *(uint2*)((uint8_t*)cache + dst_row * D + sub * 8) =
-                    make_uint2(e4m3x2(x[0], x[1]) | (e4m3x2(x[2], x[3]) << 16),
-                               e4m3x2(x[4], x[5]) | (e4m3x2(x[6], x[7]) << 16));
-                if (sub == 0) (is_v ? a.v_scale : a.k_scale)[dst_row] = sc;
-            }
         }
+        __syncthreads();            // the places are read before the next run's are written
     }
 }
 
@@ -593,9 +645,8 @@ cudaError_t launch_copies(const Launch& L, const CacheList& l, const int32_t* sr
 }  // namespace
 
 cudaError_t launch_kv_append(const Launch& L, const AppendArgs& a, dsa_dtype_t in, dsa_dtype_t fmt, int head_dim) {
-    const int64_t threads = (int64_t)a.n * 2 * a.n_kv_heads * (head_dim / 8);
-    const int64_t want = (threads + 255) / 256;
-    const int grid = (int)(want < (int64_t)L.num_sms * 16 ? want : (int64_t)L.num_sms * 16);
+    // four blocks per SM (two rounds of them for long lists), one row each while that lasts
+    const int grid = a.n < L.num_sms * 8 ? a.n : L.num_sms * 8;
     const bool f32 = in == DSA_FP32;
     void (*k)(AppendArgs);
 #define DSA_APPEND(D)                                                                              \

@@ -98,6 +98,7 @@ struct AppendArgs {
     void* v_cache;
     float* k_scale;             // [num_pages, n_kv_heads, page_size] (fp8)
     float* v_scale;
+    FastDiv by_page, by_head;   // by page_size, n_kv_heads
     unsigned* err;
 };
 cudaError_t launch_kv_append(const Launch& L, const AppendArgs& a, dsa_dtype_t in, dsa_dtype_t fmt, int head_dim);
@@ -159,7 +160,7 @@ struct DecodeArgs {
     const int32_t* row_batch;
     const int32_t* row_pos;
     int rows, n_heads, n_kv_heads;
-    uint32_t page_mul, page_shift;      // s / page_size = (s * page_mul) >> page_shift for 0 <= s < 2^31
+    FastDiv by_page;            // by page_size
     float scale_log2;
     void* out;                  // [rows, n_heads, head_dim]
     float* lse;                 // [rows, n_heads]
