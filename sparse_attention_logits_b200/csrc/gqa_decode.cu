@@ -149,201 +149,41 @@ template <int KT> __device__ __forceinline__ int cache_row(const DecodeArgs& a, 
     return (page * a.n_kv_heads + w.kvh) * a.page_size + (s - pi * a.page_size);
 }
 
-// ------------------------------------------------------------ CUDA cores --
+// ------------------------------------------------------------ the kernel --
 //
-// fp32 caches.  A warp takes 4 keys at a
-// time for 8 heads: every lane holds D/32 dims of the queries, keys and
-// outputs, the 32 partial dot products per lane are summed over the lanes by
-// one transposing butterfly (31 shuffles for 32 sums), after which lane l
-// holds the score of key l / 8 and head l % 8.
-template <int VEC> __device__ __forceinline__ void load_vec(const float* p, float (&x)[VEC]);
-template <> __device__ __forceinline__ void load_vec<4>(const float* p, float (&x)[4]) {
-    const float4 v = __ldg((const float4*)p);
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-}
-template <> __device__ __forceinline__ void load_vec<2>(const float* p, float (&x)[2]) {
-    const float2 v = __ldg((const float2*)p);
-    x[0] = v.x; x[1] = v.y;
-}
-
-template <int D>
-__global__ void __launch_bounds__(THREADS) gqa_decode_simt_kernel(const DecodeArgs a, const Parts parts) {
-    pdl_wait();
-    pdl_launch_dependents();
-    constexpr int GT = 8, VEC = D / 32, KT = 64, WK = KT / WARPS;
-    __shared__ LocateShared sh;
-    __shared__ float s_o[WARPS][GT][D];
-    __shared__ float s_m[WARPS][GT], s_l[WARPS][GT];
-    const int group = a.n_heads / a.n_kv_heads, tiles = ceil_div(group, GT);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    Walk<KT> w;
-    int64_t begin, end, stretch;
-    locate<KT>(a, tiles, 2, sh, w, begin, end, stretch);
-    const float* kc = (const float*)a.k_cache;
-    const float* vc = (const float*)a.v_cache;
-    for (int64_t at = begin; at < end;) {
-        const int h0 = w.kvh * group + w.tile * GT, heads = min(GT, group - w.tile * GT);
-        const int n = (int)min((int64_t)(w.units - w.unit), end - at);
-        if (w.unit == 0 && w.kvh == 0 && w.tile == 0 && tid == 0) {
-            // reported once per row, by the block that begins it
-            const int b = w.batch;
-            if (b < 0 || b >= a.batch || __ldg(a.row_pos + w.row) >= (int64_t)a.max_pages * a.page_size)
-                record_error(a.err, DEV_ERR_BAD_INDEX);
-        }
-        float q[GT][VEC], acc[GT][VEC];
-#pragma unroll
-        for (int h = 0; h < GT; ++h) {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                q[h][v] = h < heads ? ((const float*)a.q)[(int64_t)w.row * a.ld_q + (h0 + h) * D + lane * VEC + v] * a.scale_log2 : 0.f;
-                acc[h][v] = 0.f;
-            }
-        }
-        float m = -INFINITY, l = 0.f;       // of head lane % 8
-        for (int u = w.unit; u < w.unit + n; ++u) {
-            const int s0 = u * KT + warp * WK;
-            const int my_row = lane < WK ? cache_row<KT>(a, w, s0 + lane) : -1;
-#pragma unroll 1
-            for (int k0 = 0; k0 < WK; k0 += 4) {
-                float kx[4][VEC], vx[4][VEC];
-                int row[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    row[k] = __shfl_sync(0xffffffffu, my_row, k0 + k);
-                    if (row[k] >= 0) {
-                        load_vec<VEC>(kc + (int64_t)row[k] * D + lane * VEC, kx[k]);
-                        load_vec<VEC>(vc + (int64_t)row[k] * D + lane * VEC, vx[k]);
-                    } else {
-#pragma unroll
-                        for (int v = 0; v < VEC; ++v) kx[k][v] = vx[k][v] = 0.f;
-                    }
-                }
-                if (row[0] < 0 && row[1] < 0 && row[2] < 0 && row[3] < 0) continue;
-                const int mine = lane >> 3;
-                const int mrow = mine == 0 ? row[0] : mine == 1 ? row[1] : mine == 2 ? row[2] : row[3];
-                float s[32];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int h = 0; h < GT; ++h) {
-                        float d = q[h][0] * kx[k][0];
-#pragma unroll
-                        for (int v = 1; v < VEC; ++v) d = fmaf(q[h][v], kx[k][v], d);
-                        s[k * GT + h] = d;
-                    }
-#pragma unroll
-                for (int half = 16; half > 0; half >>= 1) {
-                    const bool up = lane & half;
-#pragma unroll
-                    for (int i = 0; i < half; ++i) {
-                        const float give = up ? s[i] : s[i + half];
-                        const float keep = up ? s[i + half] : s[i];
-                        s[i] = keep + __shfl_xor_sync(0xffffffffu, give, half);
-                    }
-                }
-                const float z = mrow >= 0 ? s[0] : -INFINITY;
-                float top = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 8));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                const float m_new = fmaxf(m, top);
-                if (__any_sync(0xffffffffu, m_new > m)) {
-                    const float f = m_new > m ? fast_exp2(m - m_new) : 1.f;
-                    l *= f;
-                    m = m_new;
-#pragma unroll
-                    for (int h = 0; h < GT; ++h) {
-                        const float fh = __shfl_sync(0xffffffffu, f, h);
-#pragma unroll
-                        for (int v = 0; v < VEC; ++v) acc[h][v] *= fh;
-                    }
-                }
-                const float p = mrow >= 0 && m > -INFINITY ? fast_exp2(z - m) : 0.f;
-                l += p;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int h = 0; h < GT; ++h) {
-                        const float ph = __shfl_sync(0xffffffffu, p, k * GT + h);
-#pragma unroll
-                        for (int v = 0; v < VEC; ++v) acc[h][v] = fmaf(ph, vx[k][v], acc[h][v]);
-                    }
-            }
-        }
-        l += __shfl_xor_sync(0xffffffffu, l, 8);
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        // the four warps' shares of the pair
-        if (lane < GT) {
-            s_m[warp][lane] = m;
-            s_l[warp][lane] = l;
-        }
-#pragma unroll
-        for (int h = 0; h < GT; ++h)
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) s_o[warp][h][lane * VEC + v] = acc[h][v];
-        __syncthreads();
-        const bool begins = w.unit == 0, ends = w.unit + n == w.units;
-        const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
-        for (int h = warp; h < heads; h += WARPS) {
-            float mm = -INFINITY, ll = 0.f;
-#pragma unroll
-            for (int i = 0; i < WARPS; ++i) mm = fmaxf(mm, s_m[i][h]);
-            float o[VEC];
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) o[v] = 0.f;
-#pragma unroll
-            for (int i = 0; i < WARPS; ++i) {
-                const float f = mm == -INFINITY ? 0.f : fast_exp2(s_m[i][h] - mm);
-                ll += f * s_l[i][h];
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) o[v] = fmaf(f, s_o[i][h][lane * VEC + v], o[v]);
-            }
-            if (begins && ends) {
-                const float inv = ll == 0.f ? 0.f : 1.f / ll;
-                float* out = (float*)a.out + ((int64_t)w.row * a.n_heads + h0 + h) * D + lane * VEC;
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) out[v] = o[v] * inv;
-                if (lane == 0)
-                    a.lse[(int64_t)w.row * a.n_heads + h0 + h] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * LN2;
-            } else {
-                float* po = parts.o + ((int64_t)slot * GT + h) * D + lane * VEC;
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) po[v] = o[v];
-                if (lane == 0) parts.ml[slot * GT + h] = make_float2(mm, ll);
-            }
-        }
-        if (begins && tid == 0) {
-            const int64_t last = (at + w.units - 1) / stretch;      // block of the pair's last unit
-            parts.meta[((int64_t)w.row * a.n_kv_heads + w.kvh) * tiles + w.tile] = make_int2(blockIdx.x, (int)(last - blockIdx.x) + 1);
-        }
-        __syncthreads();
-        at += n;
-        w.unit += n - 1;
-        w.next(a, tiles);
-    }
-}
-
-// ---------------------------------------------------------- tensor cores --
+// The work is bound by the cache's bytes, so the kernel is built around its
+// loads: each warp owns 16 (fp8: 32) keys of a unit and streams their K and V
+// rows through a ring of its own (cp.async, 16 bytes per lane, rows of unused
+// places zero-filled), never waiting for another warp while a pair lasts.
+// With up to 16 heads of a group as the M of mma.m16n8, one slice costs a warp
+// a few dozen products and one softmax step in registers: a small part of an
+// SM's issue slots at the HBM rate, which is why the products need no more
+// than the warp-level tensor instruction (M = 128 of tcgen05 would be filled
+// to an eighth).  Groups of up to 8 heads leave rows 8-15 of the products
+// unused: they are fed zeros (fp32: see below).
 //
-// bf16 and fp8 caches.  The work is bound by the cache's bytes, so the kernel
-// is built around its loads: each warp owns 16 (fp8: 32) keys of a unit and streams
-// their K and V rows through a ring of its own (cp.async, 16 bytes per lane,
-// rows of unused places zero-filled), never waiting for another warp while a
-// pair lasts.  With up to 16 heads of a group as the M of mma.m16n8k16, one
-// slice costs a warp 2 D/16 + D/8 products and one softmax step in registers:
-// about a tenth of an SM's issue slots at the HBM rate, which is why the
-// products need no more than the warp-level tensor instruction (M = 128 of
-// tcgen05 would be filled to an eighth).
+// Which dims a k-step of the first product holds is free as long as Q and K
+// agree, and so is which dim a column of the output holds and which key a
+// k-step of the second product holds.  bf16 uses ldmatrix and the plain
+// order; fp8 and fp32 choose the orders so that a lane reads its keys as
+// 16-byte pieces.
 //
-// fp8: codes are widened to f16 (exact) on the way into the product.  Which 16
-// dims a k-step holds is free as long as Q and K agree, and which d a column
-// of the output holds is free altogether; both are chosen so that a lane
-// reads its keys as 16-byte (V, D = 64: 8-byte) pieces.  The query row is
-// first brought to [1, 2) by a power of two, so that f16 holds it (a value
-// below 2^-14 of the row's largest loses bits below 2^-25 of it); P is taken
-// times the value scale relative to the largest scale met so far, which the
-// output carries like the running maximum.
-template <typename KV> struct MmaCfg;
-template <> struct MmaCfg<__nv_bfloat16> { static constexpr int WK = 16, STAGES = 3, BLOCKS = 2; };
-template <> struct MmaCfg<__nv_fp8_e4m3> { static constexpr int WK = 32, STAGES = 2, BLOCKS = 3; };
+// fp8: codes are widened to f16 (exact) on the way into the product.  The
+// query row is first brought to [1, 2) by a power of two, so that f16 holds
+// it (a value below 2^-14 of the row's largest loses bits below 2^-25 of it);
+// P is taken times the value scale relative to the largest scale met so far,
+// which the output carries like the running maximum.
+//
+// fp32: every factor is split into two tf32 numbers, x = hi + lo.  The unused
+// half of the product's rows takes the lo parts of the eight heads, so two
+// tensor products (with the keys' hi and lo parts) give all four partial
+// products.  What rounding lo loses is at most 2^-22 of a factor, no more than
+// a dot product of a few fp32 terms; the multiply-adds on the CUDA cores would
+// take three times the instructions.
+template <typename KV, int D> struct MmaCfg;
+template <int D> struct MmaCfg<__nv_bfloat16, D> { static constexpr int WK = 16, STAGES = 3, BLOCKS = 2; };
+template <int D> struct MmaCfg<__nv_fp8_e4m3, D> { static constexpr int WK = 32, STAGES = 2, BLOCKS = 3; };
+template <int D> struct MmaCfg<float, D> { static constexpr int WK = 16, STAGES = D == 64 ? 3 : 2, BLOCKS = D == 64 ? 2 : 1; };
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -364,6 +204,30 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+
+// tf32 parts of an fp32 number: hi = x rounded to 11 bits, lo = x - hi, each
+// as the tensor core reads it (it ignores the low 13 bits).
+__device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
+}
+// C += A B on tf32: lane (r4, c4) gives A's rows r4 and r4 + 8 at k = c4 (a[0],
+// a[1]) and c4 + 4 (a[2], a[3]), and B's column r4 at k = c4 and c4 + 4.
+__device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// fp32 product of eight rows: A holds their hi parts in rows 0-7 and their lo
+// parts in rows 8-15, so the sum of C's halves is the product's.
+__device__ __forceinline__ void mma_split(float (&c)[4], const uint32_t (&a)[4], float b0, float b1) {
+    uint32_t h0, l0, h1, l1;
+    split(b0, h0, l0);
+    split(b1, h1, l1);
+    mma1688(c, a, l0, l1);
+    mma1688(c, a, h0, h1);
+}
+
 template <bool F16> __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     uint32_t r;
     if (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -382,10 +246,15 @@ __device__ __forceinline__ void cp_async_4(void* dst, const void* src, uint32_t 
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Shared-memory place of 16-byte piece c of key r, within a slice of 16 rows
-// of RB bytes (swizzled so that the reads below meet no bank twice).
-template <bool FP8, int RB, bool IS_V> __device__ __forceinline__ uint32_t piece_at(int r, int c) {
-    if (!FP8) return r * RB + ((c ^ (r & 7)) << 4);
+// Shared-memory place of 16-byte piece c of key r, within a slice of rows of RB
+// bytes (swizzled so that the kernel's reads meet no bank twice).
+template <int ES, int RB, bool IS_V> __device__ __forceinline__ uint32_t piece_at(int r, int c) {
+    if (ES == 2) return r * RB + ((c ^ (r & 7)) << 4);
+    if (ES == 4) {
+        const int f = (r >> 1) & 3;             // V: a read covers four even (or odd) keys and two runs of pieces
+        const int x = !IS_V ? (r & 1) << 2 : RB == 512 ? f : (f & 1) | ((f & 2) << 1);
+        return r * RB + ((c ^ x) << 4);
+    }
     if (IS_V) {                     // lines of 128 bytes
         const int lin = r * (RB / 16) + c;
         return (lin >> 3) * 128 + (((lin & 7) ^ (((r >> 1) & 3) << 1)) << 4);
@@ -401,19 +270,21 @@ template <int D> __device__ __forceinline__ int exch_at(int r, int d) {
 }
 
 template <typename KV, int D, int GT>
-__global__ void __launch_bounds__(THREADS, MmaCfg<KV>::BLOCKS) gqa_decode_mma_kernel(const DecodeArgs a, const Parts parts) {
+__global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_kernel(const DecodeArgs a, const Parts parts) {
     pdl_wait();
     pdl_launch_dependents();
-    constexpr bool FP8 = sizeof(KV) == 1;
-    constexpr int WK = MmaCfg<KV>::WK, KT = WK * WARPS;     // keys of a warp's slice, and of a unit
-    constexpr int RB = D * (int)sizeof(KV);         // bytes of a row
+    constexpr int ES = (int)sizeof(KV);
+    constexpr bool FP8 = ES == 1, FP32 = ES == 4;
+    constexpr int WK = MmaCfg<KV, D>::WK, KT = WK * WARPS;  // keys of a warp's slice, and of a unit
+    constexpr int RB = D * ES;                      // bytes of a row
     constexpr int PIECES = RB / 16;
     constexpr int SLICE = WK * RB;                  // K (or V) bytes of a warp's slice
-    constexpr int STAGES = MmaCfg<KV>::STAGES;
+    constexpr int STAGES = MmaCfg<KV, D>::STAGES;
     constexpr uint32_t ALL = WK == 32 ? 0xffffffffu : 0xffffu;
     constexpr int SLOT = 2 * SLICE + (FP8 ? 2 * WK * 4 : 0) + 16;   // K, V, scales, the mask of valid keys
     constexpr int KS = D / 16, NT = D / 8;
     static_assert(!FP8 || WK == 32, "a lane per key's scales");
+    static_assert(!FP32 || GT == 8, "fp32 takes eight heads");
     static_assert(2 * SLICE >= 8 * D * 4, "the outputs of 8 heads are exchanged in a slot");
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ LocateShared sh;
@@ -446,8 +317,8 @@ __global__ void __launch_bounds__(THREADS, MmaCfg<KV>::BLOCKS) gqa_decode_mma_ke
                 const int from = __shfl_sync(0xffffffffu, row, r);
                 const int64_t off = from >= 0 ? (int64_t)from * RB + c * 16 : 0;
                 const uint32_t n = from >= 0 ? 16u : 0u;
-                cp_async_16(slot + piece_at<FP8, RB, false>(r, c), kc + off, n);
-                cp_async_16(slot + SLICE + piece_at<FP8, RB, true>(r, c), vc + off, n);
+                cp_async_16(slot + piece_at<ES, RB, false>(r, c), kc + off, n);
+                cp_async_16(slot + SLICE + piece_at<ES, RB, true>(r, c), vc + off, n);
             }
             if (FP8) {
                 cp_async_4(slot + 2 * SLICE + lane * 4, a.k_scale + (row >= 0 ? row : 0), row >= 0 ? 4u : 0u);
@@ -473,15 +344,29 @@ __global__ void __launch_bounds__(THREADS, MmaCfg<KV>::BLOCKS) gqa_decode_mma_ke
             record_error(a.err, DEV_ERR_BAD_INDEX);     // reported once per row, by the block that begins it
         // Q fragments: rows r4 and r4 + 8 (heads); k-step kk holds dims
         // 16 kk + {2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9} (bf16), or
-        // 64 (kk / 4) + 16 c4 + 4 (kk % 4) + {0, 1, 2, 3} (fp8)
+        // 64 (kk / 4) + 16 c4 + 4 (kk % 4) + {0, 1, 2, 3} (fp8), or, as two
+        // k-steps of 8, 16 kk + 4 c4 + {0, 1} and {2, 3} (fp32)
         uint32_t qf[KS][4];
+        uint32_t q32[FP32 ? KS : 1][2][4];
         float zs[2] = {a.scale_log2, a.scale_log2};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const bool on = (half == 0 || GT > 8) && r4 + 8 * half < heads;
-            const __nv_bfloat16* q = (const __nv_bfloat16*)a.q + (int64_t)w.row * a.ld_q +
-                                     (h0 + (on ? r4 + 8 * half : 0)) * D;
-            if (!FP8) {
+            const int64_t at_q = (int64_t)w.row * a.ld_q + (h0 + (on ? r4 + 8 * half : 0)) * D;
+            const __nv_bfloat16* q = (const __nv_bfloat16*)a.q + at_q;
+            if constexpr (FP32) {
+                if (half == 0) {
+#pragma unroll
+                    for (int kk = 0; kk < KS; ++kk) {
+                        const float4 x = on ? __ldg((const float4*)((const float*)a.q + at_q + 16 * kk + 4 * c4))
+                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+                        split(x.x, q32[kk][0][0], q32[kk][0][1]);
+                        split(x.y, q32[kk][0][2], q32[kk][0][3]);
+                        split(x.z, q32[kk][1][0], q32[kk][1][1]);
+                        split(x.w, q32[kk][1][2], q32[kk][1][3]);
+                    }
+                }
+            } else if (!FP8) {
 #pragma unroll
                 for (int kk = 0; kk < KS; ++kk) {
                     qf[kk][half] = on ? __ldg((const uint32_t*)(q + 16 * kk + 2 * c4)) : 0u;
@@ -534,13 +419,27 @@ __global__ void __launch_bounds__(THREADS, MmaCfg<KV>::BLOCKS) gqa_decode_mma_ke
                 for (int t = 0; t < WK / 8; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
-                if (!FP8) {
+                if constexpr (FP32) {
+#pragma unroll
+                    for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+                        for (int t = 0; t < WK / 8; ++t) {
+                            const uint4 x = ld_shared_v4(slot + piece_at<ES, RB, false>(t * 8 + r4, 4 * kk + c4));
+                            mma_split(s[t], q32[kk][0], __uint_as_float(x.x), __uint_as_float(x.y));
+                            mma_split(s[t], q32[kk][1], __uint_as_float(x.z), __uint_as_float(x.w));
+                        }
+#pragma unroll
+                    for (int t = 0; t < WK / 8; ++t) {
+                        s[t][0] += s[t][2];
+                        s[t][1] += s[t][3];
+                    }
+                } else if (!FP8) {
 #pragma unroll
                     for (int kk = 0; kk < KS; ++kk)
 #pragma unroll
                         for (int t = 0; t < WK / 8; t += 2) {
                             uint32_t b[4];
-                            ldmatrix_x4(b, kb + piece_at<FP8, RB, false>(t * 8 + (lane >> 4) * 8 + (lane & 7),
+                            ldmatrix_x4(b, kb + piece_at<ES, RB, false>(t * 8 + (lane >> 4) * 8 + (lane & 7),
                                                                          kk * 2 + ((lane >> 3) & 1)));
                             mma16816<FP8>(s[t], qf[kk], b[0], b[1]);
                             mma16816<FP8>(s[t + 1], qf[kk], b[2], b[3]);
@@ -550,7 +449,7 @@ __global__ void __launch_bounds__(THREADS, MmaCfg<KV>::BLOCKS) gqa_decode_mma_ke
                     for (int i = 0; i < D / 64; ++i)
 #pragma unroll
                         for (int t = 0; t < WK / 8; ++t) {
-                            const uint4 x = ld_shared_v4(slot + piece_at<FP8, RB, false>(t * 8 + r4, 4 * i + c4));
+                            const uint4 x = ld_shared_v4(slot + piece_at<ES, RB, false>(t * 8 + r4, 4 * i + c4));
                             const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
@@ -611,10 +510,12 @@ __global__ void __launch_bounds__(THREADS, MmaCfg<KV>::BLOCKS) gqa_decode_mma_ke
                     for (int t = 0; t < NT; ++t) {
                         o[t][0] *= f[0] * vmove; o[t][1] *= f[0] * vmove;
                         if (GT > 8) { o[t][2] *= f[1] * vmove; o[t][3] *= f[1] * vmove; }
+                        if (FP32) { o[t][2] *= f[0]; o[t][3] *= f[0]; }
                     }
                 }
                 // P (as the A operand, 16 keys a piece), and O += P V
                 uint32_t pf[WK / 16][4];
+                uint32_t p32[FP32 ? WK / 8 : 1][4];     // keys 8 t + 2 c4 + {0, 1}
 #pragma unroll
                 for (int t = 0; t < WK / 8; ++t) {
                     pf[t / 2][2 * (t & 1) + 1] = 0u;
@@ -628,16 +529,35 @@ __global__ void __launch_bounds__(THREADS, MmaCfg<KV>::BLOCKS) gqa_decode_mma_ke
                             p0 *= vs2[t].x * vinv;
                             p1 *= vs2[t].y * vinv;
                         }
-                        pf[t / 2][half + 2 * (t & 1)] = pack2<FP8>(p0, p1);
+                        if constexpr (FP32) {
+                            split(p0, p32[t][0], p32[t][1]);
+                            split(p1, p32[t][2], p32[t][3]);
+                        } else {
+                            pf[t / 2][half + 2 * (t & 1)] = pack2<FP8>(p0, p1);
+                        }
                     }
                 }
 #pragma unroll
                 for (int k16 = 0; k16 < WK / 16; ++k16) {
-                    if (!FP8) {
+                    if constexpr (FP32) {
+                        // column r4 of tile j is dim (D / 8) r4 + j
+                        constexpr int RUN = D / 8;
+#pragma unroll
+                        for (int t = 2 * k16; t < 2 * k16 + 2; ++t)
+#pragma unroll
+                            for (int i = 0; i < RUN / 4; ++i) {
+                                const uint4 x = ld_shared_v4(slot + SLICE + piece_at<ES, RB, true>(8 * t + 2 * c4, r4 * RUN / 4 + i));
+                                const uint4 y = ld_shared_v4(slot + SLICE + piece_at<ES, RB, true>(8 * t + 2 * c4 + 1, r4 * RUN / 4 + i));
+                                mma_split(o[4 * i], p32[t], __uint_as_float(x.x), __uint_as_float(y.x));
+                                mma_split(o[4 * i + 1], p32[t], __uint_as_float(x.y), __uint_as_float(y.y));
+                                mma_split(o[4 * i + 2], p32[t], __uint_as_float(x.z), __uint_as_float(y.z));
+                                mma_split(o[4 * i + 3], p32[t], __uint_as_float(x.w), __uint_as_float(y.w));
+                            }
+                    } else if (!FP8) {
 #pragma unroll
                         for (int t = 0; t < NT; t += 2) {
                             uint32_t b[4];
-                            ldmatrix_x4_t(b, vb + piece_at<FP8, RB, true>(k16 * 16 + ((lane >> 3) & 1) * 8 + (lane & 7),
+                            ldmatrix_x4_t(b, vb + piece_at<ES, RB, true>(k16 * 16 + ((lane >> 3) & 1) * 8 + (lane & 7),
                                                                           t + (lane >> 4)));
                             mma16816<FP8>(o[t], pf[k16], b[0], b[1]);
                             mma16816<FP8>(o[t + 1], pf[k16], b[2], b[3]);
@@ -649,7 +569,7 @@ __global__ void __launch_bounds__(THREADS, MmaCfg<KV>::BLOCKS) gqa_decode_mma_ke
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int key = k16 * 16 + 2 * c4 + (k & 1) + 8 * (k >> 1);
-                            const uint8_t* src = slot + SLICE + piece_at<FP8, RB, true>(key, r4 * RUN / 16) + (r4 * RUN) % 16;
+                            const uint8_t* src = slot + SLICE + piece_at<ES, RB, true>(key, r4 * RUN / 16) + (r4 * RUN) % 16;
                             if (RUN == 16) {
                                 const uint4 v = ld_shared_v4(src);
                                 x[k][0] = v.x; x[k][1] = v.y; x[k][RUN / 4 - 2] = v.z; x[k][RUN / 4 - 1] = v.w;
@@ -688,11 +608,18 @@ __global__ void __launch_bounds__(THREADS, MmaCfg<KV>::BLOCKS) gqa_decode_mma_ke
         const int place = 2 * blockIdx.x + (begins ? 1 : 0);
         const float carry = FP8 ? vref : 1.f;
         float* mine = (float*)(ring + st * SLOT);
+        if (FP32) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                o[t][0] += o[t][2];
+                o[t][1] += o[t][3];
+            }
+        }
 #pragma unroll
         for (int half = 0; half < (GT > 8 ? 2 : 1); ++half) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                if (!FP8) {
+                if (ES == 2) {
                     *(float2*)(mine + exch_at<D>(r4, 8 * t + 2 * c4)) = make_float2(o[t][2 * half], o[t][2 * half + 1]);
                 } else if ((t & 3) == 0) {
 #pragma unroll
@@ -723,10 +650,12 @@ __global__ void __launch_bounds__(THREADS, MmaCfg<KV>::BLOCKS) gqa_decode_mma_ke
                 }
                 if (begins && ends) {
                     const float inv = ll == 0.f ? 0.f : 1.f / ll;
-                    __nv_bfloat16* out = (__nv_bfloat16*)a.out + ((int64_t)w.row * a.n_heads + h0 + h) * D + lane * VEC;
+                    const int64_t to = ((int64_t)w.row * a.n_heads + h0 + h) * D + lane * VEC;
 #pragma unroll
-                    for (int v = 0; v < VEC; v += 2)
-                        *(uint32_t*)(out + v) = pack2<false>(acc[v] * inv, acc[v + 1] * inv);
+                    for (int v = 0; v < VEC; v += 2) {
+                        if (FP32) *(float2*)((float*)a.out + to + v) = make_float2(acc[v] * inv, acc[v + 1] * inv);
+                        else *(uint32_t*)((__nv_bfloat16*)a.out + to + v) = pack2<false>(acc[v] * inv, acc[v + 1] * inv);
+                    }
                     if (lane == 0)
                         a.lse[(int64_t)w.row * a.n_heads + h0 + h] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * LN2;
                 } else {
@@ -796,11 +725,14 @@ __global__ void __launch_bounds__(128) gqa_combine_kernel(const DecodeArgs a, co
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Heads per pair: 8 on the CUDA cores; on the tensor cores as many rows of
-// the product as the group fills (16, or 8 when the upper half would be idle).
+// Heads per pair: as many rows of the product as the group fills (16, or 8
+// when the upper half would be idle); 8 in fp32, whose split queries fill the
+// registers.
 int head_tile(dsa_dtype_t kv, int group) { return kv == DSA_FP32 || group <= 8 ? 8 : 16; }
-int blocks_per_sm(dsa_dtype_t kv) {
-    return kv == DSA_FP32 ? 4 : kv == DSA_BF16 ? MmaCfg<__nv_bfloat16>::BLOCKS : MmaCfg<__nv_fp8_e4m3>::BLOCKS;
+int blocks_per_sm(dsa_dtype_t kv, int d) {
+    return kv == DSA_FP32   ? (d == 64 ? MmaCfg<float, 64>::BLOCKS : MmaCfg<float, 128>::BLOCKS)
+           : kv == DSA_BF16 ? MmaCfg<__nv_bfloat16, 128>::BLOCKS
+                            : MmaCfg<__nv_fp8_e4m3, 128>::BLOCKS;
 }
 
 template <typename Q, int D, int GT, class Kern>
@@ -830,42 +762,43 @@ cudaError_t launch_decode(const Launch& L, const DecodeArgs& a, Kern kern, int s
     return e;
 }
 
-template <typename KV, int D>
-cudaError_t launch_mma(const Launch& L, const DecodeArgs& a, void* workspace) {
+template <typename Q, typename KV, int D>
+cudaError_t launch_typed(const Launch& L, const DecodeArgs& a, void* workspace) {
     constexpr bool FP8 = sizeof(KV) == 1;
-    constexpr int WK = MmaCfg<KV>::WK, slot = 2 * WK * D * (int)sizeof(KV) + (FP8 ? 2 * WK * 4 : 0) + 16;
-    constexpr int smem = WARPS * MmaCfg<KV>::STAGES * slot, per_sm = MmaCfg<KV>::BLOCKS;
-    static std::atomic<int> done8[kMaxDevices], done16[kMaxDevices];
-    if (a.n_heads / a.n_kv_heads <= 8) {
-        const cudaError_t e = allow_smem(done8, gqa_decode_mma_kernel<KV, D, 8>, smem);
-        if (e != cudaSuccess) return e;
-        return launch_decode<__nv_bfloat16, D, 8>(L, a, gqa_decode_mma_kernel<KV, D, 8>, smem, per_sm, workspace);
+    constexpr int WK = MmaCfg<KV, D>::WK, slot = 2 * WK * D * (int)sizeof(KV) + (FP8 ? 2 * WK * 4 : 0) + 16;
+    constexpr int smem = WARPS * MmaCfg<KV, D>::STAGES * slot, per_sm = MmaCfg<KV, D>::BLOCKS;
+    static std::atomic<int> done8[kMaxDevices];
+    [[maybe_unused]] static std::atomic<int> done16[kMaxDevices];
+    cudaError_t e;
+    if constexpr (sizeof(KV) != 4) {
+        if (a.n_heads / a.n_kv_heads > 8) {
+            e = allow_smem(done16, gqa_decode_kernel<KV, D, 16>, smem);
+            if (e != cudaSuccess) return e;
+            return launch_decode<Q, D, 16>(L, a, gqa_decode_kernel<KV, D, 16>, smem, per_sm, workspace);
+        }
     }
-    const cudaError_t e = allow_smem(done16, gqa_decode_mma_kernel<KV, D, 16>, smem);
+    e = allow_smem(done8, gqa_decode_kernel<KV, D, 8>, smem);
     if (e != cudaSuccess) return e;
-    return launch_decode<__nv_bfloat16, D, 16>(L, a, gqa_decode_mma_kernel<KV, D, 16>, smem, per_sm, workspace);
+    return launch_decode<Q, D, 8>(L, a, gqa_decode_kernel<KV, D, 8>, smem, per_sm, workspace);
 }
 
 }  // namespace
 
 size_t gqa_decode_workspace_bytes(int rows, int n_heads, int n_kv_heads, int head_dim, dsa_dtype_t kv, int num_sms) {
     const int group = n_heads / n_kv_heads;
-    const size_t grid = (size_t)num_sms * blocks_per_sm(kv), gt = head_tile(kv, group);
+    const size_t grid = (size_t)num_sms * blocks_per_sm(kv, head_dim), gt = head_tile(kv, group);
     const size_t pairs = (size_t)rows * n_kv_heads * ceil_div(group, (int)gt);
     return up256(2 * grid * gt * head_dim * 4) + up256(2 * grid * gt * 8) + pairs * 8;
 }
 
 cudaError_t launch_gqa_decode(const Launch& L, const DecodeArgs& a, dsa_dtype_t kv, int head_dim, void* workspace) {
-    const int per_sm = blocks_per_sm(DSA_FP32);
+    typedef __nv_bfloat16 bf16;
     if (kv == DSA_FP32)
-        return head_dim == 64
-                   ? launch_decode<float, 64, 8>(L, a, gqa_decode_simt_kernel<64>, 0, per_sm, workspace)
-                   : launch_decode<float, 128, 8>(L, a, gqa_decode_simt_kernel<128>, 0, per_sm, workspace);
+        return head_dim == 64 ? launch_typed<float, float, 64>(L, a, workspace) : launch_typed<float, float, 128>(L, a, workspace);
     if (kv == DSA_BF16)
-        return head_dim == 64 ? launch_mma<__nv_bfloat16, 64>(L, a, workspace)
-                              : launch_mma<__nv_bfloat16, 128>(L, a, workspace);
-    return head_dim == 64 ? launch_mma<__nv_fp8_e4m3, 64>(L, a, workspace)
-                          : launch_mma<__nv_fp8_e4m3, 128>(L, a, workspace);
+        return head_dim == 64 ? launch_typed<bf16, bf16, 64>(L, a, workspace) : launch_typed<bf16, bf16, 128>(L, a, workspace);
+    return head_dim == 64 ? launch_typed<bf16, __nv_fp8_e4m3, 64>(L, a, workspace)
+                          : launch_typed<bf16, __nv_fp8_e4m3, 128>(L, a, workspace);
 }
 
 }  // namespace dsa
