@@ -51,7 +51,7 @@ template <int D> struct Cfg {
 
 template <int STAGES> struct Bars {
     uint64_t q_full, q_empty, kv_full[STAGES], kv_empty[STAGES];
-    uint64_t s_full[2], p_ready[2], o_final[2], to_zero, zeroed;
+    uint64_t s_full[2], p_ready[2][2], o_final[2], to_zero, zeroed;
     uint32_t tmem;
     int abort;
 };
@@ -154,6 +154,29 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -241,7 +264,8 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prompt_tc_kernel(const __grid_
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bars->s_full[t], 1);
-            mbar_init(&bars->p_ready[t], 4);
+            mbar_init(&bars->p_ready[t][0], 4);
+            mbar_init(&bars->p_ready[t][1], 4);
             mbar_init(&bars->o_final[t], 1);
         }
         mbar_init(&bars->to_zero, 1);
@@ -285,28 +309,37 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prompt_tc_kernel(const __grid_
                 ++n_s;
                 tc_fence_after();
                 float s[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(s_col + c * 32, s[c]);
+                tmem_ld32(s_col, s[0]);
+                tmem_ld32(s_col + 32, s[1]);
                 tmem_ld_wait();
-                if (j == n - 1) {                                   // the diagonal tile: keys up to the row's own
+                tmem_ld32(s_col + 64, s[2]);                        // (these arrive under the first half's maximum)
+                tmem_ld32(s_col + 96, s[3]);
+                float mx[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                for (int half = 0; half < 2; ++half) {
+                    if (half) tmem_ld_wait();
+                    if (j == n - 1) {                               // the diagonal tile: keys up to the row's own
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (c * 32 + e > r) s[c][e] = -INFINITY;
+                        for (int c = 2 * half; c < 2 * half + 2; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (c * 32 + e > r) s[c][e] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float* x = s[2 * half + (i >> 1)] + (i & 1) * 16;
+                        if (half) mx[i] = max3(mx[i], x[0], x[1]);
+                        else mx[i] = fmaxf(x[0], x[1]);
+                    }
+#pragma unroll
+                    for (int e = 2; e < 16; e += 2)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float* x = s[2 * half + (i >> 1)] + (i & 1) * 16 + e;
+                            mx[i] = max3(mx[i], x[0], x[1]);
+                        }
                 }
-                float mx[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) mx[i] = fmaxf(s[i >> 1][(i & 1) * 16], s[i >> 1][(i & 1) * 16 + 1]);
-#pragma unroll
-                for (int e = 2; e < 16; ++e)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) mx[i] = fmaxf(mx[i], s[i >> 1][(i & 1) * 16 + e]);
-#pragma unroll
-                for (int d = 4; d > 0; d >>= 1)
-#pragma unroll
-                    for (int i = 0; i < d; ++i) mx[i] = fmaxf(mx[i], mx[i + d]);
-                const float top = mx[0] * a.scale_log2;
+                const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale_log2;
                 bool move = false;
                 float f = 1.f;
                 if (top > m + RESCALE_LOG2 || (m == -INFINITY && top > m)) {
@@ -327,24 +360,29 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prompt_tc_kernel(const __grid_
                     }
                 }
                 const float base = m == -INFINITY ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), neg = make_float2(-base, -base);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float p0 = fast_exp2(fmaf(s[c][2 * e], a.scale_log2, -base));
-                        const float p1 = fast_exp2(fmaf(s[c][2 * e + 1], a.scale_log2, -base));
-                        sum[e & 3] += p0 + p1;
-                        pk[e] = bf16x2_bits(p0, p1);
+                        float2 x = fma2(make_float2(s[c][2 * e], s[c][2 * e + 1]), sc2, neg);
+                        x.x = fast_exp2(x.x);
+                        x.y = fast_exp2(x.y);
+                        sum[e & 1] = add2(sum[e & 1], x);
+                        pk[e] = bf16x2_bits(x.x, x.y);
                     }
                     tmem_st16(s_col + c * 16, pk);
+                    if (c & 1) {                                    // half of P: its products may begin
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars->p_ready[t][c >> 1]);
+                    }
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->p_ready[t]);
+                sum[0] = add2(sum[0], sum[1]);
+                l += sum[0].x + sum[0].y;
             }
             if (!ok) break;
             ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_final[t], n_o & 1, a.err, DEV_ERR_TIMEOUT_MMA, abort_flag));
@@ -415,15 +453,19 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prompt_tc_kernel(const __grid_
                         bool have_k = false;
                         for (int t = 0; t < 2 && ok; ++t) {
                             if (j >= w.n[t]) continue;
-                            ok = mbar_wait(&bars->p_ready[t], n_p[t] & 1, a.err, DEV_ERR_TIMEOUT_PEER, abort_flag);
-                            if (!ok) break;
-                            ++n_p[t];
-                            tc_fence_after();
                             const uint32_t va = kvb + (vslot % NS) * TILE;
 #pragma unroll
-                            for (int kk = 0; kk < BN / 16; ++kk)
-                                mma_ts(tmem + C::O_COL + t * D, tmem + t * 128 + kk * 8,
-                                       desc_sw128_mn(va + kk * 16 * 128, BLK, 1024), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+                            for (int half = 0; half < 2; ++half) {
+                                ok = ok && mbar_wait(&bars->p_ready[t][half], n_p[t] & 1, a.err, DEV_ERR_TIMEOUT_PEER, abort_flag);
+                                if (!ok) break;
+                                tc_fence_after();
+#pragma unroll
+                                for (int kk = half * (BN / 32); kk < (half + 1) * (BN / 32); ++kk)
+                                    mma_ts(tmem + C::O_COL + t * D, tmem + t * 128 + kk * 8,
+                                           desc_sw128_mn(va + kk * 16 * 128, BLK, 1024), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+                            }
+                            if (!ok) break;
+                            ++n_p[t];
                             if (j == w.n[t] - 1) mma_commit(&bars->o_final[t]);
                             if (t == last_now) mma_commit(&bars->kv_empty[vslot % NS]);
                             if (j + 1 < w.n[t]) {
