@@ -12,9 +12,19 @@
 //   O_t += P_t V       tcgen05 with P from tensor memory
 // The products alternate between the tiles (O_0, S_0', O_1, S_1'), so that
 // one tile's exponentials run under the other tile's products.  The running
-// maximum is lazy: O is rescaled only when a row's maximum grows by more than
-// 2^8, by the row's own thread, which knows from S's arrival that all earlier
-// products have finished (products complete in order).
+// maximum is lazy: it moves, and O is rescaled by the row's own thread, only
+// when a row's maximum grows by more than 2^8; S's arrival means that all
+// earlier products have finished (products complete in order).  P is announced
+// in two parts, so that its first products run under the last exponentials.
+//
+// What bounds it (32 / 8 heads of 128, 8K-token prompts, cycles per 128 keys
+// of both tiles): 2048 are tensor work at its nominal rate; with the softmax
+// replaced by nothing 2590 remain (the scores' product reads both operands
+// from shared memory at its full bandwidth, and the loads write there too);
+// with it 3250, a tile's softmax (1800: 128 exponentials a row at 16 a clock
+// and SM, half overlapped with the other tile's) behind its products.  Tried
+// and slower: two threads per row (3860), steps of 64 keys with two score
+// buffers per tile (3560: scores 64 wide read shared memory 1.5 times as much).
 //
 // Warps 0-3 / 4-7: softmax and epilogue of tile 0 / 1; 8: products, tensor
 // memory; 9: TMA loads; 10: zeroes the rows of a last V tile that lie behind
@@ -40,6 +50,11 @@ static_assert(256 * REGS_SOFTMAX + 128 * REGS_REST <= 168 * THREADS, "register s
 constexpr int TMEM_COLS = 512;
 constexpr int INLINE_SEQS = 32;     // prompts that a warp schedules without a list
 constexpr float RESCALE_LOG2 = 8.f;
+// Of 16 exponentials, how many run on the multiply-add pipe, and how many of
+// a tile's four 32-key pieces of P are announced together first.  Cycles per
+// 128 keys of both tiles: 0 -> 3440, 2 -> 3280, 3 -> 3256, 4 -> 3370 (three
+// pieces first); 2 with two pieces first 3249.
+constexpr int FMA_EXP = 3, FIRST_PIECES = 2;
 constexpr float LN2 = 0.6931471805599453f;
 
 template <int D> struct Cfg {
@@ -177,6 +192,27 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// 2^x of two numbers on the multiply-add pipe, for x <= 100: x = n + f with n
+// whole (rounded by adding 1.5 * 2^23) and |f| <= 1/2, 2^f by a polynomial of
+// degree 4 fitted here for the least largest relative error with its constant
+// term held at 1 (2.9e-6, a thousandth of the bf16 rounding that follows), n
+// added to the exponent.  x <= -127 gives +0: there f = 0, and 1 with its
+// exponent lowered by 127 is +0.
+__device__ __forceinline__ float2 exp2_fma(float2 x) {
+    const float2 magic = make_float2(12582912.f, 12582912.f);
+    x.x = fmaxf(x.x, -127.f);
+    x.y = fmaxf(x.y, -127.f);
+    const float2 t = add2(x, magic);
+    const float2 f = fma2(add2(t, make_float2(-12582912.f, -12582912.f)), make_float2(-1.f, -1.f), x);
+    float2 p = fma2(make_float2(0.009585382416844368f, 0.009585382416844368f), f,
+                    make_float2(0.05590662732720375f, 0.05590662732720375f));
+    p = fma2(p, f, make_float2(0.24024038016796112f, 0.24024038016796112f));
+    p = fma2(p, f, make_float2(0.6931241750717163f, 0.6931241750717163f));
+    p = fma2(p, f, make_float2(1.f, 1.f));
+    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+}
+
 __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -312,43 +348,75 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prompt_tc_kernel(const __grid_
                 tmem_ld32(s_col, s[0]);
                 tmem_ld32(s_col + 32, s[1]);
                 tmem_ld_wait();
-                tmem_ld32(s_col + 64, s[2]);                        // (these arrive under the first half's maximum)
+                tmem_ld32(s_col + 64, s[2]);                        // (these arrive under the first half's weights)
                 tmem_ld32(s_col + 96, s[3]);
-                float mx[4];
+                if (j == n - 1) {                                   // the diagonal tile: keys up to the row's own
+                    tmem_ld_wait();
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (half) tmem_ld_wait();
-                    if (j == n - 1) {                               // the diagonal tile: keys up to the row's own
+                    for (int c = 0; c < 4; ++c)
 #pragma unroll
-                        for (int c = 2 * half; c < 2 * half + 2; ++c)
+                        for (int e = 0; e < 32; ++e)
+                            if (c * 32 + e > r) s[c][e] = -INFINITY;
+                }
+                auto largest = [&]() {
+                    float mx[4];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (c * 32 + e > r) s[c][e] = -INFINITY;
-                    }
+                    for (int c = 0; c < 4; ++c) mx[c] = fmaxf(s[c][0], s[c][1]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float* x = s[2 * half + (i >> 1)] + (i & 1) * 16;
-                        if (half) mx[i] = max3(mx[i], x[0], x[1]);
-                        else mx[i] = fmaxf(x[0], x[1]);
-                    }
+                    for (int e = 2; e < 32; e += 2)
 #pragma unroll
-                    for (int e = 2; e < 16; e += 2)
+                        for (int c = 0; c < 4; ++c) mx[c] = max3(mx[c], s[c][e], s[c][e + 1]);
+                    return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale_log2;
+                };
+                const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
+                float2 sum[2], neg;
+                auto weights = [&](int c) {                         // P of 32 keys
+                    uint32_t pk[16];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float* x = s[2 * half + (i >> 1)] + (i & 1) * 16 + e;
-                            mx[i] = max3(mx[i], x[0], x[1]);
+                    for (int e = 0; e < 16; ++e) {
+                        float2 x = fma2(make_float2(s[c][2 * e], s[c][2 * e + 1]), sc2, neg);
+                        if ((e * FMA_EXP) % 16 < FMA_EXP) {
+                            x = exp2_fma(x);
+                        } else {
+                            x.x = fast_exp2(x.x);
+                            x.y = fast_exp2(x.y);
                         }
+                        sum[e & 1] = add2(sum[e & 1], x);
+                        pk[e] = bf16x2_bits(x.x, x.y);
+                    }
+                    tmem_st16(s_col + c * 16, pk);
+                };
+                auto announce = [&](int part) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->p_ready[t][part]);
+                };
+                if (j == 0) {
+                    tmem_ld_wait();
+                    m = largest();
                 }
-                const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale_log2;
-                bool move = false;
-                float f = 1.f;
-                if (top > m + RESCALE_LOG2 || (m == -INFINITY && top > m)) {
-                    f = fast_exp2(m - top);                         // 0 while nothing has been summed
-                    m = top;
+                // The weights are formed with the maximum in use while the
+                // tile's own is still being found: it seldom moves.  Where it
+                // does, O and the sum are rescaled and the weights formed again,
+                // before any of them is announced.
+#pragma unroll 1
+                for (int pass = 0;; ++pass) {
+                    const float base = m == -INFINITY ? 0.f : m;
+                    neg = make_float2(-base, -base);
+                    sum[0] = sum[1] = make_float2(0.f, 0.f);
+                    weights(0);
+                    weights(1);
+                    if (pass == 0) tmem_ld_wait();
+#pragma unroll
+                    for (int c = 2; c < FIRST_PIECES; ++c) weights(c);
+                    if (pass > 0 || j == 0) break;
+                    const float top = largest();
+                    const bool move = top > m + RESCALE_LOG2 || (m == -INFINITY && top > m);
+                    if (!__any_sync(0xffffffffu, move)) break;
+                    const float f = move ? fast_exp2(m - top) : 1.f;
+                    if (move) m = top;
                     l *= f;
-                    move = j > 0;
-                }
-                if (__any_sync(0xffffffffu, move)) {
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         float v[32];
@@ -359,28 +427,10 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prompt_tc_kernel(const __grid_
                         tmem_st32(o_col + c * 32, v);
                     }
                 }
-                const float base = m == -INFINITY ? 0.f : m;
-                const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), neg = make_float2(-base, -base);
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                announce(0);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float2 x = fma2(make_float2(s[c][2 * e], s[c][2 * e + 1]), sc2, neg);
-                        x.x = fast_exp2(x.x);
-                        x.y = fast_exp2(x.y);
-                        sum[e & 1] = add2(sum[e & 1], x);
-                        pk[e] = bf16x2_bits(x.x, x.y);
-                    }
-                    tmem_st16(s_col + c * 16, pk);
-                    if (c & 1) {                                    // half of P: its products may begin
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars->p_ready[t][c >> 1]);
-                    }
-                }
+                for (int c = FIRST_PIECES; c < 4; ++c) weights(c);
+                announce(1);
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
             }
@@ -422,12 +472,16 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prompt_tc_kernel(const __grid_
             auto wait_kv = [&](uint32_t i) {
                 return mbar_wait(&bars->kv_full[i % NS], (i / NS) & 1, a.err, DEV_ERR_TIMEOUT_TMA, abort_flag);
             };
+            // low halves of the first descriptors of Q, K (K-major) and V (MN-major)
+            constexpr uint32_t hi = desc_sw128_hi(1024);
+            const uint32_t q_lo = desc_lo(qb, 1), k_lo = desc_lo(kvb, 1), v_lo = desc_lo(kvb, BLK >> 4);
             auto product_s = [&](int t, uint32_t kslot) {
-                const uint32_t ka = kvb + (kslot % NS) * TILE, qa = qb + t * TILE;
+                const uint32_t ql = q_lo + t * (TILE >> 4), kl = k_lo + (kslot % NS) * (TILE >> 4), d = tmem + t * 128;
+                mma_ss_halves<false>(d, ql, kl, hi, idesc_s);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (uint32_t)((kk >> 2) * BLK + (kk & 3) * 32);
-                    mma_ss(tmem + t * 128, desc_sw128(qa + off, 1024), desc_sw128(ka + off, 1024), idesc_s, kk > 0);
+                for (int kk = 1; kk < D / 16; ++kk) {
+                    const uint32_t off = (uint32_t)((kk >> 2) * BLK + (kk & 3) * 32) >> 4;
+                    mma_ss_halves<true>(d, ql + off, kl + off, hi, idesc_s);
                 }
                 mma_commit(&bars->s_full[t]);
             };
@@ -453,16 +507,16 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prompt_tc_kernel(const __grid_
                         bool have_k = false;
                         for (int t = 0; t < 2 && ok; ++t) {
                             if (j >= w.n[t]) continue;
-                            const uint32_t va = kvb + (vslot % NS) * TILE;
+                            const uint32_t vl = v_lo + (vslot % NS) * (TILE >> 4), d = tmem + C::O_COL + t * D;
 #pragma unroll
                             for (int half = 0; half < 2; ++half) {
                                 ok = ok && mbar_wait(&bars->p_ready[t][half], n_p[t] & 1, a.err, DEV_ERR_TIMEOUT_PEER, abort_flag);
                                 if (!ok) break;
                                 tc_fence_after();
 #pragma unroll
-                                for (int kk = half * (BN / 32); kk < (half + 1) * (BN / 32); ++kk)
-                                    mma_ts(tmem + C::O_COL + t * D, tmem + t * 128 + kk * 8,
-                                           desc_sw128_mn(va + kk * 16 * 128, BLK, 1024), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+                                for (int kk = half ? 2 * FIRST_PIECES : 0; kk < (half ? BN / 16 : 2 * FIRST_PIECES); ++kk)
+                                    mma_ts_halves(d, tmem + t * 128 + kk * 8, vl + kk * (16 * 128 >> 4), hi, idesc_o,
+                                                  kk > 0 ? 1u : j > 0);
                             }
                             if (!ok) break;
                             ++n_p[t];
