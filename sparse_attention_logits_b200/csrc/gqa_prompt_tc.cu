@@ -57,10 +57,11 @@ constexpr float RESCALE_LOG2 = 8.f;
 constexpr int FMA_EXP = 3, FIRST_PIECES = 2;
 constexpr float LN2 = 0.6931471805599453f;
 
+constexpr int OUT_STAGE = 4096;         // per softmax warp: 32 output rows x 64 dims
 template <int D> struct Cfg {
     static constexpr int TILE = 128 * D * 2;                // bytes of a Q, K or V tile
     static constexpr int STAGES = D == 128 ? 4 : 8;         // K / V ring
-    static constexpr int SMEM = 2 * TILE + STAGES * TILE + 1024 + 1024;
+    static constexpr int SMEM = 2 * TILE + STAGES * TILE + 8 * OUT_STAGE + 1024 + 1024;
     static constexpr int O_COL = 256;                       // S_0, S_1 at 0, 128; O_0, O_1 behind
 };
 
@@ -288,7 +289,8 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prompt_tc_kernel(const __grid_
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t* qbuf = smem;                               // two Q tiles: [D / 64][128 rows x 128 B], swizzled
     uint8_t* kvbuf = smem + 2 * TILE;                   // ring of K and V tiles, same layout
-    auto* bars = (Bars<NS>*)(smem + (2 + NS) * TILE);
+    uint8_t* obuf = smem + (2 + NS) * TILE;             // output rows on their way to memory
+    auto* bars = (Bars<NS>*)(obuf + 8 * OUT_STAGE);
     volatile int* abort_flag = &bars->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -439,25 +441,38 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prompt_tc_kernel(const __grid_
             if (!ok) break;
             ++n_o;
             tc_fence_after();
-            const bool mine = w.row0[t] + r < w.len;
-            const int64_t row = (int64_t)w.first + w.row0[t] + r;
+            // Rows of 64 dims through shared memory, so that a store covers four
+            // whole 128-byte pieces instead of 32 lanes' own rows.
+            const int rows = w.len - w.row0[t] - (warp & 3) * 32;   // of this warp's 32, those inside the prompt
+            const int64_t row0 = (int64_t)w.first + w.row0[t] + (warp & 3) * 32;
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            uint4* out = (uint4*)((__nv_bfloat16*)a.out + (row * a.n_heads + w.head[t]) * D);
+            uint8_t* stage = obuf + warp * OUT_STAGE;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                float v[32];
-                tmem_ld32(o_col + c * 32, v);
-                tmem_ld_wait();
-                if (mine) {
+            for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float v[32];
+                    tmem_ld32(o_col + c * 64 + h * 32, v);
+                    tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        out[c * 4 + e] = make_uint4(bf16x2_bits(v[8 * e] * inv, v[8 * e + 1] * inv),
-                                                    bf16x2_bits(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
-                                                    bf16x2_bits(v[8 * e + 4] * inv, v[8 * e + 5] * inv),
-                                                    bf16x2_bits(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
+                        st_shared_v4(stage + lane * 128 + (((4 * h + e) ^ (lane & 7)) << 4),
+                                     bf16x2_bits(v[8 * e] * inv, v[8 * e + 1] * inv),
+                                     bf16x2_bits(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
+                                     bf16x2_bits(v[8 * e + 4] * inv, v[8 * e + 5] * inv),
+                                     bf16x2_bits(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
                 }
+                __syncwarp();
+                __nv_bfloat16* out = (__nv_bfloat16*)a.out + (row0 * a.n_heads + w.head[t]) * D + c * 64 + (lane & 7) * 8;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int k = i * 4 + (lane >> 3);
+                    const uint4 x = ld_shared_v4(stage + k * 128 + (((lane & 7) ^ (k & 7)) << 4));
+                    if (k < rows) *(uint4*)(out + (int64_t)k * a.n_heads * D) = x;
+                }
+                __syncwarp();
             }
-            if (mine) a.lse[row * a.n_heads + w.head[t]] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+            if (lane < rows) a.lse[(row0 + lane) * a.n_heads + w.head[t]] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
             tc_fence_before();          // O has been read before this tile's next P is announced
         }
     } else {
