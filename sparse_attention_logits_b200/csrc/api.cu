@@ -655,7 +655,7 @@ dsa_status_t gqa_prompt_attention(const void* q, int64_t ld_q, const void* k, in
     a.lse = lse;
     a.err = L.err;
     return cuda_status(dtype == DSA_BF16 ? dsa::launch_gqa_prompt_tc(L, a, head_dim, workspace)
-                                         : dsa::launch_gqa_prompt_simt(L, a, head_dim),
+                                         : dsa::launch_gqa_prompt_f32(L, a, head_dim),
                        "gqa_prompt_attention launch");
 }
 

@@ -1,0 +1,323 @@
+// Causal grouped-query attention over whole prompts, packed one behind the
+// other, in fp32:
+//   out[i,h] = sum_{j <= i} softmax_j(scale q_i . k_j) v_j   within each prompt.
+//
+// Every factor is split into two tf32 numbers, x = hi + lo (11 + 11 bits), and a
+// product is three tensor products hi hi + hi lo + lo hi; what is left out or
+// rounded is at most 3 x 2^-22 of |x y| a term, no more than a dot product of a
+// few fp32 terms.  (fp32 multiply-adds on the CUDA cores took 121 us where
+// this takes the time beside the launch.)
+//
+// A block takes 64 query rows of one head.  Two groups of 4 warps, 16 rows a
+// warp, walk alternate tiles of the keys with an online softmax each and are
+// joined at the end, so that the longest rows of a short batch take half as
+// long.  K and V are split once per tile, on their way into shared memory, in the order in which mma.m16n8k8's lanes read
+// them: 16-byte pieces (hi, lo, hi, lo) of two neighbouring dims of a key (K)
+// or of one dim of two neighbouring keys (V); which dims or keys a k-step
+// takes is free as long as both factors agree.  The next tile's rows are
+// requested before the present one's products.  Bound by the warp-level tensor
+// instruction and the shared-memory reads that feed it.
+#include "common.cuh"
+#include "launchers.h"
+#include "sm100.cuh"
+
+namespace dsa {
+
+using namespace sm100;
+
+namespace {
+
+constexpr int BM = 64, GROUPS = 2, GROUP = 128, THREADS = GROUPS * GROUP;
+constexpr float LN2 = 0.6931471805599453f;
+
+// Block index -> (prompt, tile of query rows): the tiles of the prompts in
+// order, the last tile of each first (the longest work first).  False past
+// the last tile.
+struct Tile {
+    int first, len, row0;           // the prompt's first packed row and length; the tile's first row in it
+};
+__device__ __forceinline__ bool find_tile(const PromptArgs& a, int t, Tile& w, int* sh) {
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x < 32) {
+        int base = 0, found = -1;
+        for (int s0 = 0; s0 < a.n_seqs && found < 0; s0 += 32) {
+            const int s = s0 + lane;
+            int b = 0, n = 0;
+            if (s < a.n_seqs) {
+                b = a.cu_seqlens[s];
+                n = a.cu_seqlens[s + 1] - b;
+                if (b < 0 || n < 0 || (int64_t)b + n > a.total) {
+                    record_error(a.err, DEV_ERR_BAD_INDEX);
+                    n = 0;
+                }
+            }
+            const int tiles = (n + BM - 1) / BM;
+            int x = tiles;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, d);
+                if (lane >= d) x += y;
+            }
+            if (t >= base + x - tiles && t < base + x) {
+                sh[0] = b;
+                sh[1] = n;
+                sh[2] = (tiles - 1 - (t - (base + x - tiles))) * BM;
+                found = 1;
+            }
+            found = __any_sync(0xffffffffu, found > 0) ? 1 : -1;
+            base += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (lane == 0) sh[3] = found;
+    }
+    __syncthreads();
+    w.first = sh[0];
+    w.len = sh[1];
+    w.row0 = sh[2];
+    return sh[3] > 0;
+}
+
+
+// tf32 parts of an fp32 number: hi = x rounded to 11 bits, lo = x - hi, each
+// as the tensor core reads it (it ignores the low 13 bits).
+__device__ __forceinline__ uint4 split2(float x, float y) {
+    uint4 r;
+    r.x = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    r.y = __float_as_uint(x - __uint_as_float(r.x)) + 0x1000u;
+    r.z = (__float_as_uint(y) + 0x1000u) & 0xffffe000u;
+    r.w = __float_as_uint(y - __uint_as_float(r.z)) + 0x1000u;
+    return r;
+}
+__device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// C[t] += A B[t], A's parts in hi / lo, B's as pieces (hi, lo, hi, lo) of k = c4
+// and c4 + 4.  A product's three parts follow one another at a distance of N.
+template <int N>
+__device__ __forceinline__ void mma_split(float (*c)[4], const uint32_t (&hi)[4], const uint32_t (&lo)[4], const uint4 (&b)[N]) {
+#pragma unroll
+    for (int t = 0; t < N; ++t) mma1688(c[t], lo, b[t].x, b[t].z);
+#pragma unroll
+    for (int t = 0; t < N; ++t) mma1688(c[t], hi, b[t].y, b[t].w);
+#pragma unroll
+    for (int t = 0; t < N; ++t) mma1688(c[t], hi, b[t].x, b[t].z);
+}
+
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <int D> struct Cfg {
+    static constexpr int BN = D == 64 ? 64 : 32;                    // keys of a tile
+    static constexpr int KV = BN * D * 8;                           // bytes of a split K (or V) tile
+    static constexpr int Q = BM * D * 8;
+    static constexpr int SMEM = Q + GROUPS * 2 * KV;
+    static_assert(2 * KV >= BM * (D + 2) * 4, "a group's output is handed over in its tiles");
+};
+
+template <int D>
+__global__ void __launch_bounds__(THREADS) gqa_prompt_f32_kernel(const PromptArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    using C = Cfg<D>;
+    constexpr int BN = C::BN, NT = D / 8, ST = BN / 8, HALF = D / 2;
+    constexpr int LOADS = BN * HALF / GROUP;          // (key, two dims) or (two keys, dim) pieces of a tile per thread
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint4* sq = (uint4*)smem;                           // [BM][D / 2] pieces, swizzled by row
+    const int grp = threadIdx.x / GROUP;
+    uint4* sk = sq + BM * HALF + grp * 2 * BN * HALF;   // the group's tile: [BN][D / 2]
+    uint4* sv = sk + BN * HALF;                         // [BN / 2][D], swizzled by key pair
+    __shared__ int sh[4];
+    Tile w;
+    const int tile = blockIdx.x / a.n_heads;
+    if (!find_tile(a, tile, w, sh)) return;
+    const int head = blockIdx.x - tile * a.n_heads, kvh = head / (a.n_heads / a.n_kv_heads);
+    const int tid = threadIdx.x % GROUP, lane = tid & 31, warp = tid >> 5, r4 = lane >> 2, c4 = lane & 3;
+    const int rows = min(BM, w.len - w.row0);
+    const float* q = (const float*)a.q + (int64_t)(w.first + w.row0) * a.ld_q + head * D;
+    const float* kb = (const float*)a.k + (int64_t)w.first * a.ld_k + kvh * D;
+    const float* vb = (const float*)a.v + (int64_t)w.first * a.ld_v + kvh * D;
+    const int keys = w.row0 + rows;                     // the tile's last row sees this many
+
+    float2 kx[LOADS], vx[LOADS];                        // the next tile's rows, on their way
+    auto request = [&](int k0) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int p = i * GROUP + tid;
+            const int key = k0 + p / HALF, d2 = p % HALF;
+            kx[i] = key < keys ? __ldg((const float2*)(kb + (int64_t)key * a.ld_k) + d2) : make_float2(0.f, 0.f);
+            const int key0 = k0 + 2 * (p / D), d = p % D;
+            vx[i].x = key0 < keys ? __ldg(vb + (int64_t)key0 * a.ld_v + d) : 0.f;
+            vx[i].y = key0 + 1 < keys ? __ldg(vb + (int64_t)(key0 + 1) * a.ld_v + d) : 0.f;
+        }
+    };
+    auto store = [&]() {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int p = i * GROUP + tid;
+            const int key = p / HALF, d2 = p % HALF;
+            sk[key * HALF + (d2 ^ ((key & 1) << 2))] = split2(kx[i].x, kx[i].y);
+            const int pair = p / D, d = p % D;
+            sv[pair * D + (d ^ ((pair & 3) << 1))] = split2(vx[i].x, vx[i].y);
+        }
+    };
+    request(grp * BN);
+    for (int p = threadIdx.x; p < BM * HALF; p += THREADS) {
+        const int r = p / HALF, d2 = p % HALF;
+        const float2 x = r < rows ? __ldg((const float2*)(q + (int64_t)r * a.ld_q) + d2) : make_float2(0.f, 0.f);
+        sq[r * HALF + (d2 ^ ((r & 1) << 2))] = split2(x.x * a.scale_log2, x.y * a.scale_log2);
+    }
+    float o[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    const int row = warp * 16 + r4;                     // this lane's rows of the tile: row, row + 8
+    const int last = w.row0 + min(rows, warp * 16 + 16) - 1;    // the warp's last row
+    __syncthreads();                                    // the queries stand
+    for (int k0 = grp * BN; k0 < keys; k0 += GROUPS * BN) {
+        named_bar_sync(1 + grp, GROUP);                 // the tile before has been read
+        store();
+        named_bar_sync(1 + grp, GROUP);
+        if (k0 + GROUPS * BN < keys) request(k0 + GROUPS * BN);
+        if (k0 > last) continue;                        // all of it lies behind this warp's rows
+        float s[ST][4];
+#pragma unroll
+        for (int t = 0; t < ST; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+        // k-step kk: dims 8 kk + 2 c4 (k = c4) and 8 kk + 2 c4 + 1 (k = c4 + 4)
+#pragma unroll 2
+        for (int kk = 0; kk < D / 8; ++kk) {
+            const uint4 x = sq[row * HALF + ((4 * kk + c4) ^ ((row & 1) << 2))];
+            const uint4 y = sq[(row + 8) * HALF + ((4 * kk + c4) ^ ((row & 1) << 2))];
+            const uint32_t hi[4] = {x.x, y.x, x.z, y.z}, lo[4] = {x.y, y.y, x.w, y.w};
+            uint4 b[ST];
+#pragma unroll
+            for (int t = 0; t < ST; ++t) b[t] = sk[(8 * t + r4) * HALF + ((4 * kk + c4) ^ ((r4 & 1) << 2))];
+            mma_split<ST>(s, hi, lo, b);
+        }
+        // lane: rows row, row + 8; keys k0 + 8 t + 2 c4 + {0, 1}
+        float f[2];
+        bool moved = false;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int at = w.row0 + row + 8 * half;
+            float top = -INFINITY;
+#pragma unroll
+            for (int t = 0; t < ST; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (k0 + 8 * t + 2 * c4 + e > at) s[t][2 * half + e] = -INFINITY;
+                    top = fmaxf(top, s[t][2 * half + e]);
+                }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            f[half] = 1.f;
+            if (top > m[half]) {
+                f[half] = fast_exp2(m[half] - top);
+                m[half] = top;
+                l[half] *= f[half];
+                moved = true;
+            }
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                o[t][0] *= f[0]; o[t][1] *= f[0]; o[t][2] *= f[1]; o[t][3] *= f[1];
+            }
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const float base = m[half] > -INFINITY ? m[half] : 0.f;
+#pragma unroll
+            for (int t = 0; t < ST; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float p = fast_exp2(s[t][2 * half + e] - base);
+                    l[half] += p;
+                    s[t][2 * half + e] = p;
+                }
+        }
+        // k-step t: keys 8 t + 2 c4 (k = c4) and 8 t + 2 c4 + 1 (k = c4 + 4), the lane's own scores
+#pragma unroll
+        for (int t = 0; t < ST; ++t) {
+            const uint4 x = split2(s[t][0], s[t][1]), y = split2(s[t][2], s[t][3]);
+            const uint32_t hi[4] = {x.x, y.x, x.z, y.z}, lo[4] = {x.y, y.y, x.w, y.w};
+#pragma unroll
+            for (int n0 = 0; n0 < NT; n0 += 8) {
+                uint4 b[8];
+#pragma unroll
+                for (int n = 0; n < 8; ++n) b[n] = sv[(4 * t + c4) * D + ((8 * (n0 + n) + r4) ^ (c4 << 1))];
+                mma_split<8>(o + n0, hi, lo, b);
+            }
+        }
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
+        l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
+    }
+    // group 1's (maximum, sum, output) go over through its own tiles, a row of D + 2 floats each
+    __syncthreads();
+    float* hand = (float*)(sq + BM * HALF + 2 * BN * HALF);
+    if (grp == 1) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float* h = hand + (row + 8 * half) * (D + 2);
+            if (c4 == 0) *(float2*)h = make_float2(m[half], l[half]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) *(float2*)(h + 2 + 8 * n + 2 * c4) = make_float2(o[n][2 * half], o[n][2 * half + 1]);
+        }
+    }
+    __syncthreads();
+    if (grp == 1) return;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        if (row + 8 * half >= rows) continue;
+        const float* h = hand + (row + 8 * half) * (D + 2);
+        const float2 other = *(const float2*)h;
+        const float top = fmaxf(m[half], other.x), base = top > -INFINITY ? top : 0.f;
+        const float f0 = fast_exp2(m[half] - base), f1 = fast_exp2(other.x - base);
+        const float sum = f0 * l[half] + f1 * other.y, inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int64_t at = w.first + w.row0 + row + 8 * half;
+        float* out = (float*)a.out + (at * a.n_heads + head) * D + 2 * c4;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const float2 x = *(const float2*)(h + 2 + 8 * n + 2 * c4);
+            *(float2*)(out + 8 * n) = make_float2((f0 * o[n][2 * half] + f1 * x.x) * inv, (f0 * o[n][2 * half + 1] + f1 * x.y) * inv);
+        }
+        if (c4 == 0) a.lse[at * a.n_heads + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * LN2;
+    }
+}
+
+template <int D>
+cudaError_t launch(const Launch& L, const PromptArgs& a) {
+    static std::atomic<int> done[kMaxDevices];
+    cudaError_t e = allow_smem(done, gqa_prompt_f32_kernel<D>, Cfg<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1] = {pdl_attr()};
+    // as many tiles as any split of `total` rows over the prompts can have
+    cfg.gridDim = dim3((unsigned)a.n_heads * (unsigned)(a.total / BM + (a.n_seqs < a.total ? a.n_seqs : a.total)));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = Cfg<D>::SMEM;
+    cfg.stream = L.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, gqa_prompt_f32_kernel<D>, a);
+    count_launch();
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_gqa_prompt_f32(const Launch& L, const PromptArgs& a, int head_dim) {
+    return head_dim == 64 ? launch<64>(L, a) : launch<128>(L, a);
+}
+
+}  // namespace dsa

@@ -183,6 +183,6 @@ struct PromptArgs {
     unsigned* err;
 };
 size_t gqa_prompt_workspace_bytes(int total, int n_seqs, dsa_dtype_t dtype);
-cudaError_t launch_gqa_prompt_simt(const Launch& L, const PromptArgs& a, int head_dim);                     // fp32
+cudaError_t launch_gqa_prompt_f32(const Launch& L, const PromptArgs& a, int head_dim);                     // fp32
 cudaError_t launch_gqa_prompt_tc(const Launch& L, const PromptArgs& a, int head_dim, void* workspace);      // bf16
 }  // namespace dsa
