@@ -345,6 +345,22 @@ __device__ __forceinline__ void load_free_bits(const int32_t* ref_count, int num
     }
 }
 
+// Exclusive prefix counts of a quantity over the words of this block's slice
+// (count(w) of word w) into before[w]; the slice's total is returned.
+template <class F>
+__device__ __forceinline__ int word_ranks(int words, int* before, int* warp_sum, F&& count) {
+    const int per = (words + BOOK_THREADS - 1) / BOOK_THREADS;
+    const int w0 = min(words, (int)threadIdx.x * per), w1 = min(words, w0 + per);
+    int mine = 0, total;
+    for (int w = w0; w < w1; ++w) mine += count(w);
+    int run = block_scan(mine, warp_sum, &total);
+    for (int w = w0; w < w1; ++w) {
+        before[w] = run;
+        run += count(w);
+    }
+    return total;
+}
+
 // kv_pages_extend (FORK = false) and kv_pages_fork (FORK = true).  Items are
 // the list's entries; each needs some fresh pages (extend: as many as its new
 // length asks for; fork: one for a last page that is not full).  An item is
@@ -359,7 +375,8 @@ kv_assign_kernel(const BooksArgs a, int words_per_cta) {
     extern __shared__ uint32_t dyn[];
     __shared__ BookShared sh;
     uint32_t* bits = dyn;                               // [words_per_cta]
-    int* start = (int*)(dyn + words_per_cta);           // [n + 1] needs before each item
+    int* before = (int*)(dyn + words_per_cta);          // [words_per_cta] free pages of the slice before each word
+    int* start = before + words_per_cta;                // [n + 1] needs before each item
     int* len = start + a.n + 1;                         // [n] extend: new length; fork: the parent's; -1: not served
     int* what = len + a.n;                              // [n] sequence (fork: child)
     const int rank = (int)cluster_ctarank(), tid = threadIdx.x;
@@ -415,46 +432,40 @@ kv_assign_kernel(const BooksArgs a, int words_per_cta) {
     }
     if (tid == 0) start[a.n] = total_need;
 
-    // free pages of this slice, by threads of consecutive words
-    const int wper = (words_per_cta + BOOK_THREADS - 1) / BOOK_THREADS;
-    const int w0 = min(words_per_cta, tid * wper), w1 = min(words_per_cta, w0 + wper);
-    int free_mine = 0;
-    for (int w = w0; w < w1; ++w) free_mine += __popc(bits[w]);
-    int slice_free;
-    int page_rank = block_scan(free_mine, sh.warp_sum[1], &slice_free);
+    const int slice_free = word_ranks(words_per_cta, before, sh.warp_sum[1], [&](int w) { return __popc(bits[w]); });
     if (tid == 0) sh.mine[0] = slice_free;
     cluster_sync_all();             // every block has read lengths and counts, and its own number stands
-    int n_free = 0;
+    int n_free = 0, rank0 = 0;
     for (int r = 0; r < BOOK_CTAS; ++r) {
         const int f = ld_cluster_s32(&sh.mine[0], r);
-        if (r < rank) page_rank += f;
+        if (r < rank) rank0 += f;
         n_free += f;
     }
 
-    // this slice's free pages to the items that they fall to
-    for (int w = w0; w < w1 && page_rank < total_need; ++w) {
-        uint32_t m = bits[w];
-        while (m && page_rank < total_need) {
-            const int page = (first_word + w) * 32 + __ffs(m) - 1;
-            m &= m - 1;
-            int lo = 0, hi = a.n;                       // last item with start <= rank: one that needs pages
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (start[mid] <= page_rank) lo = mid;
-                else hi = mid;
-            }
-            if (start[lo + 1] <= n_free) {
-                // the item's pages end where its new length ends
-                const int at = pages_of(len[lo], a.page_size) - (start[lo + 1] - page_rank);
-                a.page_table[(int64_t)what[lo] * a.max_pages + at] = page;
-                a.ref_count[page] = 1;
-                if (FORK) a.pair_dst[lo] = page;
-            }
-            ++page_rank;
+    // this slice's free pages to the items that they fall to: one warp per
+    // word, a page per lane (a thread walking its words' pages one after the
+    // other took 4 of extend's 12 us at 101K pages)
+    const int lane = tid & 31;
+    for (int w = tid >> 5; w < words_per_cta; w += BOOK_WARPS) {
+        const uint32_t m = bits[w];
+        const int page_rank = rank0 + before[w] + __popc(m & ((1u << lane) - 1u));
+        if (!((m >> lane) & 1u) || page_rank >= total_need) continue;
+        const int page = (first_word + w) * 32 + lane;
+        int lo = 0, hi = a.n;                           // last item with start <= rank: one that needs pages
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (start[mid] <= page_rank) lo = mid;
+            else hi = mid;
+        }
+        if (start[lo + 1] <= n_free) {
+            // the item's pages end where its new length ends
+            const int at = pages_of(len[lo], a.page_size) - (start[lo + 1] - page_rank);
+            a.page_table[(int64_t)what[lo] * a.max_pages + at] = page;
+            a.ref_count[page] = 1;
+            if (FORK) a.pair_dst[lo] = page;
         }
     }
     // the lengths, the shared pages (fork) and reports: one warp per item
-    const int lane = tid & 31;
     for (int i = rank + BOOK_CTAS * (tid >> 5); i < a.n; i += BOOK_CTAS * BOOK_WARPS) {
         const int need = start[i + 1] - start[i];
         const bool fits = need == 0 || start[i + 1] <= n_free;
@@ -496,7 +507,9 @@ kv_compact_plan_kernel(const CompactArgs a, int words_per_cta) {
     pdl_launch_dependents();
     extern __shared__ uint32_t dyn[];
     __shared__ BookShared sh;
-    uint32_t* bits = dyn;
+    uint32_t* bits = dyn;                               // [words_per_cta]
+    int* up = (int*)(dyn + words_per_cta);              // [words_per_cta] of the slice before each word: pages that move
+    int* hole = up + words_per_cta;                     // [words_per_cta] and places to fill
     const int rank = (int)cluster_ctarank(), tid = threadIdx.x;
     const int first_word = rank * words_per_cta;
     load_free_bits(a.ref_count, a.num_pages, first_word, words_per_cta, bits);
@@ -512,27 +525,22 @@ kv_compact_plan_kernel(const CompactArgs a, int words_per_cta) {
     int n_live = 0;
     for (int r = 0; r < BOOK_CTAS; ++r) n_live += ld_cluster_s32(&sh.mine[0], r);
 
-    int up = 0, hole = 0;           // this thread's pages that move, and places to fill
-    for (int w = w0; w < w1; ++w) {
-        const uint32_t pool = below(a.num_pages, first_word + w), low = below(n_live, first_word + w);
-        up += __popc(~bits[w] & pool & ~low);
-        hole += __popc(bits[w] & low);
-    }
-    int slice_up, slice_hole;
-    int r_up = block_scan(up, sh.warp_sum[1], &slice_up);
+    auto movers = [&](int w) { return ~bits[w] & below(a.num_pages, first_word + w) & ~below(n_live, first_word + w); };
+    auto holes = [&](int w) { return bits[w] & below(n_live, first_word + w); };
+    const int slice_up = word_ranks(words_per_cta, up, sh.warp_sum[1], [&](int w) { return __popc(movers(w)); });
     __syncthreads();                // warp_sum[0] is free again
-    int r_hole = block_scan(hole, sh.warp_sum[0], &slice_hole);
+    const int slice_hole = word_ranks(words_per_cta, hole, sh.warp_sum[0], [&](int w) { return __popc(holes(w)); });
     if (tid == 0) {
         sh.mine[1] = slice_up;
         sh.mine[2] = slice_hole;
     }
     cluster_sync_all();
-    int moves = 0;
+    int moves = 0, up0 = 0, hole0 = 0;
     for (int r = 0; r < BOOK_CTAS; ++r) {
         const int u = ld_cluster_s32(&sh.mine[1], r), h = ld_cluster_s32(&sh.mine[2], r);
         if (r < rank) {
-            r_up += u;
-            r_hole += h;
+            up0 += u;
+            hole0 += h;
         }
         moves += u;
     }
@@ -540,21 +548,22 @@ kv_compact_plan_kernel(const CompactArgs a, int words_per_cta) {
         a.state[0] = moves;
         a.state[1] = n_live;
     }
-    for (int w = w0; w < w1; ++w) {
-        const uint32_t pool = below(a.num_pages, first_word + w), low = below(n_live, first_word + w);
-        for (uint32_t m = pool; m; m &= m - 1) {
-            const int bit = __ffs(m) - 1, page = (first_word + w) * 32 + bit;
-            const bool is_free = (bits[w] >> bit) & 1u, is_low = (low >> bit) & 1u;
-            int to = is_free ? -1 : page;
-            if (!is_free && !is_low) {
-                a.pair_src[r_up] = page;
-                a.moved_ref[r_up] = a.ref_count[page];
-                to = -2 - r_up++;
-            } else if (is_free && is_low) {
-                a.pair_dst[r_hole++] = page;
-            }
-            a.to[page] = to;
+    // one warp per word, a page per lane
+    const int lane = tid & 31;
+    for (int w = tid >> 5; w < words_per_cta; w += BOOK_WARPS) {
+        const int page = (first_word + w) * 32 + lane;
+        if (page >= a.num_pages) continue;
+        const uint32_t u = movers(w), h = holes(w), under = (1u << lane) - 1u;
+        int to = (bits[w] >> lane) & 1u ? -1 : page;
+        if ((u >> lane) & 1u) {
+            const int k = up0 + up[w] + __popc(u & under);
+            a.pair_src[k] = page;
+            a.moved_ref[k] = a.ref_count[page];
+            to = -2 - k;
+        } else if ((h >> lane) & 1u) {
+            a.pair_dst[hole0 + hole[w] + __popc(h & under)] = page;
         }
+        a.to[page] = to;
     }
     cluster_sync_all();
 }
@@ -596,9 +605,10 @@ __global__ void __launch_bounds__(256) kv_compact_kernel(const __grid_constant__
 }
 
 constexpr int words_per_book_cta(int num_pages) { return ceil_div(ceil_div(num_pages, 32), BOOK_CTAS); }
-constexpr int books_smem(int num_pages, int n) { return (words_per_book_cta(num_pages) + 3 * n + 1) * 4; }
+constexpr int books_smem(int num_pages, int n) { return (2 * words_per_book_cta(num_pages) + 3 * n + 1) * 4; }
 constexpr int BOOK_SMEM_MAX = books_smem(DSA_KV_PAGES_MAX_POOL, DSA_KV_PAGES_MAX_LIST);
-static_assert(BOOK_SMEM_MAX <= 200 * 1024, "the books' bits and lists fit in shared memory");
+constexpr int PLAN_SMEM_MAX = 3 * 4 * words_per_book_cta(DSA_KV_PAGES_MAX_POOL);
+static_assert(BOOK_SMEM_MAX <= 200 * 1024 && PLAN_SMEM_MAX <= 200 * 1024, "the books' bits and lists fit in shared memory");
 
 // Caches [c0, c0 + n) of the caller's list as a kernel parameter.
 CopyList copy_list(const CacheList& l, int c0, int n) {
@@ -697,9 +707,9 @@ cudaError_t launch_kv_compact(const Launch& L, CompactArgs a, const CacheList& l
     a.moved_ref = a.pair_dst + a.num_pages;
     const int words = words_per_book_cta(a.num_pages);
     static std::atomic<int> done[kMaxDevices];
-    cudaError_t e = allow_smem(done, kv_compact_plan_kernel, BOOK_SMEM_MAX);
+    cudaError_t e = allow_smem(done, kv_compact_plan_kernel, PLAN_SMEM_MAX);
     if (e != cudaSuccess) return e;
-    e = launch(kv_compact_plan_kernel, BOOK_CTAS, BOOK_THREADS, (size_t)words * 4, L, a, words);
+    e = launch(kv_compact_plan_kernel, BOOK_CTAS, BOOK_THREADS, (size_t)words * 12, L, a, words);
     if (e != cudaSuccess) return e;
     const CopyList c = copy_list(l, 0, l.n_caches < kMaxCopyCaches ? l.n_caches : kMaxCopyCaches);
     e = launch(kv_compact_kernel, L.num_sms * 8, 256, 0, L, c, a);
