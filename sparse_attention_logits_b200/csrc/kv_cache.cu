@@ -278,11 +278,10 @@ __global__ void __launch_bounds__(256) kv_free_kernel(const BooksArgs a) {
     if (threadIdx.x == 0) a.seq_len[q] = 0;
 }
 
-// The pool's books are kept by one cluster of 8 blocks: each owns a
-// contiguous eighth of the pool and holds it as one bit per page in shared
-// memory, so that the pool's counts are read once, by 8 SMs, and ranks of
-// free pages need one exchange of eight numbers.  (One block alone takes the
-// whole scan: 102K pages cost it about three times as long.)
+// The pool's books are kept by one cluster of 8 blocks: each holds an eighth of
+// the pool as one bit per page in shared memory, so that the pool's counts are
+// read once, by 8 SMs, and ranks of free pages need one exchange through
+// distributed shared memory.
 constexpr int BOOK_CTAS = 8;
 constexpr int BOOK_THREADS = 1024;
 constexpr int BOOK_WARPS = BOOK_THREADS / 32;
@@ -325,16 +324,17 @@ __device__ __forceinline__ int ld_cluster_s32(const int* p, uint32_t rank) {
     return v;
 }
 
-// Bits of this block's slice of the pool: bit set = reference count <= 0 (free).
-// Pages past the pool read as used.  Words are 32 consecutive pages.
-__device__ __forceinline__ void load_free_bits(const int32_t* ref_count, int num_pages, int first_word, int words,
-                                               uint32_t* bits) {
+// Bits of this block's words of the pool: bit set = reference count <= 0 (free).
+// Word `local` holds the 32 pages from 32 place(local) on; pages past the pool
+// read as used.
+template <class F>
+__device__ __forceinline__ void load_free_bits(const int32_t* ref_count, int num_pages, int words, uint32_t* bits, F&& place) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int w0 = warp * 8; w0 < words; w0 += BOOK_WARPS * 8) {
         int v[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            const int64_t p = (int64_t)(first_word + w0 + u) * 32 + lane;
+            const int64_t p = (int64_t)place(w0 + u) * 32 + lane;
             v[u] = w0 + u < words && p < num_pages ? ref_count[p] : 1;
         }
 #pragma unroll
@@ -366,7 +366,13 @@ __device__ __forceinline__ int word_ranks(int words, int* before, int* warp_sum,
 // length asks for; fork: one for a last page that is not full).  An item is
 // served when the needs up to and with it fit the free pages; its r-th page
 // is the free page of rank (needs before it) + r, found by the block that
-// owns the page.  Nothing is written before every block has read its inputs.
+// holds the page.  Nothing is written before every block has read its inputs.
+//
+// The pool is dealt to the blocks in runs of 128 pages, since the pages handed
+// out are the lowest and would otherwise all fall to the first blocks (102K
+// pages, 16K of them handed out: 10 of 15 us, in three of eight blocks).
+constexpr int RUN_WORDS = 4;
+
 template <bool FORK>
 __global__ void __cluster_dims__(BOOK_CTAS, 1, 1) __launch_bounds__(BOOK_THREADS)
 kv_assign_kernel(const BooksArgs a, int words_per_cta) {
@@ -374,17 +380,26 @@ kv_assign_kernel(const BooksArgs a, int words_per_cta) {
     pdl_launch_dependents();
     extern __shared__ uint32_t dyn[];
     __shared__ BookShared sh;
+    const int runs = words_per_cta / RUN_WORDS;         // of this block
     uint32_t* bits = dyn;                               // [words_per_cta]
-    int* before = (int*)(dyn + words_per_cta);          // [words_per_cta] free pages of the slice before each word
-    int* start = before + words_per_cta;                // [n + 1] needs before each item
+    int* run_free = (int*)(dyn + words_per_cta);        // [runs] free pages of each run, read by the others
+    int* before = run_free + runs;                      // [runs] free pages of the pool before each run
+    int* start = before + runs;                         // [n + 1] needs before each item
     int* len = start + a.n + 1;                         // [n] extend: new length; fork: the parent's; -1: not served
     int* what = len + a.n;                              // [n] sequence (fork: child)
+    int* entry = what + a.n;                            // [n] table entry of the item's page of rank 0
     const int rank = (int)cluster_ctarank(), tid = threadIdx.x;
-    const int first_word = rank * words_per_cta;
+    auto place = [&](int w) { return (w / RUN_WORDS * BOOK_CTAS + rank) * RUN_WORDS + w % RUN_WORDS; };
     const int32_t* list = FORK ? a.children : a.seqs;
     for (int i = tid; i < a.n; i += BOOK_THREADS) what[i] = list[i];
-    load_free_bits(a.ref_count, a.num_pages, first_word, words_per_cta, bits);
+    load_free_bits(a.ref_count, a.num_pages, words_per_cta, bits, place);
     __syncthreads();
+    for (int r = tid; r < runs; r += BOOK_THREADS) {
+        int n = 0;
+#pragma unroll
+        for (int w = 0; w < RUN_WORDS; ++w) n += __popc(bits[r * RUN_WORDS + w]);
+        run_free[r] = n;
+    }
 
     // items: validity and needs, the same in every block
     const int per = (a.n + BOOK_THREADS - 1) / BOOK_THREADS;
@@ -429,28 +444,32 @@ kv_assign_kernel(const BooksArgs a, int words_per_cta) {
         const int need = start[i];
         start[i] = run;
         run += need;
+        // the item's pages end where its new length ends
+        entry[i] = what[i] * a.max_pages + pages_of(len[i], a.page_size) - run;
     }
     if (tid == 0) start[a.n] = total_need;
+    cluster_sync_all();             // every block has read lengths and counts, and its runs' numbers stand
 
-    const int slice_free = word_ranks(words_per_cta, before, sh.warp_sum[1], [&](int w) { return __popc(bits[w]); });
-    if (tid == 0) sh.mine[0] = slice_free;
-    cluster_sync_all();             // every block has read lengths and counts, and its own number stands
-    int n_free = 0, rank0 = 0;
-    for (int r = 0; r < BOOK_CTAS; ++r) {
-        const int f = ld_cluster_s32(&sh.mine[0], r);
-        if (r < rank) rank0 += f;
-        n_free += f;
+    // free pages of the pool before each run of this block, and in all
+    const int all_runs = runs * BOOK_CTAS, rper = (all_runs + BOOK_THREADS - 1) / BOOK_THREADS;
+    const int r0 = min(all_runs, tid * rper), r1 = min(all_runs, r0 + rper);
+    int mine = 0, n_free;
+    for (int r = r0; r < r1; ++r) mine += ld_cluster_s32(run_free + r / BOOK_CTAS, r % BOOK_CTAS);
+    int sum = block_scan(mine, sh.warp_sum[1], &n_free);
+    for (int r = r0; r < r1; ++r) {
+        if (r % BOOK_CTAS == rank) before[r / BOOK_CTAS] = sum;
+        sum += ld_cluster_s32(run_free + r / BOOK_CTAS, r % BOOK_CTAS);
     }
+    __syncthreads();
 
-    // this slice's free pages to the items that they fall to: one warp per
-    // word, a page per lane (a thread walking its words' pages one after the
-    // other took 4 of extend's 12 us at 101K pages)
+    // the free pages to the items that they fall to: one warp per word, a page per lane
     const int lane = tid & 31;
     for (int w = tid >> 5; w < words_per_cta; w += BOOK_WARPS) {
         const uint32_t m = bits[w];
-        const int page_rank = rank0 + before[w] + __popc(m & ((1u << lane) - 1u));
+        int page_rank = before[w / RUN_WORDS] + __popc(m & ((1u << lane) - 1u));
+        for (int v = w / RUN_WORDS * RUN_WORDS; v < w; ++v) page_rank += __popc(bits[v]);
         if (!((m >> lane) & 1u) || page_rank >= total_need) continue;
-        const int page = (first_word + w) * 32 + lane;
+        const int page = place(w) * 32 + lane;
         int lo = 0, hi = a.n;                           // last item with start <= rank: one that needs pages
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -458,9 +477,7 @@ kv_assign_kernel(const BooksArgs a, int words_per_cta) {
             else hi = mid;
         }
         if (start[lo + 1] <= n_free) {
-            // the item's pages end where its new length ends
-            const int at = pages_of(len[lo], a.page_size) - (start[lo + 1] - page_rank);
-            a.page_table[(int64_t)what[lo] * a.max_pages + at] = page;
+            a.page_table[entry[lo] + page_rank] = page;
             a.ref_count[page] = 1;
             if (FORK) a.pair_dst[lo] = page;
         }
@@ -492,7 +509,7 @@ kv_assign_kernel(const BooksArgs a, int words_per_cta) {
             }
         }
     }
-    cluster_sync_all();             // no block leaves while another may still read its number
+    cluster_sync_relaxed();         // no block leaves while another may still read its number
 }
 
 // kv_pages_compact, the plan.  With n_live pages in use, the ones at or above
@@ -512,7 +529,7 @@ kv_compact_plan_kernel(const CompactArgs a, int words_per_cta) {
     int* hole = up + words_per_cta;                     // [words_per_cta] and places to fill
     const int rank = (int)cluster_ctarank(), tid = threadIdx.x;
     const int first_word = rank * words_per_cta;
-    load_free_bits(a.ref_count, a.num_pages, first_word, words_per_cta, bits);
+    load_free_bits(a.ref_count, a.num_pages, words_per_cta, bits, [&](int w) { return first_word + w; });
     __syncthreads();
     const int wper = (words_per_cta + BOOK_THREADS - 1) / BOOK_THREADS;
     const int w0 = min(words_per_cta, tid * wper), w1 = min(words_per_cta, w0 + wper);
@@ -565,7 +582,7 @@ kv_compact_plan_kernel(const CompactArgs a, int words_per_cta) {
         }
         a.to[page] = to;
     }
-    cluster_sync_all();
+    cluster_sync_relaxed();
 }
 
 // kv_pages_compact, the moves: table entries and counts rewritten, then the
@@ -605,7 +622,13 @@ __global__ void __launch_bounds__(256) kv_compact_kernel(const __grid_constant__
 }
 
 constexpr int words_per_book_cta(int num_pages) { return ceil_div(ceil_div(num_pages, 32), BOOK_CTAS); }
-constexpr int books_smem(int num_pages, int n) { return (2 * words_per_book_cta(num_pages) + 3 * n + 1) * 4; }
+// kv_assign_kernel: whole runs of pages per block
+constexpr int words_per_assign_cta(int num_pages) {
+    return ceil_div(words_per_book_cta(num_pages), RUN_WORDS) * RUN_WORDS;
+}
+constexpr int books_smem(int num_pages, int n) {
+    return (words_per_assign_cta(num_pages) / RUN_WORDS * (RUN_WORDS + 2) + 4 * n + 1) * 4;
+}
 constexpr int BOOK_SMEM_MAX = books_smem(DSA_KV_PAGES_MAX_POOL, DSA_KV_PAGES_MAX_LIST);
 constexpr int PLAN_SMEM_MAX = 3 * 4 * words_per_book_cta(DSA_KV_PAGES_MAX_POOL);
 static_assert(BOOK_SMEM_MAX <= 200 * 1024 && PLAN_SMEM_MAX <= 200 * 1024, "the books' bits and lists fit in shared memory");
@@ -680,7 +703,7 @@ cudaError_t launch_kv_extend(const Launch& L, const BooksArgs& a) {
     static std::atomic<int> done[kMaxDevices];
     const cudaError_t e = allow_smem(done, kv_assign_kernel<false>, BOOK_SMEM_MAX);
     if (e != cudaSuccess) return e;
-    return launch(kv_assign_kernel<false>, BOOK_CTAS, BOOK_THREADS, smem, L, a, words_per_book_cta(a.num_pages));
+    return launch(kv_assign_kernel<false>, BOOK_CTAS, BOOK_THREADS, smem, L, a, words_per_assign_cta(a.num_pages));
 }
 
 size_t kv_fork_workspace_bytes(int n) { return (size_t)n * 8; }
@@ -692,7 +715,7 @@ cudaError_t launch_kv_fork(const Launch& L, BooksArgs a, const CacheList& l, voi
     static std::atomic<int> done[kMaxDevices];
     cudaError_t e = allow_smem(done, kv_assign_kernel<true>, BOOK_SMEM_MAX);
     if (e != cudaSuccess) return e;
-    e = launch(kv_assign_kernel<true>, BOOK_CTAS, BOOK_THREADS, smem, L, a, words_per_book_cta(a.num_pages));
+    e = launch(kv_assign_kernel<true>, BOOK_CTAS, BOOK_THREADS, smem, L, a, words_per_assign_cta(a.num_pages));
     if (e != cudaSuccess) return e;
     return launch_copies(L, l, a.pair_src, a.pair_dst, a.n);
 }
