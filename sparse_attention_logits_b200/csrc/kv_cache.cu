@@ -462,21 +462,27 @@ kv_assign_kernel(const BooksArgs a, int words_per_cta) {
     }
     __syncthreads();
 
-    // the free pages to the items that they fall to: one warp per word, a page per lane
-    const int lane = tid & 31;
-    for (int w = tid >> 5; w < words_per_cta; w += BOOK_WARPS) {
+    // the free pages to the items that they fall to: a page per lane; a warp's
+    // words follow one another, so that a lane's item is mostly its last one's
+    const int lane = tid & 31, wper = (words_per_cta + BOOK_WARPS - 1) / BOOK_WARPS;
+    const int w0 = min(words_per_cta, (tid >> 5) * wper), w1 = min(words_per_cta, w0 + wper);
+    int lo = 0;
+    for (int w = w0; w < w1; ++w) {
         const uint32_t m = bits[w];
         int page_rank = before[w / RUN_WORDS] + __popc(m & ((1u << lane) - 1u));
         for (int v = w / RUN_WORDS * RUN_WORDS; v < w; ++v) page_rank += __popc(bits[v]);
-        if (!((m >> lane) & 1u) || page_rank >= total_need) continue;
+        if (m == 0 || page_rank >= total_need) continue;    // (lanes without a free page keep their place, too)
         const int page = place(w) * 32 + lane;
-        int lo = 0, hi = a.n;                           // last item with start <= rank: one that needs pages
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (start[mid] <= page_rank) lo = mid;
-            else hi = mid;
+        // the last item with start <= rank: one that needs pages
+        if (start[lo + 1] <= page_rank) {
+            int hi = a.n;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (start[mid] <= page_rank) lo = mid;
+                else hi = mid;
+            }
         }
-        if (start[lo + 1] <= n_free) {
+        if (((m >> lane) & 1u) && start[lo + 1] <= n_free) {
             a.page_table[entry[lo] + page_rank] = page;
             a.ref_count[page] = 1;
             if (FORK) a.pair_dst[lo] = page;
