@@ -22,12 +22,16 @@ from . import _build
 
 LIB_PATH = _build.LIB_PATH
 
-if not os.path.exists(LIB_PATH):
+for _path in (LIB_PATH, _build.BINDING_PATH):
+    if os.path.exists(_path):
+        continue
     raise ImportError(
-        f"{LIB_PATH} is missing: build it with `python -m sparse_attention_logits_b200._build` "
+        f"{_path} is missing: build it with `python -m sparse_attention_logits_b200._build` "
         "(nvcc, sm_100a). There is no fallback implementation.")
 
 _lib = ctypes.CDLL(LIB_PATH)
+
+from . import _gqa  # noqa: E402  (the compiled part of the binding; calls the library above)
 
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_CUDA, DSA_ERR_DEVICE_TIMEOUT, DSA_ERR_OUT_OF_PAGES = range(6)
 DSA_FP32, DSA_BF16, DSA_FP8_E4M3, DSA_FP4_E2M1 = 0, 1, 2, 3
@@ -390,61 +394,13 @@ def indexer_key_append(k: torch.Tensor, slot: torch.Tensor, k_cache: torch.Tenso
 
 
 # ---- grouped-query attention and its paged key-value cache -------------------
+#
+# These calls are small, so their checks, outputs and workspaces are made in
+# compiled code (_gqa.so, built from csrc/gqa_binding.cpp): wrong placement,
+# shapes or strides raise ValueError, wrong types TypeError, and what the
+# library refuses DSAError, as everywhere here.
 
-# torch's current stream as a raw handle, without building a Stream object
-# (2 us a call, as much as a small kernel); the public way where it is missing.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda i: torch.cuda.current_stream(i).cuda_stream)
-
-
-def _call(name: str, dev: torch.device, *args) -> None:
-    """Entry point `name` on torch's current stream of dev; dev is made the
-    current device only when it is not."""
-    fn = getattr(_lib, name)
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, _raw_stream(dev.index))
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, _raw_stream(dev.index))
-    if st != DSA_OK:
-        raise DSAError(st, name)
-
-
-def _scratch(t: torch.Tensor, dev: torch.device, size_fn, *sizes) -> torch.Tensor:
-    """A workspace of size_fn(*sizes) bytes (asked on dev), beside tensor t."""
-    if torch.cuda.current_device() == dev.index:
-        need = size_fn(*sizes)
-    else:
-        with torch.cuda.device(dev):
-            need = size_fn(*sizes)
-    return t.new_empty(need // t.element_size() + 1)
-
-
-def _int32(*named) -> None:
-    for name, t in named:
-        if t is not None and t.dtype != torch.int32:
-            raise TypeError(f"{name} must be int32")
-
-
-def _rows(name: str, t: torch.Tensor, dev: torch.device) -> int:
-    """Distance between the rows of a [rows, heads, dim] operand, in elements:
-    rows may be strided (views of a fused projection), heads and dims dense."""
-    if t.device != dev:
-        raise ValueError("tensors on different devices")
-    n, heads, dim = t.shape
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
-        raise ValueError(f"{name}: the heads and dims of a row must be contiguous")
-    return t.stride(0) if n > 1 else heads * dim
-
-
-def _paged_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale, v_scale) -> int:
-    """Checks a cache pair's shapes; its type code."""
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
-        raise ValueError("k_cache and v_cache must be [num_pages, n_kv_heads, page_size, head_dim] of one type")
-    for s in (k_scale, v_scale):
-        if s is not None and (s.dtype != torch.float32 or s.shape != k_cache.shape[:3]):
-            raise ValueError("scales must be fp32 [num_pages, n_kv_heads, page_size]")
-    return _dt(k_cache)
+_gqa.set_error(DSAError)
 
 
 def kv_cache_append(k: torch.Tensor, v: torch.Tensor, row_batch: torch.Tensor, row_pos: torch.Tensor,
@@ -454,20 +410,7 @@ def kv_cache_append(k: torch.Tensor, v: torch.Tensor, row_batch: torch.Tensor, r
     strided) to token row_pos[r] of sequence row_batch[r] of the paged caches
     [num_pages, n_kv_heads, page_size, head_dim] (row_pos < 0: not stored).
     fp8 caches (float8_e4m3fn or uint8) take scales [num_pages, n_kv_heads, page_size]."""
-    dev = _dev(row_batch, row_pos, page_table, k_cache, v_cache, k_scale, v_scale)
-    _int32(("row_batch", row_batch), ("row_pos", row_pos), ("page_table", page_table))
-    kv = _paged_kv(k_cache, v_cache, k_scale, v_scale)
-    pages, hkv, page, d = k_cache.shape
-    n = k.shape[0]
-    if k.shape != (n, hkv, d) or v.shape != k.shape or v.dtype != k.dtype:
-        raise ValueError("k and v must be [n, n_kv_heads, head_dim] of one type")
-    if row_batch.shape != (n,) or row_pos.shape != (n,):
-        raise ValueError("row_batch and row_pos must be [n]")
-    ld_k, ld_v = _rows("k", k, dev), _rows("v", v, dev)
-    batch, width = page_table.shape
-    _call("kv_cache_append", dev, k.data_ptr(), ld_k, v.data_ptr(), ld_v, _dt(k), row_batch.data_ptr(), row_pos.data_ptr(),
-          n, page_table.data_ptr(), batch, width, page, pages, hkv, d, k_cache.data_ptr(), v_cache.data_ptr(), kv,
-          _ptr(k_scale), _ptr(v_scale))
+    _gqa.append(k, v, row_batch, row_pos, page_table, k_cache, v_cache, k_scale, v_scale)
 
 
 def gqa_decode_attention_workspace_size(rows: int, n_heads: int, n_kv_heads: int, head_dim: int,
@@ -485,32 +428,7 @@ def gqa_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     strided) over tokens 0 .. row_pos[t] of sequence row_batch[t] of the paged
     caches: (out [rows, n_heads, head_dim], lse [rows, n_heads] fp32).
     row_pos < 0: nothing visible (out = 0, lse = -inf)."""
-    dev = _dev(k_cache, v_cache, page_table, row_batch, row_pos, k_scale, v_scale, out, lse, workspace)
-    _int32(("page_table", page_table), ("row_batch", row_batch), ("row_pos", row_pos))
-    kv = _paged_kv(k_cache, v_cache, k_scale, v_scale)
-    pages, hkv, page, d = k_cache.shape
-    rows, H, d_q = q.shape
-    if d_q != d:
-        raise ValueError("q and the caches differ in head_dim")
-    if row_batch.shape != (rows,) or row_pos.shape != (rows,):
-        raise ValueError("row_batch and row_pos must be [rows]")
-    ld_q = _rows("q", q, dev)
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    elif out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("out must be [rows, n_heads, head_dim] of q's type")
-    if lse is None:
-        lse = q.new_empty((rows, H), dtype=torch.float32)
-    elif lse.shape != (rows, H) or lse.dtype != torch.float32:
-        raise ValueError("lse must be fp32 [rows, n_heads]")
-    batch, width = page_table.shape
-    if workspace is None:
-        workspace = _scratch(q, dev, _lib.gqa_decode_attention_workspace_size, rows, H, hkv, d, kv)
-    _call("gqa_decode_attention", dev, q.data_ptr(), ld_q, _dt(q), k_cache.data_ptr(), v_cache.data_ptr(), kv,
-          _ptr(k_scale), _ptr(v_scale), page_table.data_ptr(), batch, width, page, pages, row_batch.data_ptr(),
-          row_pos.data_ptr(), rows, H, hkv, d, float(scale), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-          workspace.nbytes)
-    return out, lse
+    return _gqa.decode(q, k_cache, v_cache, page_table, row_batch, row_pos, scale, k_scale, v_scale, out, lse, workspace)
 
 
 def gqa_prompt_attention_workspace_size(total: int, n_seqs: int, n_heads: int, head_dim: int,
@@ -527,78 +445,21 @@ def gqa_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_s
     strided), cu_seqlens int32 [n_seqs + 1]: (out [total, n_heads, head_dim],
     lse [total, n_heads] fp32).  Rows outside every prompt are left as they
     were in out and lse (undefined when these are allocated here)."""
-    dev = _dev(cu_seqlens, out, lse, workspace)
-    _int32(("cu_seqlens", cu_seqlens))
-    T, H, d = q.shape
-    hkv = k.shape[1]
-    if k.shape != (T, hkv, d) or v.shape != k.shape or k.dtype != q.dtype or v.dtype != q.dtype:
-        raise ValueError("k and v must be [total, n_kv_heads, head_dim] of q's type")
-    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
-        raise ValueError("cu_seqlens must be [n_seqs + 1]")
-    n_seqs = cu_seqlens.shape[0] - 1
-    ld_q, ld_k, ld_v = _rows("q", q, dev), _rows("k", k, dev), _rows("v", v, dev)
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    elif out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("out must be [total, n_heads, head_dim] of q's type")
-    if lse is None:
-        lse = q.new_empty((T, H), dtype=torch.float32)
-    elif lse.shape != (T, H) or lse.dtype != torch.float32:
-        raise ValueError("lse must be fp32 [total, n_heads]")
-    dt = _dt(q)
-    if workspace is None:
-        workspace = _scratch(q, dev, _lib.gqa_prompt_attention_workspace_size, T, n_seqs, H, d, dt)
-    _call("gqa_prompt_attention", dev, q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v, dt,
-          cu_seqlens.data_ptr(), n_seqs, T, H, hkv, d, float(scale), out.data_ptr(), lse.data_ptr(),
-          workspace.data_ptr(), workspace.nbytes)
-    return out, lse
-
-
-def _books(page_table: torch.Tensor, seq_len: torch.Tensor, ref_count: torch.Tensor, *lists) -> Tuple[torch.device, int]:
-    """Checks a pool's books and lists: (device, list entries)."""
-    dev = _dev(page_table, seq_len, ref_count, *lists)
-    for t in (page_table, seq_len, ref_count, *lists):
-        if t.dtype != torch.int32:
-            raise TypeError("page tables, lengths, counts and lists must be int32")
-    if page_table.dim() != 2 or seq_len.shape != (page_table.shape[0],) or ref_count.dim() != 1:
-        raise ValueError("page_table [batch, max_pages], seq_len [batch] and ref_count [num_pages] are needed")
-    n = lists[0].numel() if lists else 0
-    for t in lists:
-        if t.shape != (n,):
-            raise ValueError("lists must be [n], of one length")
-    return dev, n
-
-
-def _cache_list(caches, num_pages: int, dev: torch.device):
-    """A list of caches [num_pages, ...] as C arrays: (pointers, page bytes, count)."""
-    n = len(caches)
-    ptrs, sizes = (_vp * n)(), (_sz * n)()
-    for i, c in enumerate(caches):
-        if c.device != dev or not c.is_contiguous() or c.dim() < 1 or c.shape[0] != num_pages:
-            raise ValueError("caches must be contiguous [num_pages, ...] tensors on the pool's device")
-        ptrs[i] = c.data_ptr()
-        sizes[i] = c.numel() // num_pages * c.element_size() if num_pages else 0
-    return ptrs, sizes, n
+    return _gqa.prompt(q, k, v, cu_seqlens, scale, out, lse, workspace)
 
 
 def kv_pages_extend(page_table: torch.Tensor, seq_len: torch.Tensor, ref_count: torch.Tensor, seqs: torch.Tensor,
                     add: torch.Tensor, page_size: int) -> None:
     """Room for add[i] more tokens in sequence seqs[i]: fresh pages (lowest
     free ids first) and seq_len grown, in place."""
-    dev, n = _books(page_table, seq_len, ref_count, seqs, add)
-    batch, width = page_table.shape
-    _call("kv_pages_extend", dev, page_table.data_ptr(), batch, width, page_size, seq_len.data_ptr(), ref_count.data_ptr(),
-          ref_count.shape[0], seqs.data_ptr(), add.data_ptr(), n)
+    _gqa.extend(page_table, seq_len, ref_count, seqs, add, page_size)
 
 
 def kv_pages_free(page_table: torch.Tensor, seq_len: torch.Tensor, ref_count: torch.Tensor, seqs: torch.Tensor,
                   page_size: int) -> None:
     """Drop sequences seqs[i]: their pages' counts go down, their table rows
     and lengths are cleared, in place."""
-    dev, n = _books(page_table, seq_len, ref_count, seqs)
-    batch, width = page_table.shape
-    _call("kv_pages_free", dev, page_table.data_ptr(), batch, width, page_size, seq_len.data_ptr(), ref_count.data_ptr(),
-          ref_count.shape[0], seqs.data_ptr(), n)
+    _gqa.free(page_table, seq_len, ref_count, seqs, page_size)
 
 
 def kv_pages_fork(page_table: torch.Tensor, seq_len: torch.Tensor, ref_count: torch.Tensor, parents: torch.Tensor,
@@ -606,30 +467,14 @@ def kv_pages_fork(page_table: torch.Tensor, seq_len: torch.Tensor, ref_count: to
     """Empty sequence children[i] becomes a branch of parents[i]: full pages
     shared, a last page that is not full copied to a fresh page in every
     cache of `caches` ([num_pages, ...] tensors), in place."""
-    dev, n = _books(page_table, seq_len, ref_count, parents, children)
-    ptrs, sizes, n_caches = _cache_list(caches, ref_count.shape[0], dev)
-    if workspace is None:
-        workspace = parents.new_empty(_lib.kv_pages_fork_workspace_size(n) // 4 + 1)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the pool's device")
-    batch, width = page_table.shape
-    _call("kv_pages_fork", dev, page_table.data_ptr(), batch, width, page_size, seq_len.data_ptr(), ref_count.data_ptr(),
-          ref_count.shape[0], parents.data_ptr(), children.data_ptr(), n, ptrs, sizes, n_caches, workspace.data_ptr(),
-          workspace.nbytes)
+    _gqa.fork(page_table, seq_len, ref_count, parents, children, page_size, caches, workspace)
 
 
 def kv_pages_copy(caches, src: torch.Tensor, dst: torch.Tensor) -> None:
     """Copy page src[i] over page dst[i] in every cache of `caches` ([num_pages,
     ...] tensors); pairs with a -1 are skipped."""
-    dev = _dev(src, dst)
-    _int32(("src", src), ("dst", dst))
-    if src.dim() != 1 or src.shape != dst.shape:
-        raise ValueError("src and dst must be [n]")
-    if not caches:
-        return
-    pages = caches[0].shape[0]
-    ptrs, sizes, n_caches = _cache_list(caches, pages, dev)
-    _call("kv_pages_copy", dev, ptrs, sizes, n_caches, pages, src.data_ptr(), dst.data_ptr(), src.shape[0])
+    if len(caches):
+        _gqa.copy(caches, src, dst, caches[0].shape[0])
 
 
 def kv_pages_compact(page_table: torch.Tensor, ref_count: torch.Tensor, caches=(),
@@ -638,22 +483,7 @@ def kv_pages_compact(page_table: torch.Tensor, ref_count: torch.Tensor, caches=(
     """Draw the pages in use together at the pool's lowest ids, moving the
     fewest pages in every cache of `caches`: (new table, new counts), written
     to table_out / ref_out (which may be the inputs) when given."""
-    dev = _dev(page_table, ref_count, table_out, ref_out, workspace)
-    _int32(("page_table", page_table), ("ref_count", ref_count), ("table_out", table_out), ("ref_out", ref_out))
-    if page_table.dim() != 2 or ref_count.dim() != 1:
-        raise ValueError("page_table [batch, max_pages] and ref_count [num_pages] are needed")
-    table_out = torch.empty_like(page_table) if table_out is None else table_out
-    ref_out = torch.empty_like(ref_count) if ref_out is None else ref_out
-    if table_out.shape != page_table.shape or ref_out.shape != ref_count.shape:
-        raise ValueError("table_out and ref_out must have their inputs' shapes")
-    pages = ref_count.shape[0]
-    ptrs, sizes, n_caches = _cache_list(caches, pages, dev)
-    if workspace is None:
-        workspace = ref_count.new_empty(_lib.kv_pages_compact_workspace_size(pages) // 4 + 1)
-    batch, width = page_table.shape
-    _call("kv_pages_compact", dev, page_table.data_ptr(), batch, width, ref_count.data_ptr(), pages, ptrs, sizes, n_caches,
-          table_out.data_ptr(), ref_out.data_ptr(), workspace.data_ptr(), workspace.nbytes)
-    return table_out, ref_out
+    return _gqa.compact(page_table, ref_count, caches, table_out, ref_out, workspace)
 
 
 def get_device_error(device: Optional[torch.device] = None) -> int:
