@@ -445,16 +445,21 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
                             mma16816<FP8>(s[t + 1], qf[kk], b[2], b[3]);
                         }
                 } else {
+                    // (the tiles' products in turn: each tile's are a chain)
 #pragma unroll
-                    for (int i = 0; i < D / 64; ++i)
+                    for (int i = 0; i < D / 64; ++i) {
+                        uint32_t x[WK / 8][4];
 #pragma unroll
                         for (int t = 0; t < WK / 8; ++t) {
-                            const uint4 x = ld_shared_v4(slot + piece_at<ES, RB, false>(t * 8 + r4, 4 * i + c4));
-                            const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                mma16816<FP8>(s[t], qf[4 * i + j], e4m3x2_f16x2(wd[j]), e4m3x2_f16x2(wd[j] >> 16));
+                            const uint4 y = ld_shared_v4(slot + piece_at<ES, RB, false>(t * 8 + r4, 4 * i + c4));
+                            x[t][0] = y.x; x[t][1] = y.y; x[t][2] = y.z; x[t][3] = y.w;
                         }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int t = 0; t < WK / 8; ++t)
+                                mma16816<FP8>(s[t], qf[4 * i + j], e4m3x2_f16x2(x[t][j]), e4m3x2_f16x2(x[t][j] >> 16));
+                    }
                 }
                 float2 vs2[WK / 8];
                 if (FP8) {
