@@ -5,7 +5,7 @@
 // so the cache's bytes at the HBM rate are the floor.
 //
 // Work split.  A pair is (row, kv head, tile of the group's heads); its keys
-// are cut into units of KT (64, or 128 over an fp8 cache).  All pairs' units form
+// are cut into units of KT (128, in fp32 64).  All pairs' units form
 // one line, and block i of the grid takes the i-th equal stretch of it, whatever the rows' lengths:
 // ragged batches load every SM alike, and one long row uses the whole GPU.
 // Lengths are read on the device (nothing about them is known to the host),
@@ -152,21 +152,25 @@ template <int KT> __device__ __forceinline__ int cache_row(const DecodeArgs& a, 
 // ------------------------------------------------------------ the kernel --
 //
 // The work is bound by the cache's bytes, so the kernel is built around its
-// loads: each warp owns 16 (fp8: 32) keys of a unit and streams their K and V
+// loads: each warp owns 32 (fp32: 16) keys of a unit and streams their K and V
 // rows through a ring of its own (cp.async, 16 bytes per lane, rows of unused
 // places zero-filled), never waiting for another warp while a pair lasts.
-// With up to 16 heads of a group as the M of mma.m16n8, one slice costs a warp
-// a few dozen products and one softmax step in registers: a small part of an
-// SM's issue slots at the HBM rate, which is why the products need no more
-// than the warp-level tensor instruction (M = 128 of tcgen05 would be filled
-// to an eighth).  Groups of up to 8 heads leave rows 8-15 of the products
-// unused: they are fed zeros (fp32: see below).
+//
+// The products are formed transposed, with the cache as the M operand of
+// mma.m16n8 and eight heads as N:
+//   S^T [keys x heads] = K Q^T,     O^T [dims x heads] += V^T P^T
+// so that a group of up to 8 heads fills the tensor instruction (with heads
+// as M, half of it would be idle and twice the registers taken); P^T goes from
+// the first product's result to the second's operand by 8 x 8 transposes in
+// registers.  A slice costs a warp a few dozen products and one softmax step:
+// a small part of an SM's issue slots at the HBM rate, which is why the
+// products need no more than the warp-level instruction (M = 128 of tcgen05
+// would serve 128 keys at a time and leave the softmax across lanes).
 //
 // Which dims a k-step of the first product holds is free as long as Q and K
-// agree, and so is which dim a column of the output holds and which key a
-// k-step of the second product holds.  bf16 uses ldmatrix and the plain
-// order; fp8 and fp32 choose the orders so that a lane reads its keys as
-// 16-byte pieces.
+// agree, and so is which dim a row of O^T holds and which key a k-step of the
+// second product holds.  bf16 uses ldmatrix and the plain order; fp8 and fp32
+// choose the orders so that a lane reads its keys as 16-byte pieces.
 //
 // fp8: codes are widened to f16 (exact) on the way into the product.  The
 // query row is first brought to [1, 2) by a power of two, so that f16 holds
@@ -174,14 +178,13 @@ template <int KT> __device__ __forceinline__ int cache_row(const DecodeArgs& a, 
 // P is taken times the value scale relative to the largest scale met so far,
 // which the output carries like the running maximum.
 //
-// fp32: every factor is split into two tf32 numbers, x = hi + lo.  The unused
-// half of the product's rows takes the lo parts of the eight heads, so two
-// tensor products (with the keys' hi and lo parts) give all four partial
-// products.  What rounding lo loses is at most 2^-22 of a factor, no more than
-// a dot product of a few fp32 terms; the multiply-adds on the CUDA cores would
-// take three times the instructions.
+// fp32: every factor is split into two tf32 numbers, x = hi + lo (11 + 11
+// bits), and a product is three tensor products hi hi + hi lo + lo hi, the
+// small ones summed apart.  What is left out or rounded is at most 3 x 2^-22
+// of |x y| a term.  The tensor core's sums round toward zero, so each slice's
+// output is summed from zero and added to the running one in fp32.
 template <typename KV, int D> struct MmaCfg;
-template <int D> struct MmaCfg<__nv_bfloat16, D> { static constexpr int WK = 16, STAGES = 3, BLOCKS = 2; };
+template <int D> struct MmaCfg<__nv_bfloat16, D> { static constexpr int WK = 32, STAGES = 2, BLOCKS = D == 64 ? 2 : 1; };
 template <int D> struct MmaCfg<__nv_fp8_e4m3, D> { static constexpr int WK = 32, STAGES = 2, BLOCKS = 3; };
 template <int D> struct MmaCfg<float, D> { static constexpr int WK = 16, STAGES = D == 64 ? 3 : 2, BLOCKS = D == 64 ? 2 : 1; };
 
@@ -218,14 +221,12 @@ __device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], u
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// fp32 product of eight rows: A holds their hi parts in rows 0-7 and their lo
-// parts in rows 8-15, so the sum of C's halves is the product's.
-__device__ __forceinline__ void mma_split(float (&c)[4], const uint32_t (&a)[4], float b0, float b1) {
-    uint32_t h0, l0, h1, l1;
-    split(b0, h0, l0);
-    split(b1, h1, l1);
-    mma1688(c, a, l0, l1);
-    mma1688(c, a, h0, h1);
+// 8 x 8 transpose of 16-bit numbers: lane (r4, c4) gives row r4, columns 2 c4
+// and 2 c4 + 1, and gets column r4, rows 2 c4 and 2 c4 + 1.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
 }
 
 template <bool F16> __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -262,11 +263,10 @@ template <int ES, int RB, bool IS_V> __device__ __forceinline__ uint32_t piece_a
     return r * RB + ((RB == 128 ? c ^ ((r & 1) << 2) : c) << 4);
 }
 
-// Place (in floats) of dim d of row r in the exchange buffer of the warps'
+// Place (in floats) of dim d of head r in the exchange buffer of the warps'
 // outputs: 16-byte pieces swizzled among the eight of a 128-byte line.
 template <int D> __device__ __forceinline__ int exch_at(int r, int d) {
-    const int g = d >> 2;
-    return r * D + (((g ^ (((g >> 3) & 3) | ((r & 1) << 2)))) << 2) + (d & 3);
+    return r * D + (((d >> 2) ^ (((r >> 1) & 3) << 1)) << 2) + (d & 3);
 }
 
 template <typename KV, int D, int GT>
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
     constexpr int STAGES = MmaCfg<KV, D>::STAGES;
     constexpr uint32_t ALL = WK == 32 ? 0xffffffffu : 0xffffu;
     constexpr int SLOT = 2 * SLICE + (FP8 ? 2 * WK * 4 : 0) + 16;   // K, V, scales, the mask of valid keys
-    constexpr int KS = D / 16, NT = D / 8;
+    constexpr int KS = D / 16, MT = WK / 16, NG = GT / 8;   // k-steps; tiles of 16 keys, of 8 heads
     static_assert(!FP8 || WK == 32, "a lane per key's scales");
     static_assert(!FP32 || GT == 8, "fp32 takes eight heads");
     static_assert(2 * SLICE >= 8 * D * 4, "the outputs of 8 heads are exchanged in a slot");
@@ -342,69 +342,78 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
         if (w.unit == 0 && w.kvh == 0 && w.tile == 0 && tid == 0 &&
             (w.batch < 0 || w.batch >= a.batch || __ldg(a.row_pos + w.row) >= (int64_t)a.max_pages * a.page_size))
             record_error(a.err, DEV_ERR_BAD_INDEX);     // reported once per row, by the block that begins it
-        // Q fragments: rows r4 and r4 + 8 (heads); k-step kk holds dims
+        // Q fragments: head 8 g + r4; k-step kk holds dims
         // 16 kk + {2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9} (bf16), or
         // 64 (kk / 4) + 16 c4 + 4 (kk % 4) + {0, 1, 2, 3} (fp8), or, as two
-        // k-steps of 8, 16 kk + 4 c4 + {0, 1} and {2, 3} (fp32)
-        uint32_t qf[KS][4];
-        uint32_t q32[FP32 ? KS : 1][2][4];
-        float zs[2] = {a.scale_log2, a.scale_log2};
+        // k-steps of 8, 16 kk + 4 c4 + {0, 1} and {2, 3} (fp32: hi, then lo)
+        uint32_t qf[KS][FP32 ? 8 : 2 * NG];
+        float zs[NG][2];                            // score scale of heads 8 g + 2 c4 + {0, 1}
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const bool on = (half == 0 || GT > 8) && r4 + 8 * half < heads;
-            const int64_t at_q = (int64_t)w.row * a.ld_q + (h0 + (on ? r4 + 8 * half : 0)) * D;
+        for (int g = 0; g < NG; ++g) {
+            const bool on = 8 * g + r4 < heads;
+            const int64_t at_q = (int64_t)w.row * a.ld_q + (h0 + (on ? 8 * g + r4 : 0)) * D;
             const __nv_bfloat16* q = (const __nv_bfloat16*)a.q + at_q;
+            zs[g][0] = zs[g][1] = a.scale_log2;
             if constexpr (FP32) {
-                if (half == 0) {
-#pragma unroll
-                    for (int kk = 0; kk < KS; ++kk) {
-                        const float4 x = on ? __ldg((const float4*)((const float*)a.q + at_q + 16 * kk + 4 * c4))
-                                            : make_float4(0.f, 0.f, 0.f, 0.f);
-                        split(x.x, q32[kk][0][0], q32[kk][0][1]);
-                        split(x.y, q32[kk][0][2], q32[kk][0][3]);
-                        split(x.z, q32[kk][1][0], q32[kk][1][1]);
-                        split(x.w, q32[kk][1][2], q32[kk][1][3]);
-                    }
-                }
-            } else if (!FP8) {
 #pragma unroll
                 for (int kk = 0; kk < KS; ++kk) {
-                    qf[kk][half] = on ? __ldg((const uint32_t*)(q + 16 * kk + 2 * c4)) : 0u;
-                    qf[kk][half + 2] = on ? __ldg((const uint32_t*)(q + 16 * kk + 2 * c4 + 8)) : 0u;
+                    const float4 x = on ? __ldg((const float4*)((const float*)a.q + at_q + 16 * kk + 4 * c4))
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+                    split(x.x, qf[kk][0], qf[kk][4]);
+                    split(x.y, qf[kk][1], qf[kk][5]);
+                    split(x.z, qf[kk][2], qf[kk][6]);
+                    split(x.w, qf[kk][3], qf[kk][7]);
+                }
+            } else if constexpr (!FP8) {
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk) {
+                    qf[kk][2 * g] = on ? __ldg((const uint32_t*)(q + 16 * kk + 2 * c4)) : 0u;
+                    qf[kk][2 * g + 1] = on ? __ldg((const uint32_t*)(q + 16 * kk + 2 * c4 + 8)) : 0u;
                 }
             } else {
-                uint32_t raw[KS][2];
                 float top = 0.f;
 #pragma unroll
                 for (int kk = 0; kk < KS; ++kk) {
                     const uint2 x = on ? __ldg((const uint2*)(q + 64 * (kk / 4) + 16 * c4 + 4 * (kk % 4))) : make_uint2(0u, 0u);
-                    raw[kk][0] = x.x;
-                    raw[kk][1] = x.y;
+                    qf[kk][2 * g] = x.x;
+                    qf[kk][2 * g + 1] = x.y;
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(raw[kk][e] << 16)),
-                                               fabsf(__uint_as_float(raw[kk][e] & 0xFFFF0000u))));
+                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[kk][2 * g + e] << 16)),
+                                               fabsf(__uint_as_float(qf[kk][2 * g + e] & 0xFFFF0000u))));
                 }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 // 2^e <= top < 2^(e + 1), e kept where 2^-e is a normal number
                 const int e = min(max((int)(__float_as_uint(top) >> 23), 1), 253) - 127;
                 const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-                zs[half] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+                const float up = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);     // of head r4
 #pragma unroll
                 for (int kk = 0; kk < KS; ++kk)
 #pragma unroll
-                    for (int e2 = 0; e2 < 2; ++e2)
-                        qf[kk][half + 2 * e2] = pack2<true>(__uint_as_float(raw[kk][e2] << 16) * down,
-                                                            __uint_as_float(raw[kk][e2] & 0xFFFF0000u) * down);
+                    for (int i = 2 * g; i < 2 * g + 2; ++i)
+                        qf[kk][i] = pack2<true>(__uint_as_float(qf[kk][i] << 16) * down,
+                                                __uint_as_float(qf[kk][i] & 0xFFFF0000u) * down);
+                zs[g][0] = __shfl_sync(0xffffffffu, up, 8 * c4);
+                zs[g][1] = __shfl_sync(0xffffffffu, up, 8 * c4 + 4);
             }
         }
-        float o[NT][4];
+        // O^T: tile t, rows (dims) r4 and r4 + 8, columns (heads) 8 g + 2 c4 + {0, 1}
+        float o[KS][NG][4];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < KS; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, vref = 0.f, vinv = 0.f;
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[t][g][e] = 0.f;
+        float m[NG][2], l[NG][2], vref = 0.f, vinv = 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m[g][e] = -INFINITY;
+                l[g][e] = 0.f;
+            }
 
         for (int u = 0; u < n; ++u) {
             cp_async_wait<STAGES - 1>();
@@ -413,42 +422,57 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
             const uint32_t kb = smem_u32(slot), vb = kb + SLICE;
             const uint32_t valid = *(const uint32_t*)(slot + SLOT - 16);
             if (valid) {
-                // S = Q K^T: tiles of 8 keys; lane: rows r4 / r4 + 8, keys 8 t + 2 c4 + {0, 1}
-                float s[WK / 8][4];
+                // S^T: keys 16 t + r4 (+ 8), heads 8 g + 2 c4 + {0, 1}
+                float s[MT][NG][4];
 #pragma unroll
-                for (int t = 0; t < WK / 8; ++t)
+                for (int t = 0; t < MT; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+                    for (int g = 0; g < NG; ++g)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[t][g][e] = 0.f;
                 if constexpr (FP32) {
+                    float small[MT][4];             // the products with a lo part
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) small[t][e] = 0.f;
 #pragma unroll
                     for (int kk = 0; kk < KS; ++kk)
 #pragma unroll
-                        for (int t = 0; t < WK / 8; ++t) {
-                            const uint4 x = ld_shared_v4(slot + piece_at<ES, RB, false>(t * 8 + r4, 4 * kk + c4));
-                            mma_split(s[t], q32[kk][0], __uint_as_float(x.x), __uint_as_float(x.y));
-                            mma_split(s[t], q32[kk][1], __uint_as_float(x.z), __uint_as_float(x.w));
+                        for (int t = 0; t < MT; ++t) {
+                            const uint4 x = ld_shared_v4(slot + piece_at<ES, RB, false>(t * 16 + r4, 4 * kk + c4));
+                            const uint4 y = ld_shared_v4(slot + piece_at<ES, RB, false>(t * 16 + r4 + 8, 4 * kk + c4));
+                            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                uint32_t hi[4], lo[4];
+                                split(__uint_as_float(xs[2 * i]), hi[0], lo[0]);
+                                split(__uint_as_float(ys[2 * i]), hi[1], lo[1]);
+                                split(__uint_as_float(xs[2 * i + 1]), hi[2], lo[2]);
+                                split(__uint_as_float(ys[2 * i + 1]), hi[3], lo[3]);
+                                mma1688(s[t][0], hi, qf[kk][2 * i], qf[kk][2 * i + 1]);
+                                mma1688(small[t], lo, qf[kk][2 * i], qf[kk][2 * i + 1]);
+                                mma1688(small[t], hi, qf[kk][2 * i + 4], qf[kk][2 * i + 5]);
+                            }
                         }
 #pragma unroll
-                    for (int t = 0; t < WK / 8; ++t) {
-                        s[t][0] += s[t][2];
-                        s[t][1] += s[t][3];
-                    }
-                } else if (!FP8) {
+                    for (int t = 0; t < MT; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[t][0][e] += small[t][e];
+                } else if constexpr (!FP8) {
 #pragma unroll
                     for (int kk = 0; kk < KS; ++kk)
 #pragma unroll
-                        for (int t = 0; t < WK / 8; t += 2) {
-                            uint32_t b[4];
-                            ldmatrix_x4(b, kb + piece_at<ES, RB, false>(t * 8 + (lane >> 4) * 8 + (lane & 7),
-                                                                         kk * 2 + ((lane >> 3) & 1)));
-                            mma16816<FP8>(s[t], qf[kk], b[0], b[1]);
-                            mma16816<FP8>(s[t + 1], qf[kk], b[2], b[3]);
+                        for (int t = 0; t < MT; ++t) {
+                            uint32_t x[4];
+                            ldmatrix_x4(x, kb + piece_at<ES, RB, false>(t * 16 + (lane & 15), kk * 2 + (lane >> 4)));
+#pragma unroll
+                            for (int g = 0; g < NG; ++g) mma16816<FP8>(s[t][g], x, qf[kk][2 * g], qf[kk][2 * g + 1]);
                         }
                 } else {
-                    // (the tiles' products in turn: each tile's are a chain)
 #pragma unroll
                     for (int i = 0; i < D / 64; ++i) {
-                        uint32_t x[WK / 8][4];
+                        uint32_t x[WK / 8][4];      // (keys 8 t + r4)
 #pragma unroll
                         for (int t = 0; t < WK / 8; ++t) {
                             const uint4 y = ld_shared_v4(slot + piece_at<ES, RB, false>(t * 8 + r4, 4 * i + c4));
@@ -457,52 +481,66 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
 #pragma unroll
-                            for (int t = 0; t < WK / 8; ++t)
-                                mma16816<FP8>(s[t], qf[4 * i + j], e4m3x2_f16x2(x[t][j]), e4m3x2_f16x2(x[t][j] >> 16));
+                            for (int t = 0; t < MT; ++t) {
+                                const uint32_t k16[4] = {e4m3x2_f16x2(x[2 * t][j]), e4m3x2_f16x2(x[2 * t + 1][j]),
+                                                         e4m3x2_f16x2(x[2 * t][j] >> 16), e4m3x2_f16x2(x[2 * t + 1][j] >> 16)};
+#pragma unroll
+                                for (int g = 0; g < NG; ++g)
+                                    mma16816<FP8>(s[t][g], k16, qf[4 * i + j][2 * g], qf[4 * i + j][2 * g + 1]);
+                            }
                     }
                 }
-                float2 vs2[WK / 8];
+                float vs[WK / 8];                   // value scales of keys 8 t + r4
                 if (FP8) {
                     const float* ks = (const float*)(slot + 2 * SLICE);
 #pragma unroll
                     for (int t = 0; t < WK / 8; ++t) {
-                        const float2 k2 = *(const float2*)(ks + t * 8 + 2 * c4);
-                        vs2[t] = *(const float2*)(ks + WK + t * 8 + 2 * c4);
-                        s[t][0] *= k2.x; s[t][1] *= k2.y;
-                        if (GT > 8) { s[t][2] *= k2.x; s[t][3] *= k2.y; }
+                        const float k1 = ks[t * 8 + r4];
+                        vs[t] = ks[WK + t * 8 + r4];
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            s[t / 2][g][2 * (t & 1)] *= k1;
+                            s[t / 2][g][2 * (t & 1) + 1] *= k1;
+                        }
                     }
                 }
                 if (valid != ALL) {
 #pragma unroll
                     for (int t = 0; t < WK / 8; ++t)
+                        if (!((valid >> (t * 8 + r4)) & 1u)) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (!((valid >> (t * 8 + 2 * c4 + (e & 1))) & 1u)) s[t][e] = -INFINITY;
+                            for (int g = 0; g < NG; ++g) s[t / 2][g][2 * (t & 1)] = s[t / 2][g][2 * (t & 1) + 1] = -INFINITY;
+                        }
                 }
                 // running maximum (scores times zs; zs > 0), and the output brought to it
-                float f[2] = {1.f, 1.f};
+                float f[NG][2];
                 bool moved = false;
 #pragma unroll
-                for (int half = 0; half < (GT > 8 ? 2 : 1); ++half) {
-                    float top = fmaxf(s[0][2 * half], s[0][2 * half + 1]);
+                for (int g = 0; g < NG; ++g)
 #pragma unroll
-                    for (int t = 1; t < WK / 8; ++t) top = fmaxf(top, fmaxf(s[t][2 * half], s[t][2 * half + 1]));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) * zs[half];
-                    if (top > m[half]) {
-                        f[half] = fast_exp2(m[half] - top);
-                        m[half] = top;
-                        l[half] *= f[half];
-                        moved = true;
+                    for (int e = 0; e < 2; ++e) {
+                        float top = fmaxf(s[0][g][e], s[0][g][2 + e]);
+#pragma unroll
+                        for (int t = 1; t < MT; ++t) top = fmaxf(top, fmaxf(s[t][g][e], s[t][g][2 + e]));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)) * zs[g][e];
+                        f[g][e] = 1.f;
+                        if (top > m[g][e]) {
+                            f[g][e] = fast_exp2(m[g][e] - top);
+                            m[g][e] = top;
+                            l[g][e] *= f[g][e];
+                            moved = true;
+                        }
                     }
-                }
                 float vmove = 1.f;
                 if (FP8) {
-                    float top = fmaxf(fabsf(vs2[0].x), fabsf(vs2[0].y));
+                    float top = fabsf(vs[0]);
 #pragma unroll
-                    for (int t = 1; t < WK / 8; ++t) top = fmaxf(top, fmaxf(fabsf(vs2[t].x), fabsf(vs2[t].y)));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)), 1e-30f);   // its reciprocal is finite
+                    for (int t = 1; t < WK / 8; ++t) top = fmaxf(top, fabsf(vs[t]));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                    top = fmaxf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)), 1e-30f);   // its reciprocal is finite
                     if (top > vref) {
                         vmove = vref / top;
                         vref = top;
@@ -512,85 +550,118 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
                 }
                 if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        o[t][0] *= f[0] * vmove; o[t][1] *= f[0] * vmove;
-                        if (GT > 8) { o[t][2] *= f[1] * vmove; o[t][3] *= f[1] * vmove; }
-                        if (FP32) { o[t][2] *= f[0]; o[t][3] *= f[0]; }
-                    }
+                    for (int t = 0; t < KS; ++t)
+#pragma unroll
+                        for (int g = 0; g < NG; ++g)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[t][g][e] *= f[g][e & 1] * vmove;
                 }
-                // P (as the A operand, 16 keys a piece), and O += P V
-                uint32_t pf[WK / 16][4];
-                uint32_t p32[FP32 ? WK / 8 : 1][4];     // keys 8 t + 2 c4 + {0, 1}
 #pragma unroll
-                for (int t = 0; t < WK / 8; ++t) {
-                    pf[t / 2][2 * (t & 1) + 1] = 0u;
+                for (int g = 0; g < NG; ++g)
 #pragma unroll
-                    for (int half = 0; half < (GT > 8 ? 2 : 1); ++half) {
-                        const float base = m[half] > -INFINITY ? m[half] : 0.f;
-                        float p0 = fast_exp2(fmaf(s[t][2 * half], zs[half], -base));
-                        float p1 = fast_exp2(fmaf(s[t][2 * half + 1], zs[half], -base));
-                        l[half] += p0 + p1;
-                        if (FP8) {
-                            p0 *= vs2[t].x * vinv;
-                            p1 *= vs2[t].y * vinv;
+                    for (int e = 0; e < 2; ++e) {
+                        const float base = m[g][e] > -INFINITY ? m[g][e] : 0.f;
+#pragma unroll
+                        for (int t = 0; t < MT; ++t)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const float p = fast_exp2(fmaf(s[t][g][2 * i + e], zs[g][e], -base));
+                                l[g][e] += p;
+                                s[t][g][2 * i + e] = FP8 ? p * (vs[2 * t + i] * vinv) : p;
+                            }
+                    }
+                // O^T += V^T P^T
+                if constexpr (FP32) {
+                    // k-step (t, i): keys 16 t + 8 i + 2 c4 (k = c4) and + 1 (k = c4 + 4); P^T's pieces by
+                    // shuffles from the lanes of those keys.  Rows r4 / r4 + 8 of tile j are dims
+                    // (D / 8) r4 + 2 j and + 1.
+                    constexpr int RUN = D / 8;
+                    float step[KS][4];
+#pragma unroll
+                    for (int j = 0; j < KS; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) step[j][e] = 0.f;
+#pragma unroll
+                    for (int ti = 0; ti < 2 * MT; ++ti) {
+                        const int t = ti / 2, i = ti & 1;
+                        uint32_t ph[2], pl[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int from = (2 * c4 + e) * 4 + (r4 >> 1);
+                            const float even = __shfl_sync(0xffffffffu, s[t][0][2 * i], from);
+                            const float odd = __shfl_sync(0xffffffffu, s[t][0][2 * i + 1], from);
+                            split((r4 & 1) ? odd : even, ph[e], pl[e]);
                         }
-                        if constexpr (FP32) {
-                            split(p0, p32[t][0], p32[t][1]);
-                            split(p1, p32[t][2], p32[t][3]);
+                        const int key = 16 * t + 8 * i + 2 * c4;
+#pragma unroll
+                        for (int n4 = 0; n4 < RUN / 4; ++n4) {
+                            const uint4 x = ld_shared_v4(slot + SLICE + piece_at<ES, RB, true>(key, r4 * RUN / 4 + n4));
+                            const uint4 y = ld_shared_v4(slot + SLICE + piece_at<ES, RB, true>(key + 1, r4 * RUN / 4 + n4));
+                            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                uint32_t hi[4], lo[4];
+                                split(__uint_as_float(xs[2 * k]), hi[0], lo[0]);
+                                split(__uint_as_float(xs[2 * k + 1]), hi[1], lo[1]);
+                                split(__uint_as_float(ys[2 * k]), hi[2], lo[2]);
+                                split(__uint_as_float(ys[2 * k + 1]), hi[3], lo[3]);
+                                mma1688(step[2 * n4 + k], lo, ph[0], ph[1]);
+                                mma1688(step[2 * n4 + k], hi, pl[0], pl[1]);
+                                mma1688(step[2 * n4 + k], hi, ph[0], ph[1]);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < KS; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[j][0][e] += step[j][e];
+                } else {
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        uint32_t pf[NG][2];
+#pragma unroll
+                        for (int g = 0; g < NG; ++g)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                pf[g][i] = transpose8(pack2<FP8>(s[t][g][2 * i], s[t][g][2 * i + 1]));
+                        if constexpr (!FP8) {
+                            // rows r4 / r4 + 8 of tile j are dims 16 j + r4 and + 8
+#pragma unroll
+                            for (int j = 0; j < KS; ++j) {
+                                uint32_t x[4];
+                                ldmatrix_x4_t(x, vb + piece_at<ES, RB, true>(t * 16 + (lane >> 4) * 8 + (lane & 7),
+                                                                             2 * j + ((lane >> 3) & 1)));
+#pragma unroll
+                                for (int g = 0; g < NG; ++g) mma16816<FP8>(o[j][g], x, pf[g][0], pf[g][1]);
+                            }
                         } else {
-                            pf[t / 2][half + 2 * (t & 1)] = pack2<FP8>(p0, p1);
-                        }
-                    }
-                }
+                            // rows r4 / r4 + 8 of tile j are dims (D / 8) r4 + 2 j and + 1; keys 2 c4 + {0, 1, 8, 9}
+                            constexpr int RUN = D / 8;
+                            uint32_t x[4][RUN / 4];
 #pragma unroll
-                for (int k16 = 0; k16 < WK / 16; ++k16) {
-                    if constexpr (FP32) {
-                        // column r4 of tile j is dim (D / 8) r4 + j
-                        constexpr int RUN = D / 8;
-#pragma unroll
-                        for (int t = 2 * k16; t < 2 * k16 + 2; ++t)
-#pragma unroll
-                            for (int i = 0; i < RUN / 4; ++i) {
-                                const uint4 x = ld_shared_v4(slot + SLICE + piece_at<ES, RB, true>(8 * t + 2 * c4, r4 * RUN / 4 + i));
-                                const uint4 y = ld_shared_v4(slot + SLICE + piece_at<ES, RB, true>(8 * t + 2 * c4 + 1, r4 * RUN / 4 + i));
-                                mma_split(o[4 * i], p32[t], __uint_as_float(x.x), __uint_as_float(y.x));
-                                mma_split(o[4 * i + 1], p32[t], __uint_as_float(x.y), __uint_as_float(y.y));
-                                mma_split(o[4 * i + 2], p32[t], __uint_as_float(x.z), __uint_as_float(y.z));
-                                mma_split(o[4 * i + 3], p32[t], __uint_as_float(x.w), __uint_as_float(y.w));
+                            for (int k = 0; k < 4; ++k) {
+                                const int key = t * 16 + 2 * c4 + (k & 1) + 8 * (k >> 1);
+                                const uint8_t* src = slot + SLICE + piece_at<ES, RB, true>(key, r4 * RUN / 16) + (r4 * RUN) % 16;
+                                if (RUN == 16) {
+                                    const uint4 v = ld_shared_v4(src);
+                                    x[k][0] = v.x; x[k][1] = v.y; x[k][RUN / 4 - 2] = v.z; x[k][RUN / 4 - 1] = v.w;
+                                } else {
+                                    const uint2 v = *(const uint2*)src;
+                                    x[k][0] = v.x; x[k][1] = v.y;
+                                }
                             }
-                    } else if (!FP8) {
 #pragma unroll
-                        for (int t = 0; t < NT; t += 2) {
-                            uint32_t b[4];
-                            ldmatrix_x4_t(b, vb + piece_at<ES, RB, true>(k16 * 16 + ((lane >> 3) & 1) * 8 + (lane & 7),
-                                                                          t + (lane >> 4)));
-                            mma16816<FP8>(o[t], pf[k16], b[0], b[1]);
-                            mma16816<FP8>(o[t + 1], pf[k16], b[2], b[3]);
-                        }
-                    } else {
-                        // column r4 of tile t is dim (D / 8) r4 + t; keys 2 c4 + {0, 1, 8, 9}
-                        constexpr int RUN = D / 8;
-                        uint32_t x[4][RUN / 4];
+                            for (int j = 0; j < RUN / 4; ++j) {
+                                const uint32_t a0 = __byte_perm(x[0][j], x[1][j], 0x5140), a1 = __byte_perm(x[0][j], x[1][j], 0x7362);
+                                const uint32_t b0 = __byte_perm(x[2][j], x[3][j], 0x5140), b1 = __byte_perm(x[2][j], x[3][j], 0x7362);
+                                const uint32_t v0[4] = {e4m3x2_f16x2(a0), e4m3x2_f16x2(a0 >> 16), e4m3x2_f16x2(b0), e4m3x2_f16x2(b0 >> 16)};
+                                const uint32_t v1[4] = {e4m3x2_f16x2(a1), e4m3x2_f16x2(a1 >> 16), e4m3x2_f16x2(b1), e4m3x2_f16x2(b1 >> 16)};
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int key = k16 * 16 + 2 * c4 + (k & 1) + 8 * (k >> 1);
-                            const uint8_t* src = slot + SLICE + piece_at<ES, RB, true>(key, r4 * RUN / 16) + (r4 * RUN) % 16;
-                            if (RUN == 16) {
-                                const uint4 v = ld_shared_v4(src);
-                                x[k][0] = v.x; x[k][1] = v.y; x[k][RUN / 4 - 2] = v.z; x[k][RUN / 4 - 1] = v.w;
-                            } else {
-                                const uint2 v = *(const uint2*)src;
-                                x[k][0] = v.x; x[k][1] = v.y;
+                                for (int g = 0; g < NG; ++g) {
+                                    mma16816<FP8>(o[2 * j][g], v0, pf[g][0], pf[g][1]);
+                                    mma16816<FP8>(o[2 * j + 1][g], v1, pf[g][0], pf[g][1]);
+                                }
                             }
-                        }
-#pragma unroll
-                        for (int j = 0; j < RUN / 4; ++j) {
-                            const uint32_t a0 = __byte_perm(x[0][j], x[1][j], 0x5140), a1 = __byte_perm(x[0][j], x[1][j], 0x7362);
-                            const uint32_t b0 = __byte_perm(x[2][j], x[3][j], 0x5140), b1 = __byte_perm(x[2][j], x[3][j], 0x7362);
-                            mma16816<FP8>(o[4 * j], pf[k16], e4m3x2_f16x2(a0), e4m3x2_f16x2(b0));
-                            mma16816<FP8>(o[4 * j + 1], pf[k16], e4m3x2_f16x2(a0 >> 16), e4m3x2_f16x2(b0 >> 16));
-                            mma16816<FP8>(o[4 * j + 2], pf[k16], e4m3x2_f16x2(a1), e4m3x2_f16x2(b1));
-                            mma16816<FP8>(o[4 * j + 3], pf[k16], e4m3x2_f16x2(a1 >> 16), e4m3x2_f16x2(b1 >> 16));
                         }
                     }
                 }
@@ -604,36 +675,33 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
         // the four warps' shares of the pair, joined through the slots whose
         // slices were just used (their next loads are requested afterwards)
 #pragma unroll
-        for (int half = 0; half < (GT > 8 ? 2 : 1); ++half) {
-            l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
-            l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
-            if (c4 == 0) s_ml[warp][r4 + 8 * half] = make_float2(m[half], l[half]);
-        }
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[g][e] += __shfl_xor_sync(0xffffffffu, l[g][e], 4);
+                l[g][e] += __shfl_xor_sync(0xffffffffu, l[g][e], 8);
+                l[g][e] += __shfl_xor_sync(0xffffffffu, l[g][e], 16);
+                if (r4 == 0) s_ml[warp][8 * g + 2 * c4 + e] = make_float2(m[g][e], l[g][e]);
+            }
         const bool begins = w.unit == 0, ends = w.unit + n == w.units;
         const int place = 2 * blockIdx.x + (begins ? 1 : 0);
         const float carry = FP8 ? vref : 1.f;
         float* mine = (float*)(ring + st * SLOT);
-        if (FP32) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                o[t][0] += o[t][2];
-                o[t][1] += o[t][3];
-            }
-        }
+        for (int half = 0; half < NG; ++half) {
 #pragma unroll
-        for (int half = 0; half < (GT > 8 ? 2 : 1); ++half) {
+            for (int t = 0; t < KS; ++t)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if (ES == 2) {
-                    *(float2*)(mine + exch_at<D>(r4, 8 * t + 2 * c4)) = make_float2(o[t][2 * half], o[t][2 * half + 1]);
-                } else if ((t & 3) == 0) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        *(float4*)(mine + exch_at<D>(r4, (D / 8) * (2 * c4 + e) + t)) =
-                            make_float4(o[t][2 * half + e] * carry, o[t + 1][2 * half + e] * carry,
-                                        o[t + 2][2 * half + e] * carry, o[t + 3][2 * half + e] * carry);
+                for (int e = 0; e < 2; ++e) {
+                    if (ES == 2) {
+                        mine[exch_at<D>(2 * c4 + e, 16 * t + r4)] = o[t][half][e];
+                        mine[exch_at<D>(2 * c4 + e, 16 * t + r4 + 8)] = o[t][half][2 + e];
+                    } else if ((t & 1) == 0) {
+                        *(float4*)(mine + exch_at<D>(2 * c4 + e, (D / 8) * r4 + 2 * t)) =
+                            make_float4(o[t][half][e] * carry, o[t][half][2 + e] * carry, o[t + 1][half][e] * carry,
+                                        o[t + 1][half][2 + e] * carry);
+                    }
                 }
-            }
             __syncthreads();
             constexpr int VEC = D / 32;
             for (int r = warp; r < 8 && r + 8 * half < heads; r += WARPS) {
@@ -736,7 +804,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 int head_tile(dsa_dtype_t kv, int group) { return kv == DSA_FP32 || group <= 8 ? 8 : 16; }
 int blocks_per_sm(dsa_dtype_t kv, int d) {
     return kv == DSA_FP32   ? (d == 64 ? MmaCfg<float, 64>::BLOCKS : MmaCfg<float, 128>::BLOCKS)
-           : kv == DSA_BF16 ? MmaCfg<__nv_bfloat16, 128>::BLOCKS
+           : kv == DSA_BF16 ? (d == 64 ? MmaCfg<__nv_bfloat16, 64>::BLOCKS : MmaCfg<__nv_bfloat16, 128>::BLOCKS)
                             : MmaCfg<__nv_fp8_e4m3, 128>::BLOCKS;
 }
 
