@@ -235,11 +235,10 @@ template <bool F16> __device__ __forceinline__ uint32_t pack2(float lo, float hi
     else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// Two e4m3 codes (the low half of v) to two f16.
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(v));
-    return r;
+// Four e4m3 codes to f16: the low two, the high two.
+__device__ __forceinline__ void e4m3x4_f16(uint32_t v, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(v));
 }
 __device__ __forceinline__ void cp_async_4(void* dst, const void* src, uint32_t src_bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(src_bytes) : "memory");
@@ -482,8 +481,9 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
                         for (int j = 0; j < 4; ++j)
 #pragma unroll
                             for (int t = 0; t < MT; ++t) {
-                                const uint32_t k16[4] = {e4m3x2_f16x2(x[2 * t][j]), e4m3x2_f16x2(x[2 * t + 1][j]),
-                                                         e4m3x2_f16x2(x[2 * t][j] >> 16), e4m3x2_f16x2(x[2 * t + 1][j] >> 16)};
+                                uint32_t k16[4];
+                                e4m3x4_f16(x[2 * t][j], k16[0], k16[2]);
+                                e4m3x4_f16(x[2 * t + 1][j], k16[1], k16[3]);
 #pragma unroll
                                 for (int g = 0; g < NG; ++g)
                                     mma16816<FP8>(s[t][g], k16, qf[4 * i + j][2 * g], qf[4 * i + j][2 * g + 1]);
@@ -652,10 +652,12 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
                             }
 #pragma unroll
                             for (int j = 0; j < RUN / 4; ++j) {
-                                const uint32_t a0 = __byte_perm(x[0][j], x[1][j], 0x5140), a1 = __byte_perm(x[0][j], x[1][j], 0x7362);
-                                const uint32_t b0 = __byte_perm(x[2][j], x[3][j], 0x5140), b1 = __byte_perm(x[2][j], x[3][j], 0x7362);
-                                const uint32_t v0[4] = {e4m3x2_f16x2(a0), e4m3x2_f16x2(a0 >> 16), e4m3x2_f16x2(b0), e4m3x2_f16x2(b0 >> 16)};
-                                const uint32_t v1[4] = {e4m3x2_f16x2(a1), e4m3x2_f16x2(a1 >> 16), e4m3x2_f16x2(b1), e4m3x2_f16x2(b1 >> 16)};
+                                // the pairs' codes side by side: dims 0, 1 and 2, 3 of keys 0, 1 and of 8, 9
+                                uint32_t v0[4], v1[4];
+                                e4m3x4_f16(__byte_perm(x[0][j], x[1][j], 0x5140), v0[0], v0[1]);
+                                e4m3x4_f16(__byte_perm(x[2][j], x[3][j], 0x5140), v0[2], v0[3]);
+                                e4m3x4_f16(__byte_perm(x[0][j], x[1][j], 0x7362), v1[0], v1[1]);
+                                e4m3x4_f16(__byte_perm(x[2][j], x[3][j], 0x7362), v1[2], v1[3]);
 #pragma unroll
                                 for (int g = 0; g < NG; ++g) {
                                     mma16816<FP8>(o[2 * j][g], v0, pf[g][0], pf[g][1]);
