@@ -5,8 +5,9 @@
 // Every factor is split into two tf32 numbers, x = hi + lo (11 + 11 bits), and a
 // product is three tensor products hi hi + hi lo + lo hi; what is left out or
 // rounded is at most 3 x 2^-22 of |x y| a term, no more than a dot product of a
-// few fp32 terms.  (fp32 multiply-adds on the CUDA cores took 121 us where
-// this takes the time beside the launch.)
+// few fp32 terms.  1800 tokens in 3 prompts, 8 / 4 heads of 64: 65 us (fp32
+// multiply-adds on the CUDA cores: 121 us; tiles of 64 keys, whose registers
+// leave no room to sum the small products apart, 62 us at twice the error).
 //
 // A block takes 64 query rows of one head.  Two groups of 4 warps, 16 rows a
 // warp, walk alternate tiles of the keys with an online softmax each and are
@@ -93,13 +94,15 @@ __device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], u
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // C[t] += A B[t], A's parts in hi / lo, B's as pieces (hi, lo, hi, lo) of k = c4
-// and c4 + 4.  A product's three parts follow one another at a distance of N.
+// and c4 + 4; the products with a lo part go to `small` (which may be C).  A
+// product's three parts follow one another at a distance of N.
 template <int N>
-__device__ __forceinline__ void mma_split(float (*c)[4], const uint32_t (&hi)[4], const uint32_t (&lo)[4], const uint4 (&b)[N]) {
+__device__ __forceinline__ void mma_split(float (*c)[4], float (*small)[4], const uint32_t (&hi)[4], const uint32_t (&lo)[4],
+                                          const uint4 (&b)[N]) {
 #pragma unroll
-    for (int t = 0; t < N; ++t) mma1688(c[t], lo, b[t].x, b[t].z);
+    for (int t = 0; t < N; ++t) mma1688(small[t], lo, b[t].x, b[t].z);
 #pragma unroll
-    for (int t = 0; t < N; ++t) mma1688(c[t], hi, b[t].y, b[t].w);
+    for (int t = 0; t < N; ++t) mma1688(small[t], hi, b[t].y, b[t].w);
 #pragma unroll
     for (int t = 0; t < N; ++t) mma1688(c[t], hi, b[t].x, b[t].z);
 }
@@ -111,7 +114,7 @@ __device__ __forceinline__ float fast_exp2(float x) {
 }
 
 template <int D> struct Cfg {
-    static constexpr int BN = D == 64 ? 64 : 32;                    // keys of a tile
+    static constexpr int BN = 32;                                    // keys of a tile
     static constexpr int KV = BN * D * 8;                           // bytes of a split K (or V) tile
     static constexpr int Q = BM * D * 8;
     static constexpr int SMEM = Q + GROUPS * 2 * KV;
@@ -185,11 +188,13 @@ __global__ void __launch_bounds__(THREADS) gqa_prompt_f32_kernel(const PromptArg
         named_bar_sync(1 + grp, GROUP);
         if (k0 + GROUPS * BN < keys) request(k0 + GROUPS * BN);
         if (k0 > last) continue;                        // all of it lies behind this warp's rows
-        float s[ST][4];
+        // (the tensor core's sums round toward zero: the small products are
+        // summed apart, which takes two thirds of the steps off the scores' sums)
+        float s[ST][4], small[ST][4];
 #pragma unroll
         for (int t = 0; t < ST; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+            for (int e = 0; e < 4; ++e) s[t][e] = small[t][e] = 0.f;
         // k-step kk: dims 8 kk + 2 c4 (k = c4) and 8 kk + 2 c4 + 1 (k = c4 + 4)
 #pragma unroll 2
         for (int kk = 0; kk < D / 8; ++kk) {
@@ -199,8 +204,12 @@ __global__ void __launch_bounds__(THREADS) gqa_prompt_f32_kernel(const PromptArg
             uint4 b[ST];
 #pragma unroll
             for (int t = 0; t < ST; ++t) b[t] = sk[(8 * t + r4) * HALF + ((4 * kk + c4) ^ ((r4 & 1) << 2))];
-            mma_split<ST>(s, hi, lo, b);
+            mma_split<ST>(s, small, hi, lo, b);
         }
+#pragma unroll
+        for (int t = 0; t < ST; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[t][e] += small[t][e];
         // lane: rows row, row + 8; keys k0 + 8 t + 2 c4 + {0, 1}
         float f[2];
         bool moved = false;
@@ -243,18 +252,29 @@ __global__ void __launch_bounds__(THREADS) gqa_prompt_f32_kernel(const PromptArg
                     s[t][2 * half + e] = p;
                 }
         }
-        // k-step t: keys 8 t + 2 c4 (k = c4) and 8 t + 2 c4 + 1 (k = c4 + 4), the lane's own scores
+        // k-step t: keys 8 t + 2 c4 (k = c4) and 8 t + 2 c4 + 1 (k = c4 + 4), the
+        // lane's own scores.  The tensor core's sums round toward zero, so a
+        // tile's output is summed from zero and added to the running one here.
 #pragma unroll
-        for (int t = 0; t < ST; ++t) {
-            const uint4 x = split2(s[t][0], s[t][1]), y = split2(s[t][2], s[t][3]);
-            const uint32_t hi[4] = {x.x, y.x, x.z, y.z}, lo[4] = {x.y, y.y, x.w, y.w};
+        for (int n0 = 0; n0 < NT; n0 += 8) {
+            float step[8][4];
 #pragma unroll
-            for (int n0 = 0; n0 < NT; n0 += 8) {
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) step[n][e] = 0.f;
+#pragma unroll
+            for (int t = 0; t < ST; ++t) {
+                const uint4 x = split2(s[t][0], s[t][1]), y = split2(s[t][2], s[t][3]);
+                const uint32_t hi[4] = {x.x, y.x, x.z, y.z}, lo[4] = {x.y, y.y, x.w, y.w};
                 uint4 b[8];
 #pragma unroll
                 for (int n = 0; n < 8; ++n) b[n] = sv[(4 * t + c4) * D + ((8 * (n0 + n) + r4) ^ (c4 << 1))];
-                mma_split<8>(o + n0, hi, lo, b);
+                mma_split<8>(step, step, hi, lo, b);
             }
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n0 + n][e] += step[n][e];
         }
     }
 #pragma unroll
