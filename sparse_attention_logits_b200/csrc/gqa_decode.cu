@@ -41,9 +41,9 @@ struct Parts {
     int2* meta;                     // [pairs]: first block, number of blocks (1: written whole)
 };
 
-// Units of a row: at least one, so that empty rows are written too.
-template <int KT> __device__ __forceinline__ int row_units(const DecodeArgs& a, int row) {
-    const int pos = __ldg(a.row_pos + row);
+// Units of a row whose last visible token is pos: at least one, so that empty
+// rows are written too.
+template <int KT> __device__ __forceinline__ int units_of(const DecodeArgs& a, int pos) {
     const int64_t room = (int64_t)a.max_pages * a.page_size;
     return pos < 0 ? 1 : pos < room ? pos / KT + 1 : (int)((room - 1) / KT) + 1;
 }
@@ -53,13 +53,11 @@ template <int KT> struct Walk {
     int row, kvh, tile, unit, units;    // place: row, kv head, tile of its heads, unit; the row's units
     int batch, keys;                    // the row's sequence and number of visible keys (0: nothing to read)
 
-    __device__ __forceinline__ void enter_row(const DecodeArgs& a) {
-        if (row >= a.rows) return;
-        units = row_units<KT>(a, row);
-        batch = __ldg(a.row_batch + row);
+    __device__ __forceinline__ void set_row(const DecodeArgs& a, int pos, int seq) {
+        units = units_of<KT>(a, pos);
+        batch = seq;
         const int64_t room = (int64_t)a.max_pages * a.page_size;
-        const int pos = __ldg(a.row_pos + row);
-        keys = pos < 0 || batch < 0 || batch >= a.batch ? 0 : (int)(pos < room ? pos + 1 : room);
+        keys = pos < 0 || seq < 0 || seq >= a.batch ? 0 : (int)(pos < room ? pos + 1 : room);
     }
     __device__ __forceinline__ void next(const DecodeArgs& a, int tiles) {
         if (++unit < units) return;
@@ -68,15 +66,13 @@ template <int KT> struct Walk {
         tile = 0;
         if (++kvh < a.n_kv_heads) return;
         kvh = 0;
-        ++row;
-        enter_row(a);
+        if (++row < a.rows) set_row(a, __ldg(a.row_pos + row), __ldg(a.row_batch + row));
     }
 };
 
 struct LocateShared {
     int warp_sum[WARPS];
-    int row, units_before;
-    long long total;
+    int row, units_before, pos, seq;    // of the stretch's first unit
 };
 
 // This block's stretch [begin, end) of the line and the walk's start.  The
@@ -89,8 +85,12 @@ __device__ __forceinline__ void locate(const DecodeArgs& a, int tiles, int per_b
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (a.rows + THREADS - 1) / THREADS;
     const int r0 = min(a.rows, tid * per), r1 = min(a.rows, r0 + per);
-    int sum = 0;
-    for (int r = r0; r < r1; ++r) sum += row_units<KT>(a, r);
+    int sum = 0, pos = -1, seq = -1;    // (of the thread's last row)
+    for (int r = r0; r < r1; ++r) {
+        pos = __ldg(a.row_pos + r);
+        seq = __ldg(a.row_batch + r);
+        sum += units_of<KT>(a, pos);
+    }
     int x = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -110,24 +110,27 @@ __device__ __forceinline__ void locate(const DecodeArgs& a, int tiles, int per_b
     if (stretch < per_block) stretch = per_block;
     begin = min(line, (int64_t)blockIdx.x * stretch);
     end = min(line, begin + stretch);
-    if (begin < end) {
-        // the thread whose rows hold the stretch's first unit finds its row
-        const int64_t lo = (int64_t)before * hvs, hi = (int64_t)(before + sum) * hvs;
-        if (begin >= lo && begin < hi) {
-            int r = r0, u = before;
+    // the thread whose rows hold the stretch's first unit finds its row
+    if (begin < end && begin >= (int64_t)before * hvs && begin < (int64_t)(before + sum) * hvs) {
+        int r = r0, u = before;
+        if (per > 1) {
             for (; r < r1; ++r) {
-                const int n = row_units<KT>(a, r);
+                pos = __ldg(a.row_pos + r);
+                const int n = units_of<KT>(a, pos);
                 if (begin < (int64_t)(u + n) * hvs) break;
                 u += n;
             }
-            sh.row = r;
-            sh.units_before = u;
+            seq = __ldg(a.row_batch + r);
         }
+        sh.row = r;
+        sh.units_before = u;
+        sh.pos = pos;
+        sh.seq = seq;
     }
     __syncthreads();
     if (begin < end) {
         w.row = sh.row;
-        w.enter_row(a);
+        w.set_row(a, sh.pos, sh.seq);
         const int in_row = (int)(begin - (int64_t)sh.units_before * hvs);
         const int hv = in_row / w.units;
         w.unit = in_row - hv * w.units;
@@ -773,23 +776,37 @@ __global__ void __launch_bounds__(128) gqa_combine_kernel(const DecodeArgs a, co
     const int2 me = parts.meta[(int64_t)row * a.n_kv_heads * tiles + kvh * tiles + tile];
     if (me.y <= 1) return;                                  // written whole
     // part 0 lies in the first block's "begins" place, the others in the
-    // "continues" places of the blocks behind it
-    float m = -INFINITY;
-    for (int i = lane; i < me.y; i += 32) m = fmaxf(m, parts.ml[(int64_t)(2 * (me.x + i) + (i == 0)) * GT + h].x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    float l = 0.f, o[VEC];
+    // "continues" places of the blocks behind it; four parts' numbers are
+    // requested together and joined like the steps of an online softmax
+    float m = -INFINITY, l = 0.f, o[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) o[v] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < me.y; ++i) {
-        const int64_t at = (int64_t)(2 * (me.x + i) + (i == 0)) * GT + h;
-        const float2 ml = parts.ml[at];
-        const float f = m == -INFINITY ? 0.f : fast_exp2(ml.x - m);
-        l = fmaf(f, ml.y, l);
-        const float* po = parts.o + at * D + lane * VEC;
+    for (int i0 = 0; i0 < me.y; i0 += 4) {
+        float2 ml[4];
+        float po[4][VEC];
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) o[v] = fmaf(f, po[v], o[v]);
+        for (int k = 0; k < 4; ++k) {
+            const int i = min(i0 + k, me.y - 1);
+            const int64_t at = (int64_t)(2 * (me.x + i) + (i == 0)) * GT + h;
+            ml[k] = parts.ml[at];
+            if (VEC == 4) *(float4*)po[k] = *(const float4*)(parts.o + at * D + lane * VEC);
+            else *(float2*)po[k] = *(const float2*)(parts.o + at * D + lane * VEC);
+            if (i0 + k >= me.y) ml[k].x = -INFINITY;
+        }
+        const float top = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m);
+        if (top == -INFINITY) continue;                     // parts without a visible key
+        const float f = fast_exp2(m - top);
+        m = top;
+        l *= f;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) o[v] *= f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float g = fast_exp2(ml[k].x - top);
+            l = fmaf(g, ml[k].y, l);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) o[v] = fmaf(g, po[k][v], o[v]);
+        }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     Q* out = (Q*)a.out + item * D + lane * VEC;
