@@ -19,6 +19,10 @@ def _gen(seed):
     return torch.Generator(device="cuda").manual_seed(seed)
 
 
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
 def _randn(shape, g, dtype=torch.float32):
     return torch.randn(shape, generator=g, device="cuda").to(dtype)
 
@@ -95,6 +99,72 @@ def test_prompt_large_and_peaked_scores(cuda_device, dtype):
     q[::3] *= -3
     out, lse = dsa.gqa_prompt_attention(q, k, v, torch.tensor([0, n], dtype=torch.int32, device="cuda"), 0.3)
     _prompt_check(out, lse, q, k, v, [0, n], 0.3, 0, n)
+
+
+@pytest.mark.parametrize("dtype,D,H,Hkv", [("bf16", 128, 4, 2), ("bf16", 64, 3, 1), ("fp32", 64, 2, 2)])
+def test_prompts_never_reach_one_another(cuda_device, dtype, D, H, Hkv):
+    """Prompts between others full of NaN and infinities, ending inside a tile of keys."""
+    g = _gen(7)
+    lens = [70, 61, 200, 3, 129, 50]
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    qkv = _randn((cu[-1], H + 2 * Hkv, D), g, DT[dtype])
+    for i in (0, 2, 4):
+        qkv[cu[i]:cu[i + 1]] = math.inf if i == 2 else NAN
+    q, k, v = qkv[:, :H], qkv[:, H:H + Hkv], qkv[:, H + Hkv:]
+    out, lse = dsa.gqa_prompt_attention(q, k, v, _i32(cu), 0.1)
+    assert dsa.get_device_error(cuda_device) == dsa.DSA_OK
+    for i in (1, 3, 5):
+        _prompt_check(out, lse, q, k, v, cu, 0.1, cu[i], cu[i + 1])
+
+
+def test_prompt_nan_queries_stay_in_their_rows(cuda_device):
+    q, k, v = (_randn((300, 2, 128), _gen(8), torch.bfloat16) for _ in range(3))
+    clean = dsa.gqa_prompt_attention(q, k, v, _i32([0, 300]), 0.1)
+    q = q.clone()
+    q[[5, 130, 299]] = NAN
+    out, lse = dsa.gqa_prompt_attention(q, k, v, _i32([0, 300]), 0.1)
+    rows = torch.ones(300, dtype=torch.bool, device="cuda")
+    rows[[5, 130, 299]] = False
+    assert torch.equal(out[rows], clean[0][rows]) and torch.equal(lse[rows], clean[1][rows])
+    assert bool(torch.isnan(out[~rows]).all())
+
+
+def test_prompt_row_strides_past_32_bits(cuda_device):
+    """Rows 2.5 MB apart: the last lie more than 2^31 elements behind the first."""
+    n, wide = 1800, 1250000
+    big = torch.empty((n, wide), dtype=torch.bfloat16, device="cuda")
+    part = _randn((n, 4, 64), _gen(9), torch.bfloat16)
+    big[:, wide - 256:] = part.reshape(n, 256)
+    x = big[:, wide - 256:].view(n, 4, 64)
+    out, lse = dsa.gqa_prompt_attention(x[:, :2], x[:, 2:3], x[:, 3:], _i32([0, n]), 0.2)
+    _prompt_check(out, lse, part[:, :2], part[:, 2:3], part[:, 3:], None, 0.2, 0, n)
+
+
+def test_two_streams_at_once(cuda_device):
+    """Calls that overlap on two streams, each with its own buffers: the results of the calls alone."""
+    runs = []
+    for seed in (1, 2):
+        g = _gen(80 + seed)
+        qkv = _randn((2000, 8, 128), g, torch.bfloat16)
+        c = Paged([3000, 1234, 5], 2, 128, 16, "bf16", 90 + seed)
+        q = _randn((3, 6, 128), g, torch.bfloat16)
+        cu, b, p = _i32([0, 700, 2000]), _i32([0, 1, 2]), _i32([2999, 1233, 4])
+
+        def run(qkv=qkv, c=c, q=q, cu=cu, b=b, p=p):
+            return (*dsa.gqa_prompt_attention(qkv[:, :4], qkv[:, 4:6], qkv[:, 6:], cu, 0.1),
+                    *dsa.gqa_decode_attention(q, c.k, c.v, c.table, b, p, 0.1))
+        runs.append((run, run(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for run, _, stream in runs:
+            with torch.cuda.stream(stream):
+                got.append(run())
+        torch.cuda.synchronize()
+        for (_, want, _), x in zip(runs, got):
+            assert all(torch.equal(a, b) for a, b in zip(want, x))
 
 
 def test_prompt_bad_bounds_are_reported_and_skipped(cuda_device):
@@ -198,10 +268,6 @@ def _decode_case(case, seed=11):
     return c, fused[:, 1:H + 1], batch, pos, 1.0 / math.sqrt(D)
 
 
-def _i32(x):
-    return torch.tensor(x, dtype=torch.int32, device="cuda")
-
-
 @pytest.mark.parametrize("case", list(DECODES))
 def test_decode_attention(cuda_device, case):
     c, q, batch, pos, scale = _decode_case(case)
@@ -264,6 +330,32 @@ def test_decode_bad_indexes_are_reported(cuda_device, kind):
         out, lse = run(batch, pos, table)
         assert bool(torch.isfinite(lse[::2]).all())         # (row 1 of the first names places that hold NaN)
         _decode_check(c, q[2:], out[2:], lse[2:], [1], [99], 0.1)
+    assert dsa.get_device_error(cuda_device) == dsa.DSA_OK
+
+
+def test_cache_offsets_past_32_bits(cuda_device):
+    """Pages whose first elements lie beyond 2^31 elements (and 2^32 bytes) of the cache: written, read and copied."""
+    pages, hkv, page, D = 17000, 8, 128, 128                # 2.2e9 elements, 4.5 GB a cache
+    k_cache, v_cache = (torch.empty((pages, hkv, page, D), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    table = _i32([[pages - 1, 3, pages - 2], [pages - 3, pages - 4, 5]])
+    n = 300
+    g = _gen(43)
+    batch = torch.arange(2, device="cuda", dtype=torch.int32).repeat_interleave(n)
+    pos = torch.arange(n, device="cuda", dtype=torch.int32).repeat(2)
+    k, v = (_randn((2 * n, hkv, D), g, torch.bfloat16) for _ in "kv")
+    dsa.kv_cache_append(k, v, batch, pos, table, k_cache, v_cache)
+    q = _randn((2, 16, D), g, torch.bfloat16)
+
+    def check_rows(t):
+        out, lse = dsa.gqa_decode_attention(q, k_cache, v_cache, t, _i32([0, 1]), _i32([n - 1, n - 1]), 0.1)
+        for r in range(2):
+            part = slice(r * n, (r + 1) * n)
+            ref, ref_lse, A, d = attend(q[r][:, None], k[part].transpose(0, 1), v[part].transpose(0, 1), 0.1,
+                                        torch.ones(1, n, dtype=torch.bool, device="cuda"))
+            check(out[r][:, None], lse[r][:, None], ref, ref_lse, A, d, n, U[torch.bfloat16])
+    check_rows(table)
+    dsa.kv_pages_copy([k_cache, v_cache], _i32([pages - 1, 3]), _i32([7, pages - 6]))
+    check_rows(_i32([[7, pages - 6, pages - 2], [pages - 3, pages - 4, 5]]))
     assert dsa.get_device_error(cuda_device) == dsa.DSA_OK
 
 
