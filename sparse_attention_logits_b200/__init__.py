@@ -427,7 +427,8 @@ def gqa_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     """Attention of query rows q [rows, n_heads, head_dim] (rows may be
     strided) over tokens 0 .. row_pos[t] of sequence row_batch[t] of the paged
     caches: (out [rows, n_heads, head_dim], lse [rows, n_heads] fp32).
-    row_pos < 0: nothing visible (out = 0, lse = -inf)."""
+    row_pos < 0: nothing visible (out = 0, lse = -inf).  Rows of one sequence
+    beside each other (several tokens at once) share its reads."""
     return _gqa.decode(q, k_cache, v_cache, page_table, row_batch, row_pos, scale, k_scale, v_scale, out, lse, workspace)
 
 

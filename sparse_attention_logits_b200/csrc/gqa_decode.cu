@@ -2,9 +2,19 @@
 //   z_s    = scale * q[t,h,:] . k_s          s <= row_pos[t], kv head h / group
 //   out    = sum_s softmax_s(z) v_s,   lse = log sum_s exp(z_s)
 // Every visible key and value row is read once for all heads of its group,
-// so the cache's bytes at the HBM rate are the floor.
+// so the cache's bytes at the HBM rate are the floor.  32 sequences of up to
+// 32K tokens, 8 / 32 heads of 128, bf16: 514 us, 6.36 TB/s (a plain copy runs at
+// 6.5); 64 of them, 8 / 64 heads, fp8: 570 us, 5.9 TB/s.  One row of 777 tokens
+// takes 7.7 us, a chain of latencies: rows, pages, cache, joining of the parts.
 //
-// Work split.  A pair is (row, kv head, tile of the group's heads); its keys
+// Rows of one sequence that stand beside each other (several tokens verified
+// at once) share its reads too: a bunch is up to `merge` such rows, whose heads
+// fill the 16 columns of the products together; past a row's last key its
+// columns are masked.  Against a pair for every row: 8 sequences of up to 16K
+// tokens, 4 rows each, 8 / 32 heads: 272 -> 82 us in bf16, 122 -> 69 in fp8; one
+// sequence of 777 tokens 9.5 -> 10.8 us.
+//
+// Work split.  A pair is (bunch of rows, kv head, tile of the group's heads); its keys
 // are cut into units of KT (128, in fp32 64).  All pairs' units form
 // one line, and block i of the grid takes the i-th equal stretch of it, whatever the rows' lengths:
 // ragged batches load every SM alike, and one long row uses the whole GPU.
@@ -15,6 +25,8 @@
 #include "common.cuh"
 #include "launchers.h"
 #include "sm100.cuh"
+
+#include <type_traits>
 
 namespace dsa {
 
@@ -38,35 +50,82 @@ __device__ __forceinline__ float fast_exp2(float x) {
 struct Parts {
     float* o;                       // [2 * grid][GT][D], relative to the maximum
     float2* ml;                     // [2 * grid][GT]: maximum (log2 units), sum
-    int2* meta;                     // [pairs]: first block, number of blocks (1: written whole)
+    int2* meta;                     // [row, kv head, tile]: first block; blocks (1: written whole), and
+                                    // above bit 16 the row's place in its bunch
 };
 
 // Units of a row whose last visible token is pos: at least one, so that empty
 // rows are written too.
 template <int KT> __device__ __forceinline__ int units_of(const DecodeArgs& a, int pos) {
-    const int64_t room = (int64_t)a.max_pages * a.page_size;
-    return pos < 0 ? 1 : pos < room ? pos / KT + 1 : (int)((room - 1) / KT) + 1;
+    return pos < 0 ? 1 : min(pos, a.room - 1) / KT + 1;
+}
+__device__ __forceinline__ int keys_of(const DecodeArgs& a, int pos, int seq) {
+    return pos < 0 || seq < 0 || seq >= a.batch ? 0 : min(pos, a.room - 1) + 1;
 }
 
-// A walk along the line of units.
-template <int KT> struct Walk {
-    int row, kvh, tile, unit, units;    // place: row, kv head, tile of its heads, unit; the row's units
-    int batch, keys;                    // the row's sequence and number of visible keys (0: nothing to read)
+// Rows' positions and sequences, and the bunches that begin with them, in
+// shared memory when there are not too many.
+constexpr int ROWS_HELD = 256;
+struct RowsShared {
+    int2 row[ROWS_HELD];
+    int4 bunch[ROWS_HELD];
+};
+__device__ __forceinline__ int2 row_at(const DecodeArgs& a, const RowsShared& sh, int r) {
+    if (a.rows <= ROWS_HELD) return sh.row[r];
+    return make_int2(__ldg(a.row_pos + r), __ldg(a.row_batch + r));
+}
+
+// The bunch that begins with row r: rows of one sequence, all empty or none,
+// as (rows, sequence, least and largest position); none (0 rows) where row r
+// joins the one before it.
+__device__ __forceinline__ int4 bunch_at(const DecodeArgs& a, const RowsShared& sh, int r) {
+    const int in_seq = r - a.by_tokens.div(r) * a.tokens, k = in_seq - a.by_merge.div(in_seq) * a.merge;
+    const int2 x = row_at(a, sh, r);
+    if (k > 0) {
+        const int2 y = row_at(a, sh, r - 1);
+        if (x.y == y.y && (x.x < 0) == (y.x < 0)) return make_int4(0, 0, 0, 0);
+    }
+    const int most = min(min(a.merge - k, a.tokens - in_seq), a.rows - r);
+    int4 b = make_int4(1, x.y, x.x, x.x);
+    for (; b.x < most; ++b.x) {
+        const int2 y = row_at(a, sh, r + b.x);
+        if (y.y != x.y || (y.x < 0) != (x.x < 0)) break;
+        b.z = min(b.z, y.x);
+        b.w = max(b.w, y.x);
+    }
+    return b;
+}
+
+// A walk along the line of units.  MANY: pairs of more than one row.
+template <int KT, bool MANY> struct Walk {
+    int row, kvh, tile, unit, units;    // place: (first) row, kv head, tile of its heads, unit; the pair's units
+    int batch, keys;                    // the sequence and number of visible keys (0: nothing to read)
+    int rows, least;                    // MANY: the bunch's rows, the fewest visible keys of one
 
     __device__ __forceinline__ void set_row(const DecodeArgs& a, int pos, int seq) {
         units = units_of<KT>(a, pos);
         batch = seq;
-        const int64_t room = (int64_t)a.max_pages * a.page_size;
-        keys = pos < 0 || seq < 0 || seq >= a.batch ? 0 : (int)(pos < room ? pos + 1 : room);
+        keys = keys_of(a, pos, seq);
     }
-    __device__ __forceinline__ void next(const DecodeArgs& a, int tiles) {
+    __device__ __forceinline__ void set_bunch(const DecodeArgs& a, const RowsShared& sh) {
+        const int4 b = a.rows <= ROWS_HELD ? sh.bunch[row] : bunch_at(a, sh, row);
+        rows = b.x;
+        batch = b.y;
+        least = keys_of(a, b.z, batch);
+        keys = keys_of(a, b.w, batch);
+        units = units_of<KT>(a, b.w);
+    }
+    __device__ __forceinline__ void next(const DecodeArgs& a, const RowsShared& sh, int tiles) {
         if (++unit < units) return;
         unit = 0;
         if (++tile < tiles) return;
         tile = 0;
         if (++kvh < a.n_kv_heads) return;
         kvh = 0;
-        if (++row < a.rows) set_row(a, __ldg(a.row_pos + row), __ldg(a.row_batch + row));
+        row += MANY ? rows : 1;
+        if (row >= a.rows) return;
+        if (MANY) set_bunch(a, sh);
+        else set_row(a, __ldg(a.row_pos + row), __ldg(a.row_batch + row));
     }
 };
 
@@ -78,18 +137,32 @@ struct LocateShared {
 // This block's stretch [begin, end) of the line and the walk's start.  The
 // whole block takes part.  `per_block` units at least, so that short lines
 // are not cut finer than is worth joining.
-template <int KT>
-__device__ __forceinline__ void locate(const DecodeArgs& a, int tiles, int per_block, LocateShared& sh, Walk<KT>& w,
+template <int KT, bool MANY>
+__device__ __forceinline__ void locate(const DecodeArgs& a, int tiles, int per_block, LocateShared& sh, RowsShared& held, Walk<KT, MANY>& w,
                                        int64_t& begin, int64_t& end, int64_t& stretch) {
     const int hvs = a.n_kv_heads * tiles;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (a.rows + THREADS - 1) / THREADS;
     const int r0 = min(a.rows, tid * per), r1 = min(a.rows, r0 + per);
     int sum = 0, pos = -1, seq = -1;    // (of the thread's last row)
-    for (int r = r0; r < r1; ++r) {
+    if (MANY) {
+        if (a.rows <= ROWS_HELD)
+            for (int r = tid; r < a.rows; r += THREADS) held.row[r] = make_int2(__ldg(a.row_pos + r), __ldg(a.row_batch + r));
+        __syncthreads();
+    }
+    // units of a pair that begins with row r (MANY: a row that joins another has none of its own)
+    auto units_at = [&](int r) {
+        if (MANY) {
+            const int4 b = bunch_at(a, held, r);
+            if (a.rows <= ROWS_HELD) held.bunch[r] = b;
+            return b.x ? units_of<KT>(a, b.w) : 0;
+        }
         pos = __ldg(a.row_pos + r);
-        seq = __ldg(a.row_batch + r);
-        sum += units_of<KT>(a, pos);
+        return units_of<KT>(a, pos);
+    };
+    for (int r = r0; r < r1; ++r) {
+        sum += units_at(r);
+        if (!MANY) seq = __ldg(a.row_batch + r);
     }
     int x = sum;
 #pragma unroll
@@ -115,8 +188,7 @@ __device__ __forceinline__ void locate(const DecodeArgs& a, int tiles, int per_b
         int r = r0, u = before;
         if (per > 1) {
             for (; r < r1; ++r) {
-                pos = __ldg(a.row_pos + r);
-                const int n = units_of<KT>(a, pos);
+                const int n = units_at(r);
                 if (begin < (int64_t)(u + n) * hvs) break;
                 u += n;
             }
@@ -130,7 +202,8 @@ __device__ __forceinline__ void locate(const DecodeArgs& a, int tiles, int per_b
     __syncthreads();
     if (begin < end) {
         w.row = sh.row;
-        w.set_row(a, sh.pos, sh.seq);
+        if (MANY) w.set_bunch(a, held);
+        else w.set_row(a, sh.pos, sh.seq);
         const int in_row = (int)(begin - (int64_t)sh.units_before * hvs);
         const int hv = in_row / w.units;
         w.unit = in_row - hv * w.units;
@@ -139,17 +212,25 @@ __device__ __forceinline__ void locate(const DecodeArgs& a, int tiles, int per_b
     }
 }
 
-// Row of the cache (in head_dim vectors) that holds key s of the walk's
-// sequence, or -1: not visible, or a bad page (reported).
-template <int KT> __device__ __forceinline__ int cache_row(const DecodeArgs& a, const Walk<KT>& w, int s) {
-    if (s >= w.keys) return -1;
+// Where key s of the walk's sequence lies: its page, and its row (of head_dim
+// numbers) relative to that of the page; -1: not visible.  The page is looked
+// at later (cache_row), so that its load is not waited for here.
+struct Place {
+    int page, row;
+};
+template <int KT, bool MANY> __device__ __forceinline__ Place look_up(const DecodeArgs& a, const Walk<KT, MANY>& w, int s) {
+    if (s >= w.keys) return Place{0, -1};
     const int pi = a.by_page.div(s);
-    const int page = __ldg(a.page_table + (int64_t)w.batch * a.max_pages + pi);
-    if (page < 0 || page >= a.num_pages) {
+    return Place{__ldg(a.page_table + (int64_t)w.batch * a.max_pages + pi), w.kvh * a.page_size + (s - pi * a.page_size)};
+}
+// The row of the cache, or -1: not visible, or a bad page (reported).
+__device__ __forceinline__ int cache_row(const DecodeArgs& a, Place p) {
+    if (p.row < 0) return -1;
+    if (p.page < 0 || p.page >= a.num_pages) {
         record_error(a.err, DEV_ERR_BAD_INDEX);
         return -1;
     }
-    return (page * a.n_kv_heads + w.kvh) * a.page_size + (s - pi * a.page_size);
+    return p.page * a.n_kv_heads * a.page_size + p.row;
 }
 
 // ------------------------------------------------------------ the kernel --
@@ -186,10 +267,20 @@ template <int KT> __device__ __forceinline__ int cache_row(const DecodeArgs& a, 
 // small ones summed apart.  What is left out or rounded is at most 3 x 2^-22
 // of |x y| a term.  The tensor core's sums round toward zero, so each slice's
 // output is summed from zero and added to the running one in fp32.
-template <typename KV, int D> struct MmaCfg;
-template <int D> struct MmaCfg<__nv_bfloat16, D> { static constexpr int WK = 32, STAGES = 2, BLOCKS = D == 64 ? 2 : 1; };
-template <int D> struct MmaCfg<__nv_fp8_e4m3, D> { static constexpr int WK = 32, STAGES = 2, BLOCKS = 3; };
-template <int D> struct MmaCfg<float, D> { static constexpr int WK = 16, STAGES = D == 64 ? 3 : 2, BLOCKS = D == 64 ? 2 : 1; };
+// WK: keys of a warp's slice; BLOCKS per SM, with STAGES slices in flight per
+// warp; Q_BYTES: the query fragments, where the registers have no room for them.
+template <typename KV, int D, int GT> struct MmaCfg;
+template <int D, int GT> struct MmaCfg<__nv_bfloat16, D, GT> {
+    static constexpr int WK = 32, STAGES = 2, BLOCKS = D == 64 ? 2 : 1, Q_BYTES = 0;
+};
+// 16 heads of 128: 32 sequences of up to 16K, 8 / 128 heads, take 202 us with two
+// blocks and 332 us with three, whose registers spill.
+template <int D, int GT> struct MmaCfg<__nv_fp8_e4m3, D, GT> {
+    static constexpr int WK = 32, STAGES = 2, BLOCKS = D == 64 || GT == 8 ? 3 : 2, Q_BYTES = GT == 16 ? D / 16 * 512 : 0;
+};
+template <int D, int GT> struct MmaCfg<float, D, GT> {
+    static constexpr int WK = 16, STAGES = D == 64 ? 3 : 2, BLOCKS = D == 64 ? 2 : 1, Q_BYTES = GT == 16 ? D / 8 * 1024 : 0;
+};
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -265,6 +356,14 @@ template <int ES, int RB, bool IS_V> __device__ __forceinline__ uint32_t piece_a
     return r * RB + ((RB == 128 ? c ^ ((r & 1) << 2) : c) << 4);
 }
 
+// Whether a word of cache values holds one that is, or in the products becomes,
+// infinite or NaN.
+template <int ES> __device__ __forceinline__ bool not_finite(uint32_t x) {
+    if (ES == 4) return (x & 0x7fffffffu) >= 0x7f7ff000u;       // (its hi part is rounded up)
+    if (ES == 2) return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+    return __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0u;
+}
+
 // Place (in floats) of dim d of head r in the exchange buffer of the warps'
 // outputs: 16-byte pieces swizzled among the eight of a 128-byte line.
 template <int D> __device__ __forceinline__ int exch_at(int r, int d) {
@@ -272,46 +371,55 @@ template <int D> __device__ __forceinline__ int exch_at(int r, int d) {
 }
 
 template <typename KV, int D, int GT>
-__global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_kernel(const DecodeArgs a, const Parts parts) {
+__global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D, GT>::BLOCKS)) gqa_decode_kernel(const DecodeArgs a, const Parts parts) {
     pdl_wait();
     pdl_launch_dependents();
     constexpr int ES = (int)sizeof(KV);
     constexpr bool FP8 = ES == 1, FP32 = ES == 4;
-    constexpr int WK = MmaCfg<KV, D>::WK, KT = WK * WARPS;  // keys of a warp's slice, and of a unit
+    constexpr int WK = MmaCfg<KV, D, GT>::WK, KT = WK * WARPS;  // keys of a warp's slice, and of a unit
     constexpr int RB = D * ES;                      // bytes of a row
     constexpr int PIECES = RB / 16;
     constexpr int SLICE = WK * RB;                  // K (or V) bytes of a warp's slice
-    constexpr int STAGES = MmaCfg<KV, D>::STAGES;
+    constexpr int STAGES = MmaCfg<KV, D, GT>::STAGES;
     constexpr uint32_t ALL = WK == 32 ? 0xffffffffu : 0xffffu;
     constexpr int SLOT = 2 * SLICE + (FP8 ? 2 * WK * 4 : 0) + 16;   // K, V, scales, the mask of valid keys
     constexpr int KS = D / 16, MT = WK / 16, NG = GT / 8;   // k-steps; tiles of 16 keys, of 8 heads
+    constexpr bool MANY = GT == 16;                 // pairs of several rows
+    constexpr bool Q_SHARED = MANY && ES != 2;      // query fragments in shared memory, for want of registers
+    constexpr int VG = MANY ? NG : 1, VE = MANY ? 2 : 1;    // references of the value scales: per head, or one
     static_assert(!FP8 || WK == 32, "a lane per key's scales");
-    static_assert(!FP32 || GT == 8, "fp32 takes eight heads");
     static_assert(2 * SLICE >= 8 * D * 4, "the outputs of 8 heads are exchanged in a slot");
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ LocateShared sh;
+    __shared__ RowsShared held;             // (MANY only)
     __shared__ float2 s_ml[WARPS][16];
     const int group = a.n_heads / a.n_kv_heads, tiles = ceil_div(group, GT);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r4 = lane >> 2, c4 = lane & 3;        // fragment row / column group
     uint8_t* ring = smem + warp * STAGES * SLOT;
-    Walk<KT> w;
+    uint8_t* qs = smem + WARPS * STAGES * SLOT;     // fp32 of 16 heads: the query fragments
+    Walk<KT, MANY> w;
     int64_t begin, end, stretch;
-    locate<KT>(a, tiles, 128 / KT, sh, w, begin, end, stretch);
+    locate<KT, MANY>(a, tiles, 128 / KT, sh, held, w, begin, end, stretch);
     if (begin >= end) return;
     const uint8_t* kc = (const uint8_t*)a.k_cache;
     const uint8_t* vc = (const uint8_t*)a.v_cache;
 
     // the loads' walk runs STAGES units ahead of the products'; the page
     // of a slice is looked up one unit before its rows are requested
-    Walk<KT> lw = w;
+    Walk<KT, MANY> lw = w;
     int64_t to_load = end - begin;
-    auto look = [&]() -> int {
-        return to_load > 0 ? cache_row<KT>(a, lw, lw.unit * KT + warp * WK + (lane & (WK - 1))) : -1;
+    auto look = [&]() -> Place {            // of the walk's unit, and a step on
+        if (to_load <= 0) return Place{0, -1};
+        const Place p = look_up(a, lw, lw.unit * KT + warp * WK + (lane & (WK - 1)));
+        --to_load;
+        lw.next(a, held, tiles);
+        return p;
     };
-    int row = look();
-    auto request = [&](int st) {
-        if (to_load > 0) {
+    int64_t to_request = end - begin;
+    auto request = [&](int st, Place place) {
+        if (to_request > 0) {
+            const int row = cache_row(a, place);
             uint8_t* slot = ring + st * SLOT;
 #pragma unroll
             for (int i = 0; i < WK * PIECES / 32; ++i) {
@@ -328,43 +436,62 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
             }
             const uint32_t valid = __ballot_sync(0xffffffffu, row >= 0) & ALL;
             if (lane == 0) *(uint32_t*)(slot + SLOT - 16) = valid;
-            lw.next(a, tiles);
-            --to_load;
-            row = look();
+            --to_request;
         }
         cp_async_commit();
     };
-#pragma unroll 1
-    for (int st = 0; st < STAGES; ++st) request(st);
+    Place ahead[STAGES];
+#pragma unroll
+    for (int st = 0; st < STAGES; ++st) ahead[st] = look();
+    Place place = look();
+#pragma unroll
+    for (int st = 0; st < STAGES; ++st) request(st, ahead[st]);
+    auto request_next = [&](int st) {
+        request(st, place);
+        place = look();
+    };
 
     int st = 0;
     for (int64_t at = begin; at < end;) {
-        const int h0 = w.kvh * group + w.tile * GT, heads = min(GT, group - w.tile * GT);
+        // columns of the products: the tile's heads, or all heads of all rows of the bunch
+        const bool bunch = MANY && w.rows > 1;
+        const int h0 = w.kvh * group + w.tile * GT, heads = bunch ? w.rows * group : min(GT, group - w.tile * GT);
         const int n = (int)min((int64_t)(w.units - w.unit), end - at);
-        if (w.unit == 0 && w.kvh == 0 && w.tile == 0 && tid == 0 &&
-            (w.batch < 0 || w.batch >= a.batch || __ldg(a.row_pos + w.row) >= (int64_t)a.max_pages * a.page_size))
+        if (w.unit == 0 && w.kvh == 0 && w.tile == 0 && tid < (MANY ? w.rows : 1) &&
+            (w.batch < 0 || w.batch >= a.batch || __ldg(a.row_pos + w.row + tid) >= (int64_t)a.max_pages * a.page_size))
             record_error(a.err, DEV_ERR_BAD_INDEX);     // reported once per row, by the block that begins it
         // Q fragments: head 8 g + r4; k-step kk holds dims
         // 16 kk + {2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9} (bf16), or
         // 64 (kk / 4) + 16 c4 + 4 (kk % 4) + {0, 1, 2, 3} (fp8), or, as two
         // k-steps of 8, 16 kk + 4 c4 + {0, 1} and {2, 3} (fp32: hi, then lo)
-        uint32_t qf[KS][FP32 ? 8 : 2 * NG];
+        uint32_t qf[KS][FP32 ? 8 : 2 * NG];         // (Q_SHARED: in shared memory; fp32: place of k-step 2 kk + i)
+        auto q_at = [&](int step, int g) { return qs + ((step * (FP32 ? NG : 1) + g) * 32 + lane) * 16; };
         float zs[NG][2];                            // score scale of heads 8 g + 2 c4 + {0, 1}
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             const bool on = 8 * g + r4 < heads;
-            const int64_t at_q = (int64_t)w.row * a.ld_q + (h0 + (on ? 8 * g + r4 : 0)) * D;
+            const int x = on ? 8 * g + r4 : 0, xr = bunch ? a.by_group.div(x) : 0;
+            const int64_t at_q = (int64_t)(w.row + xr) * a.ld_q + (h0 + x - xr * group) * D;
             const __nv_bfloat16* q = (const __nv_bfloat16*)a.q + at_q;
             zs[g][0] = zs[g][1] = a.scale_log2;
             if constexpr (FP32) {
 #pragma unroll
                 for (int kk = 0; kk < KS; ++kk) {
-                    const float4 x = on ? __ldg((const float4*)((const float*)a.q + at_q + 16 * kk + 4 * c4))
+                    if (Q_SHARED && kk % WARPS != warp) continue;
+                    const float4 v = on ? __ldg((const float4*)((const float*)a.q + at_q + 16 * kk + 4 * c4))
                                         : make_float4(0.f, 0.f, 0.f, 0.f);
-                    split(x.x, qf[kk][0], qf[kk][4]);
-                    split(x.y, qf[kk][1], qf[kk][5]);
-                    split(x.z, qf[kk][2], qf[kk][6]);
-                    split(x.w, qf[kk][3], qf[kk][7]);
+                    uint32_t y[8];
+                    split(v.x, y[0], y[4]);
+                    split(v.y, y[1], y[5]);
+                    split(v.z, y[2], y[6]);
+                    split(v.w, y[3], y[7]);
+                    if (Q_SHARED) {
+                        st_shared_v4(q_at(2 * kk, g), y[0], y[1], y[4], y[5]);
+                        st_shared_v4(q_at(2 * kk + 1, g), y[2], y[3], y[6], y[7]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) qf[kk][i] = y[i];
+                    }
                 }
             } else if constexpr (!FP8) {
 #pragma unroll
@@ -400,6 +527,20 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
                 zs[g][1] = __shfl_sync(0xffffffffu, up, 8 * c4 + 4);
             }
         }
+        if constexpr (FP8 && Q_SHARED) {
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk)
+                if (kk % WARPS == warp) st_shared_v4(q_at(kk, 0), qf[kk][0], qf[kk][1], qf[kk][NG], qf[kk][NG + 1]);
+        }
+        if (Q_SHARED) __syncthreads();
+        int sees[NG][2];                            // MANY: keys that heads 8 g + 2 c4 + {0, 1} see
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int x = 8 * g + 2 * c4 + e;
+                sees[g][e] = bunch ? (x < heads ? keys_of(a, row_at(a, held, w.row + a.by_group.div(x)).x, w.batch) : w.least) : w.keys;
+            }
         // O^T: tile t, rows (dims) r4 and r4 + 8, columns (heads) 8 g + 2 c4 + {0, 1}
         float o[KS][NG][4];
 #pragma unroll
@@ -408,7 +549,11 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
             for (int g = 0; g < NG; ++g)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[t][g][e] = 0.f;
-        float m[NG][2], l[NG][2], vref = 0.f, vinv = 0.f;
+        float m[NG][2], l[NG][2], vref[VG][VE], vinv[VG][VE];
+#pragma unroll
+        for (int g = 0; g < VG; ++g)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) vref[g][e] = vinv[g][e] = 0.f;
 #pragma unroll
         for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -423,6 +568,9 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
             const uint8_t* slot = ring + st * SLOT;
             const uint32_t kb = smem_u32(slot), vb = kb + SLICE;
             const uint32_t valid = *(const uint32_t*)(slot + SLOT - 16);
+            // MANY: the slice's first key; whether some of its keys are hidden from some of the rows
+            const int key0 = (w.unit + u) * KT + warp * WK;
+            const bool partly = MANY && bunch && key0 + WK > w.least;
             if (valid) {
                 // S^T: keys 16 t + r4 (+ 8), heads 8 g + 2 c4 + {0, 1}
                 float s[MT][NG][4];
@@ -433,11 +581,13 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
 #pragma unroll
                         for (int e = 0; e < 4; ++e) s[t][g][e] = 0.f;
                 if constexpr (FP32) {
-                    float small[MT][4];             // the products with a lo part
+                    float small[MT][NG][4], small2[MT][NG][4];      // the products with a lo part
 #pragma unroll
                     for (int t = 0; t < MT; ++t)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) small[t][e] = 0.f;
+                        for (int g = 0; g < NG; ++g)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) small[t][g][e] = small2[t][g][e] = 0.f;
 #pragma unroll
                     for (int kk = 0; kk < KS; ++kk)
 #pragma unroll
@@ -452,15 +602,22 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
                                 split(__uint_as_float(ys[2 * i]), hi[1], lo[1]);
                                 split(__uint_as_float(xs[2 * i + 1]), hi[2], lo[2]);
                                 split(__uint_as_float(ys[2 * i + 1]), hi[3], lo[3]);
-                                mma1688(s[t][0], hi, qf[kk][2 * i], qf[kk][2 * i + 1]);
-                                mma1688(small[t], lo, qf[kk][2 * i], qf[kk][2 * i + 1]);
-                                mma1688(small[t], hi, qf[kk][2 * i + 4], qf[kk][2 * i + 5]);
+#pragma unroll
+                                for (int g = 0; g < NG; ++g) {
+                                    uint4 y = make_uint4(qf[kk][2 * i], qf[kk][2 * i + 1], qf[kk][2 * i + 4], qf[kk][2 * i + 5]);
+                                    if (Q_SHARED) y = ld_shared_v4(q_at(2 * kk + i, g));
+                                    mma1688(s[t][g], hi, y.x, y.y);
+                                    mma1688(small[t][g], lo, y.x, y.y);
+                                    mma1688(small2[t][g], hi, y.z, y.w);
+                                }
                             }
                         }
 #pragma unroll
                     for (int t = 0; t < MT; ++t)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) s[t][0][e] += small[t][e];
+                        for (int g = 0; g < NG; ++g)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) s[t][g][e] += small[t][g][e] + small2[t][g][e];
                 } else if constexpr (!FP8) {
 #pragma unroll
                     for (int kk = 0; kk < KS; ++kk)
@@ -470,6 +627,24 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
                             ldmatrix_x4(x, kb + piece_at<ES, RB, false>(t * 16 + (lane & 15), kk * 2 + (lane >> 4)));
 #pragma unroll
                             for (int g = 0; g < NG; ++g) mma16816<FP8>(s[t][g], x, qf[kk][2 * g], qf[kk][2 * g + 1]);
+                        }
+                } else if constexpr (Q_SHARED) {
+#pragma unroll
+                    for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) {
+                            const uint4 x = ld_shared_v4(slot + piece_at<ES, RB, false>(t * 16 + r4, 4 * i + c4));
+                            const uint4 y = ld_shared_v4(slot + piece_at<ES, RB, false>(t * 16 + r4 + 8, 4 * i + c4));
+                            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                uint32_t k16[4];
+                                e4m3x4_f16(xs[j], k16[0], k16[2]);
+                                e4m3x4_f16(ys[j], k16[1], k16[3]);
+                                const uint4 q = ld_shared_v4(q_at(4 * i + j, 0));
+                                mma16816<FP8>(s[t][0], k16, q.x, q.y);
+                                mma16816<FP8>(s[t][NG - 1], k16, q.z, q.w);
+                            }
                         }
                 } else {
 #pragma unroll
@@ -515,6 +690,15 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
                             for (int g = 0; g < NG; ++g) s[t / 2][g][2 * (t & 1)] = s[t / 2][g][2 * (t & 1) + 1] = -INFINITY;
                         }
                 }
+                if (MANY && partly) {
+#pragma unroll
+                    for (int t = 0; t < WK / 8; ++t)
+#pragma unroll
+                        for (int g = 0; g < NG; ++g)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (key0 + 8 * t + r4 >= sees[g][e]) s[t / 2][g][2 * (t & 1) + e] = -INFINITY;
+                }
                 // running maximum (scores times zs; zs > 0), and the output brought to it
                 float f[NG][2];
                 bool moved = false;
@@ -536,20 +720,36 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
                             moved = true;
                         }
                     }
-                float vmove = 1.f;
-                if (FP8) {
-                    float top = fabsf(vs[0]);
+                float vmove[VG][VE], all_top = 0.f;
 #pragma unroll
-                    for (int t = 1; t < WK / 8; ++t) top = fmaxf(top, fabsf(vs[t]));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                    top = fmaxf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)), 1e-30f);   // its reciprocal is finite
-                    if (top > vref) {
-                        vmove = vref / top;
-                        vref = top;
-                        vinv = 1.f / top;
-                        moved = true;
-                    }
+                for (int g = 0; g < VG; ++g)
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) vmove[g][e] = 1.f;
+                if (FP8) {
+                    // the largest value scale (MANY: of the keys that a head sees)
+#pragma unroll
+                    for (int g = 0; g < VG; ++g)
+#pragma unroll
+                        for (int e = 0; e < VE; ++e) {
+                            float top = 0.f;
+                            if (MANY && !partly && g + e > 0) {
+                                top = all_top;
+                            } else {
+#pragma unroll
+                                for (int t = 0; t < WK / 8; ++t)
+                                    if (!MANY || !partly || key0 + 8 * t + r4 < sees[g][e]) top = fmaxf(top, fabsf(vs[t]));
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                                top = fmaxf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)), 1e-30f);   // its reciprocal is finite
+                                all_top = top;
+                            }
+                            if (top > vref[g][e]) {
+                                vmove[g][e] = vref[g][e] / top;
+                                vref[g][e] = top;
+                                vinv[g][e] = 1.f / top;
+                                moved = true;
+                            }
+                        }
                 }
                 if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -557,7 +757,7 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
 #pragma unroll
                         for (int g = 0; g < NG; ++g)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) o[t][g][e] *= f[g][e & 1] * vmove;
+                            for (int e = 0; e < 4; ++e) o[t][g][e] *= f[g][e & 1] * vmove[g % VG][e % VE];
                 }
 #pragma unroll
                 for (int g = 0; g < NG; ++g)
@@ -570,110 +770,180 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
                             for (int i = 0; i < 2; ++i) {
                                 const float p = fast_exp2(fmaf(s[t][g][2 * i + e], zs[g][e], -base));
                                 l[g][e] += p;
-                                s[t][g][2 * i + e] = FP8 ? p * (vs[2 * t + i] * vinv) : p;
+                                s[t][g][2 * i + e] = FP8 ? p * (vs[2 * t + i] * vinv[g % VG][e % VE]) : p;
+                                if (FP8 && MANY && partly && key0 + 16 * t + 8 * i + r4 >= sees[g][e]) s[t][g][2 * i + e] = 0.f;
                             }
                     }
-                // O^T += V^T P^T
-                if constexpr (FP32) {
-                    // k-step (t, i): keys 16 t + 8 i + 2 c4 (k = c4) and + 1 (k = c4 + 4); P^T's pieces by
-                    // shuffles from the lanes of those keys.  Rows r4 / r4 + 8 of tile j are dims
-                    // (D / 8) r4 + 2 j and + 1.
-                    constexpr int RUN = D / 8;
-                    float step[KS][4];
+                // O^T += V^T P^T.  Zero times a value that a row may not see need not be zero: where some
+                // such value is infinite or NaN, the product is formed once per row (ONE: the row of `sees`
+                // = n_keys) with the values behind its keys set to zero, for its columns alone.
+                auto product_o = [&](auto one, int n_keys) {
+                    constexpr bool ONE = decltype(one)::value;
+                    auto put = [&](float (&to)[4], const float (&from)[4], int g) {
 #pragma unroll
-                    for (int j = 0; j < KS; ++j)
+                        for (int e = 0; e < 4; ++e)
+                            if (sees[g][e & 1] == n_keys) to[e] = from[e];
+                    };
+                    auto shown = [&](int key) { return ONE && key0 + key >= n_keys ? 0u : 0xffffffffu; };
+                    if constexpr (FP32) {
+                        // k-step (t, i): keys 16 t + 8 i + 2 c4 (k = c4) and + 1 (k = c4 + 4); P^T's pieces by
+                        // shuffles from the lanes of those keys.  Rows r4 / r4 + 8 of tile j are dims
+                        // (D / 8) r4 + 2 j and + 1.
+                        constexpr int RUN = D / 8;
+                        uint32_t ph[2 * MT][NG][2], pl[2 * MT][NG][2];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) step[j][e] = 0.f;
+                        for (int ti = 0; ti < 2 * MT; ++ti)
 #pragma unroll
-                    for (int ti = 0; ti < 2 * MT; ++ti) {
-                        const int t = ti / 2, i = ti & 1;
-                        uint32_t ph[2], pl[2];
+                            for (int g = 0; g < NG; ++g)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int from = (2 * c4 + e) * 4 + (r4 >> 1);
-                            const float even = __shfl_sync(0xffffffffu, s[t][0][2 * i], from);
-                            const float odd = __shfl_sync(0xffffffffu, s[t][0][2 * i + 1], from);
-                            split((r4 & 1) ? odd : even, ph[e], pl[e]);
-                        }
-                        const int key = 16 * t + 8 * i + 2 * c4;
+                                for (int e = 0; e < 2; ++e) {
+                                    const int from = (2 * c4 + e) * 4 + (r4 >> 1);
+                                    const float even = __shfl_sync(0xffffffffu, s[ti / 2][g][2 * (ti & 1)], from);
+                                    const float odd = __shfl_sync(0xffffffffu, s[ti / 2][g][2 * (ti & 1) + 1], from);
+                                    split((r4 & 1) ? odd : even, ph[ti][g][e], pl[ti][g][e]);
+                                }
 #pragma unroll
                         for (int n4 = 0; n4 < RUN / 4; ++n4) {
-                            const uint4 x = ld_shared_v4(slot + SLICE + piece_at<ES, RB, true>(key, r4 * RUN / 4 + n4));
-                            const uint4 y = ld_shared_v4(slot + SLICE + piece_at<ES, RB, true>(key + 1, r4 * RUN / 4 + n4));
-                            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+                            float step[2][NG][4];
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                uint32_t hi[4], lo[4];
-                                split(__uint_as_float(xs[2 * k]), hi[0], lo[0]);
-                                split(__uint_as_float(xs[2 * k + 1]), hi[1], lo[1]);
-                                split(__uint_as_float(ys[2 * k]), hi[2], lo[2]);
-                                split(__uint_as_float(ys[2 * k + 1]), hi[3], lo[3]);
-                                mma1688(step[2 * n4 + k], lo, ph[0], ph[1]);
-                                mma1688(step[2 * n4 + k], hi, pl[0], pl[1]);
-                                mma1688(step[2 * n4 + k], hi, ph[0], ph[1]);
-                            }
-                        }
-                    }
+                            for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int j = 0; j < KS; ++j)
+                                for (int g = 0; g < NG; ++g)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) o[j][0][e] += step[j][e];
-                } else {
+                                    for (int e = 0; e < 4; ++e) step[k][g][e] = 0.f;
 #pragma unroll
-                    for (int t = 0; t < MT; ++t) {
-                        uint32_t pf[NG][2];
+                            for (int ti = 0; ti < 2 * MT; ++ti) {
+                                const int key = 8 * ti + 2 * c4;
+                                const uint4 x = ld_shared_v4(slot + SLICE + piece_at<ES, RB, true>(key, r4 * RUN / 4 + n4));
+                                const uint4 y = ld_shared_v4(slot + SLICE + piece_at<ES, RB, true>(key + 1, r4 * RUN / 4 + n4));
+                                const uint32_t mx = shown(key), my = shown(key + 1);
+                                const uint32_t xs[4] = {x.x & mx, x.y & mx, x.z & mx, x.w & mx};
+                                const uint32_t ys[4] = {y.x & my, y.y & my, y.z & my, y.w & my};
 #pragma unroll
-                        for (int g = 0; g < NG; ++g)
+                                for (int k = 0; k < 2; ++k) {
+                                    uint32_t hi[4], lo[4];
+                                    split(__uint_as_float(xs[2 * k]), hi[0], lo[0]);
+                                    split(__uint_as_float(xs[2 * k + 1]), hi[1], lo[1]);
+                                    split(__uint_as_float(ys[2 * k]), hi[2], lo[2]);
+                                    split(__uint_as_float(ys[2 * k + 1]), hi[3], lo[3]);
 #pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                pf[g][i] = transpose8(pack2<FP8>(s[t][g][2 * i], s[t][g][2 * i + 1]));
-                        if constexpr (!FP8) {
-                            // rows r4 / r4 + 8 of tile j are dims 16 j + r4 and + 8
-#pragma unroll
-                            for (int j = 0; j < KS; ++j) {
-                                uint32_t x[4];
-                                ldmatrix_x4_t(x, vb + piece_at<ES, RB, true>(t * 16 + (lane >> 4) * 8 + (lane & 7),
-                                                                             2 * j + ((lane >> 3) & 1)));
-#pragma unroll
-                                for (int g = 0; g < NG; ++g) mma16816<FP8>(o[j][g], x, pf[g][0], pf[g][1]);
-                            }
-                        } else {
-                            // rows r4 / r4 + 8 of tile j are dims (D / 8) r4 + 2 j and + 1; keys 2 c4 + {0, 1, 8, 9}
-                            constexpr int RUN = D / 8;
-                            uint32_t x[4][RUN / 4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int key = t * 16 + 2 * c4 + (k & 1) + 8 * (k >> 1);
-                                const uint8_t* src = slot + SLICE + piece_at<ES, RB, true>(key, r4 * RUN / 16) + (r4 * RUN) % 16;
-                                if (RUN == 16) {
-                                    const uint4 v = ld_shared_v4(src);
-                                    x[k][0] = v.x; x[k][1] = v.y; x[k][RUN / 4 - 2] = v.z; x[k][RUN / 4 - 1] = v.w;
-                                } else {
-                                    const uint2 v = *(const uint2*)src;
-                                    x[k][0] = v.x; x[k][1] = v.y;
+                                    for (int g = 0; g < NG; ++g) {
+                                        mma1688(step[k][g], lo, ph[ti][g][0], ph[ti][g][1]);
+                                        mma1688(step[k][g], hi, pl[ti][g][0], pl[ti][g][1]);
+                                        mma1688(step[k][g], hi, ph[ti][g][0], ph[ti][g][1]);
+                                    }
                                 }
                             }
 #pragma unroll
-                            for (int j = 0; j < RUN / 4; ++j) {
-                                // the pairs' codes side by side: dims 0, 1 and 2, 3 of keys 0, 1 and of 8, 9
-                                uint32_t v0[4], v1[4];
-                                e4m3x4_f16(__byte_perm(x[0][j], x[1][j], 0x5140), v0[0], v0[1]);
-                                e4m3x4_f16(__byte_perm(x[2][j], x[3][j], 0x5140), v0[2], v0[3]);
-                                e4m3x4_f16(__byte_perm(x[0][j], x[1][j], 0x7362), v1[0], v1[1]);
-                                e4m3x4_f16(__byte_perm(x[2][j], x[3][j], 0x7362), v1[2], v1[3]);
+                            for (int k = 0; k < 2; ++k)
 #pragma unroll
                                 for (int g = 0; g < NG; ++g) {
-                                    mma16816<FP8>(o[2 * j][g], v0, pf[g][0], pf[g][1]);
-                                    mma16816<FP8>(o[2 * j + 1][g], v1, pf[g][0], pf[g][1]);
+                                    float (&to)[4] = o[2 * n4 + k][g];
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) step[k][g][e] += to[e];
+                                    if (ONE) put(to, step[k][g], g);
+                                    else
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e) to[e] = step[k][g][e];
+                                }
+                        }
+                    } else {
+                        // keys 16 t + 2 c4 + {0, 1} lie in x[0] and x[1], + {8, 9} in x[2] and x[3]
+                        auto add = [&](int t, int j, int g, const uint32_t (&x)[4], uint32_t b0, uint32_t b1) {
+                            if (ONE) {
+                                float sum[4];
+                                uint32_t y[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    sum[e] = o[j][g][e];
+                                    const int key = 16 * t + 2 * c4 + 8 * (e >> 1);
+                                    y[e] = x[e] & ((shown(key) & 0xffffu) | (shown(key + 1) & 0xffff0000u));
+                                }
+                                mma16816<FP8>(sum, y, b0, b1);
+                                put(o[j][g], sum, g);
+                            } else {
+                                mma16816<FP8>(o[j][g], x, b0, b1);
+                            }
+                        };
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) {
+                            uint32_t pf[NG][2];
+#pragma unroll
+                            for (int g = 0; g < NG; ++g)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    pf[g][i] = transpose8(pack2<FP8>(s[t][g][2 * i], s[t][g][2 * i + 1]));
+                            if constexpr (!FP8) {
+                                // rows r4 / r4 + 8 of tile j are dims 16 j + r4 and + 8
+#pragma unroll
+                                for (int j = 0; j < KS; ++j) {
+                                    uint32_t x[4];
+                                    ldmatrix_x4_t(x, vb + piece_at<ES, RB, true>(t * 16 + (lane >> 4) * 8 + (lane & 7),
+                                                                                 2 * j + ((lane >> 3) & 1)));
+#pragma unroll
+                                    for (int g = 0; g < NG; ++g) add(t, j, g, x, pf[g][0], pf[g][1]);
+                                }
+                            } else {
+                                // rows r4 / r4 + 8 of tile j are dims (D / 8) r4 + 2 j and + 1; keys 2 c4 + {0, 1, 8, 9}
+                                constexpr int RUN = D / 8;
+                                uint32_t x[4][RUN / 4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const int key = t * 16 + 2 * c4 + (k & 1) + 8 * (k >> 1);
+                                    const uint8_t* src = slot + SLICE + piece_at<ES, RB, true>(key, r4 * RUN / 16) + (r4 * RUN) % 16;
+                                    if (RUN == 16) {
+                                        const uint4 v = ld_shared_v4(src);
+                                        x[k][0] = v.x; x[k][1] = v.y; x[k][RUN / 4 - 2] = v.z; x[k][RUN / 4 - 1] = v.w;
+                                    } else {
+                                        const uint2 v = *(const uint2*)src;
+                                        x[k][0] = v.x; x[k][1] = v.y;
+                                    }
+                                }
+#pragma unroll
+                                for (int j = 0; j < RUN / 4; ++j) {
+                                    // the pairs' codes side by side: dims 0, 1 and 2, 3 of keys 0, 1 and of 8, 9
+                                    uint32_t v0[4], v1[4];
+                                    e4m3x4_f16(__byte_perm(x[0][j], x[1][j], 0x5140), v0[0], v0[1]);
+                                    e4m3x4_f16(__byte_perm(x[2][j], x[3][j], 0x5140), v0[2], v0[3]);
+                                    e4m3x4_f16(__byte_perm(x[0][j], x[1][j], 0x7362), v1[0], v1[1]);
+                                    e4m3x4_f16(__byte_perm(x[2][j], x[3][j], 0x7362), v1[2], v1[3]);
+#pragma unroll
+                                    for (int g = 0; g < NG; ++g) {
+                                        add(t, 2 * j, g, v0, pf[g][0], pf[g][1]);
+                                        add(t, 2 * j + 1, g, v1, pf[g][0], pf[g][1]);
+                                    }
                                 }
                             }
                         }
                     }
+                };
+                bool apart = false;
+                if (MANY && partly) {
+                    bool odd = false;
+                    for (int r = max(w.least - key0, 0) + lane / PIECES; r < WK; r += max(32 / PIECES, 1))
+                        for (int c = lane % PIECES; c < PIECES; c += 32) {
+                            const uint4 x = ld_shared_v4(slot + SLICE + piece_at<ES, RB, true>(r, c));
+                            odd = odd || not_finite<ES>(x.x) || not_finite<ES>(x.y) || not_finite<ES>(x.z) || not_finite<ES>(x.w);
+                        }
+                    apart = __any_sync(0xffffffffu, odd);
+                }
+                if constexpr (MANY) {
+                    if (!apart) product_o(std::false_type{}, 0);
+                    else                                    // from row to row of different numbers of keys
+                        for (int i = 0; i < w.rows; ++i) {
+                            const int n_keys = keys_of(a, row_at(a, held, w.row + i).x, w.batch);
+                            bool again = false;
+                            for (int k = 0; k < i; ++k)
+                                again = again || keys_of(a, row_at(a, held, w.row + k).x, w.batch) == n_keys;
+                            if (!again) product_o(std::true_type{}, n_keys);
+                        }
+                } else {
+                    product_o(std::false_type{}, 0);
                 }
             }
             __syncwarp();
             if (u + 1 < n) {
-                request(st);
+                request_next(st);
                 st = st + 1 == STAGES ? 0 : st + 1;
             }
         }
@@ -690,7 +960,6 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
             }
         const bool begins = w.unit == 0, ends = w.unit + n == w.units;
         const int place = 2 * blockIdx.x + (begins ? 1 : 0);
-        const float carry = FP8 ? vref : 1.f;
         float* mine = (float*)(ring + st * SLOT);
 #pragma unroll
         for (int half = 0; half < NG; ++half) {
@@ -698,6 +967,7 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
             for (int t = 0; t < KS; ++t)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
+                    const float carry = FP8 ? vref[half % VG][e % VE] : 1.f;
                     if (ES == 2) {
                         mine[exch_at<D>(2 * c4 + e, 16 * t + r4)] = o[t][half][e];
                         mine[exch_at<D>(2 * c4 + e, 16 * t + r4 + 8)] = o[t][half][2 + e];
@@ -728,14 +998,15 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
                 }
                 if (begins && ends) {
                     const float inv = ll == 0.f ? 0.f : 1.f / ll;
-                    const int64_t to = ((int64_t)w.row * a.n_heads + h0 + h) * D + lane * VEC;
+                    const int hr = bunch ? a.by_group.div(h) : 0;
+                    const int64_t to_head = (int64_t)(w.row + hr) * a.n_heads + h0 + h - hr * group, to = to_head * D + lane * VEC;
 #pragma unroll
                     for (int v = 0; v < VEC; v += 2) {
                         if (FP32) *(float2*)((float*)a.out + to + v) = make_float2(acc[v] * inv, acc[v + 1] * inv);
                         else *(uint32_t*)((__nv_bfloat16*)a.out + to + v) = pack2<false>(acc[v] * inv, acc[v + 1] * inv);
                     }
                     if (lane == 0)
-                        a.lse[(int64_t)w.row * a.n_heads + h0 + h] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * LN2;
+                        a.lse[to_head] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * LN2;
                 } else {
                     float* po = parts.o + ((int64_t)place * GT + h) * D + lane * VEC;
 #pragma unroll
@@ -745,15 +1016,16 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D>::BLOCKS)) gqa_decode_k
             }
             __syncthreads();
         }
-        if (begins && tid == 0) {
+        if (begins && tid < (MANY ? w.rows : 1)) {
             const int64_t last = (at + w.units - 1) / stretch;      // block of the pair's last unit
-            parts.meta[((int64_t)w.row * a.n_kv_heads + w.kvh) * tiles + w.tile] = make_int2(blockIdx.x, (int)(last - blockIdx.x) + 1);
+            parts.meta[((int64_t)(w.row + tid) * a.n_kv_heads + w.kvh) * tiles + w.tile] =
+                make_int2(blockIdx.x, (int)(last - blockIdx.x) + 1 + (tid << 16));
         }
-        request(st);
+        request_next(st);
         st = st + 1 == STAGES ? 0 : st + 1;
         at += n;
         w.unit += n - 1;
-        w.next(a, tiles);
+        if (at < end) w.next(a, held, tiles);
     }
     cp_async_wait<0>();
 }
@@ -772,8 +1044,11 @@ __global__ void __launch_bounds__(128) gqa_combine_kernel(const DecodeArgs a, co
     if (item >= (int64_t)a.rows * a.n_heads) return;
     const int row = (int)(item / a.n_heads), head = (int)(item - (int64_t)row * a.n_heads);
     const int group = a.n_heads / a.n_kv_heads, tiles = ceil_div(group, GT);
-    const int kvh = head / group, in = head - kvh * group, tile = in / GT, h = in - tile * GT;
-    const int2 me = parts.meta[(int64_t)row * a.n_kv_heads * tiles + kvh * tiles + tile];
+    const int kvh = head / group, in = head - kvh * group, tile = in / GT;
+    int h = in - tile * GT;
+    int2 me = parts.meta[(int64_t)row * a.n_kv_heads * tiles + kvh * tiles + tile];
+    if (GT == 16) h += (me.y >> 16) * group;                // the row's columns within its bunch
+    me.y &= 0xffff;
     if (me.y <= 1) return;                                  // written whole
     // part 0 lies in the first block's "begins" place, the others in the
     // "continues" places of the blocks behind it; four parts' numbers are
@@ -817,24 +1092,39 @@ __global__ void __launch_bounds__(128) gqa_combine_kernel(const DecodeArgs a, co
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Heads per pair: as many rows of the product as the group fills (16, or 8
-// when the upper half would be idle); 8 in fp32, whose split queries fill the
-// registers.
-int head_tile(dsa_dtype_t kv, int group) { return kv == DSA_FP32 || group <= 8 ? 8 : 16; }
-int blocks_per_sm(dsa_dtype_t kv, int d) {
-    return kv == DSA_FP32   ? (d == 64 ? MmaCfg<float, 64>::BLOCKS : MmaCfg<float, 128>::BLOCKS)
-           : kv == DSA_BF16 ? (d == 64 ? MmaCfg<__nv_bfloat16, 64>::BLOCKS : MmaCfg<__nv_bfloat16, 128>::BLOCKS)
-                            : MmaCfg<__nv_fp8_e4m3, 128>::BLOCKS;
+// Rows of one sequence that share a pair: as many as fill the products' 16
+// columns, when there are at least two rows a sequence on average and they
+// come in runs of about `tokens`.
+int tokens_of(int rows, int batch) { return ceil_div(rows, batch); }
+int merge_of(int group, int tokens) {
+    const int most = 16 / group;
+    return most < 2 || tokens < 2 ? 1 : ceil_div(tokens, ceil_div(tokens, most));
+}
+// Heads per pair: as many columns of the products as the pair fills (16, or 8
+// when half of them would be idle).
+int head_tile(int group, int merge) { return group > 8 || merge > 1 ? 16 : 8; }
+template <int GT> int blocks_per_sm(dsa_dtype_t kv, int d) {
+    return kv == DSA_FP32   ? (d == 64 ? MmaCfg<float, 64, GT>::BLOCKS : MmaCfg<float, 128, GT>::BLOCKS)
+           : kv == DSA_BF16 ? (d == 64 ? MmaCfg<__nv_bfloat16, 64, GT>::BLOCKS : MmaCfg<__nv_bfloat16, 128, GT>::BLOCKS)
+           : d == 64        ? MmaCfg<__nv_fp8_e4m3, 64, GT>::BLOCKS
+                            : MmaCfg<__nv_fp8_e4m3, 128, GT>::BLOCKS;
 }
 
-template <typename Q, int D, int GT, class Kern>
-cudaError_t launch_decode(const Launch& L, const DecodeArgs& a, Kern kern, int smem, int per_sm, void* workspace) {
-    const int grid = L.num_sms * per_sm;
+template <typename Q, typename KV, int D, int GT>
+cudaError_t launch_tile(const Launch& L, const DecodeArgs& a, void* workspace) {
+    using C = MmaCfg<KV, D, GT>;
+    constexpr bool FP8 = sizeof(KV) == 1;
+    constexpr int slot = 2 * C::WK * D * (int)sizeof(KV) + (FP8 ? 2 * C::WK * 4 : 0) + 16;
+    constexpr int smem = WARPS * C::STAGES * slot + C::Q_BYTES;
+    const auto kern = gqa_decode_kernel<KV, D, GT>;
+    static std::atomic<int> done[kMaxDevices];
+    cudaError_t e = allow_smem(done, kern, smem);
+    if (e != cudaSuccess) return e;
+    const int grid = L.num_sms * C::BLOCKS;
     Parts p;
     p.o = (float*)workspace;
     p.ml = (float2*)((char*)workspace + up256((size_t)2 * grid * GT * D * 4));
     p.meta = (int2*)((char*)p.ml + up256((size_t)2 * grid * GT * 8));
-    cudaError_t e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1] = {pdl_attr()};
     cfg.gridDim = dim3(grid);
@@ -856,35 +1146,37 @@ cudaError_t launch_decode(const Launch& L, const DecodeArgs& a, Kern kern, int s
 
 template <typename Q, typename KV, int D>
 cudaError_t launch_typed(const Launch& L, const DecodeArgs& a, void* workspace) {
-    constexpr bool FP8 = sizeof(KV) == 1;
-    constexpr int WK = MmaCfg<KV, D>::WK, slot = 2 * WK * D * (int)sizeof(KV) + (FP8 ? 2 * WK * 4 : 0) + 16;
-    constexpr int smem = WARPS * MmaCfg<KV, D>::STAGES * slot, per_sm = MmaCfg<KV, D>::BLOCKS;
-    static std::atomic<int> done8[kMaxDevices];
-    [[maybe_unused]] static std::atomic<int> done16[kMaxDevices];
-    cudaError_t e;
-    if constexpr (sizeof(KV) != 4) {
-        if (a.n_heads / a.n_kv_heads > 8) {
-            e = allow_smem(done16, gqa_decode_kernel<KV, D, 16>, smem);
-            if (e != cudaSuccess) return e;
-            return launch_decode<Q, D, 16>(L, a, gqa_decode_kernel<KV, D, 16>, smem, per_sm, workspace);
-        }
-    }
-    e = allow_smem(done8, gqa_decode_kernel<KV, D, 8>, smem);
-    if (e != cudaSuccess) return e;
-    return launch_decode<Q, D, 8>(L, a, gqa_decode_kernel<KV, D, 8>, smem, per_sm, workspace);
+    return head_tile(a.n_heads / a.n_kv_heads, a.merge) == 16 ? launch_tile<Q, KV, D, 16>(L, a, workspace)
+                                                              : launch_tile<Q, KV, D, 8>(L, a, workspace);
+}
+
+template <int GT> size_t workspace_of(int rows, int n_heads, int n_kv_heads, int head_dim, dsa_dtype_t kv, int num_sms) {
+    const size_t grid = (size_t)num_sms * blocks_per_sm<GT>(kv, head_dim);
+    const size_t pairs = (size_t)rows * n_kv_heads * ceil_div(n_heads / n_kv_heads, GT);
+    return up256(2 * grid * GT * head_dim * 4) + up256(2 * grid * GT * 8) + pairs * 8;
 }
 
 }  // namespace
 
+// (The number of sequences is not asked for: enough for either head tile,
+// where rows might share pairs.)
 size_t gqa_decode_workspace_bytes(int rows, int n_heads, int n_kv_heads, int head_dim, dsa_dtype_t kv, int num_sms) {
     const int group = n_heads / n_kv_heads;
-    const size_t grid = (size_t)num_sms * blocks_per_sm(kv, head_dim), gt = head_tile(kv, group);
-    const size_t pairs = (size_t)rows * n_kv_heads * ceil_div(group, (int)gt);
-    return up256(2 * grid * gt * head_dim * 4) + up256(2 * grid * gt * 8) + pairs * 8;
+    const size_t one = workspace_of<8>(rows, n_heads, n_kv_heads, head_dim, kv, num_sms);
+    const size_t many = workspace_of<16>(rows, n_heads, n_kv_heads, head_dim, kv, num_sms);
+    return group > 8 ? many : rows == 1 || one > many ? one : many;
 }
 
-cudaError_t launch_gqa_decode(const Launch& L, const DecodeArgs& a, dsa_dtype_t kv, int head_dim, void* workspace) {
+cudaError_t launch_gqa_decode(const Launch& L, const DecodeArgs& args, dsa_dtype_t kv, int head_dim, void* workspace) {
     typedef __nv_bfloat16 bf16;
+    DecodeArgs a = args;
+    a.tokens = tokens_of(a.rows, a.batch);
+    a.merge = merge_of(a.n_heads / a.n_kv_heads, a.tokens);
+    a.by_tokens = fast_div(a.tokens);
+    a.by_merge = fast_div(a.merge);
+    a.by_group = fast_div(a.n_heads / a.n_kv_heads);
+    const int64_t room = (int64_t)a.max_pages * a.page_size;
+    a.room = room < 0x7fffffff ? (int)room : 0x7fffffff;
     if (kv == DSA_FP32)
         return head_dim == 64 ? launch_typed<float, float, 64>(L, a, workspace) : launch_typed<float, float, 128>(L, a, workspace);
     if (kv == DSA_BF16)

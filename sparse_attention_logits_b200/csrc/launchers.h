@@ -161,6 +161,9 @@ struct DecodeArgs {
     const int32_t* row_pos;
     int rows, n_heads, n_kv_heads;
     FastDiv by_page;            // by page_size
+    // set by the launcher: rows a sequence on average; rows that may share a pair; max_pages * page_size
+    int tokens, merge, room;
+    FastDiv by_tokens, by_merge, by_group;
     float scale_log2;
     void* out;                  // [rows, n_heads, head_dim]
     float* lse;                 // [rows, n_heads]

@@ -294,6 +294,62 @@ def test_decode_empty_rows_and_shuffled_batch(cuda_device, kind):
     _decode_check(c, q, out, lse, batch, [-1] * 7, 0.2)
 
 
+# several rows of a sequence beside each other share its reads:
+# (sequence lengths, [(sequence, position), ...], heads, kv heads, dim, page)
+SHARED = {
+    "drafts_of_4": ([1000, 7, 129, 4000], [(b, n - 4 + i) for b, n in enumerate([1000, 7, 129, 4000]) for i in range(4)],
+                    8, 2, 128, 64),
+    "drafts_of_2_d64": ([300, 128, 129], [(b, n - 2 + i) for b, n in enumerate([300, 128, 129]) for i in range(2)], 16, 2, 64, 16),
+    "drafts_of_6_group_5": ([700, 64], [(b, n - 6 + i) for b, n in enumerate([700, 64]) for i in range(6)], 10, 2, 64, 5),
+    "mha_of_20": ([500], [(0, 480 + i) for i in range(20)], 3, 3, 128, 16),
+    "falling": ([900], [(0, p) for p in (899, 640, 639, 12)], 4, 1, 128, 64),
+    "far_apart": ([3000], [(0, p) for p in (200, 2999, 5, 2600)], 4, 1, 64, 32),
+    "one_place": ([777], [(0, 700)] * 5, 6, 2, 128, 64),
+    "whole_units": ([1024], [(0, p) for p in (127, 255, 127, 511)], 8, 2, 128, 64),
+    "empty_ones": ([400, 50], [(0, 399), (0, -1), (0, 380), (1, -1), (1, -1), (1, 49)], 4, 1, 128, 16),
+    "uneven": ([600, 90, 10, 300], [(0, 599), (1, 85), (1, 86), (1, 87), (1, 88), (1, 89), (2, 9), (3, 290), (3, 291), (0, 12)],
+               8, 2, 64, 16),
+    "long": ([30000], [(0, 29997 + i) for i in range(3)], 5, 1, 64, 64),
+    "many": ([40 + 9 * i for i in range(70)], [(b, 39 + 9 * b - i) for b in range(70) for i in range(3)], 8, 2, 64, 16),
+    "very_many": ([20 + 5 * i for i in range(140)], [(b, 19 + 5 * b - i) for b in range(140) for i in range(2)], 4, 2, 64, 16),
+}
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp32"])
+@pytest.mark.parametrize("case", list(SHARED))
+def test_decode_rows_that_share_a_sequence(cuda_device, case, kind):
+    lens, rows, H, Hkv, D, page = SHARED[case]
+    c = Paged(lens, Hkv, D, page, kind, 23)
+    batch, pos = [b for b, _ in rows], [p for _, p in rows]
+    q = _randn((len(rows), H, D), _gen(24), torch.float32 if kind == "fp32" else torch.bfloat16)
+    out, lse = dsa.gqa_decode_attention(q, c.k, c.v, c.table, _i32(batch), _i32(pos), 0.15, c.k_scale, c.v_scale)
+    assert dsa.get_device_error(cuda_device) == dsa.DSA_OK
+    _decode_check(c, q, out, lse, batch, pos, 0.15)
+    again = dsa.gqa_decode_attention(q, c.k, c.v, c.table, _i32(batch), _i32(pos), 0.15, c.k_scale, c.v_scale)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp32"])
+@pytest.mark.parametrize("n", [3, 130, 700])
+def test_decode_rows_never_see_later_tokens(cuda_device, kind, n):
+    """Four rows of a sequence whose last two tokens are NaN, infinite or 1e30 times the others."""
+    D = 64
+    c = Paged([n + 4, 50], 2, D, 16, kind, 25)
+    batch, pos = [0, 0, 0, 0, 1], [n, n + 1, n + 2, n + 3, 49]
+    q = _randn((5, 8, D), _gen(26), torch.float32 if kind == "fp32" else torch.bfloat16)
+
+    def put(x, at, value):
+        x[int(c.table[0, at // 16]), :, at % 16] = value
+    for bad in (NAN, math.inf, 1e30):
+        for at in (n + 2, n + 3):
+            for x in (c.k_scale, c.v_scale) if kind == "fp8" else (c.k, c.v):
+                put(x, at, bad)
+        out, lse = dsa.gqa_decode_attention(q, c.k, c.v, c.table, _i32(batch), _i32(pos), 0.15, c.k_scale, c.v_scale)
+        assert dsa.get_device_error(cuda_device) == dsa.DSA_OK
+        keep = [0, 1, 4]
+        _decode_check(c, q[keep], out[keep], lse[keep], [0, 0, 1], [n, n + 1, 49], 0.15)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "fp32"])
 def test_decode_large_scores(cuda_device, kind):
     """Scores of a few hundred that grow along the sequence: every slice moves the maximum."""
