@@ -436,7 +436,7 @@ DSA_API size_t gqa_decode_attention_workspace_size(int rows, int n_heads, int n_
  * One row per sequence decodes one token; several rows of a sequence (at
  * successive positions) verify several tokens or run a piece of a prompt.
  * Rows of one sequence beside each other share the reads of its cache as far
- * as their heads fill 16 columns, when rows > batch.
+ * as their heads fill 16 columns, when rows >= 1.5 * batch.
  *   q          [rows, n_heads, head_dim] of dtype, rows ld_q elements apart, 16-byte
  *              aligned rows; n_heads a multiple of n_kv_heads
  *   row_pos    [rows] int32: last visible token; < 0: none (out = 0, lse = -inf), as

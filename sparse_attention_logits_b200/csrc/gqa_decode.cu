@@ -1093,9 +1093,10 @@ __global__ void __launch_bounds__(128) gqa_combine_kernel(const DecodeArgs a, co
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Rows of one sequence that share a pair: as many as fill the products' 16
-// columns, when there are at least two rows a sequence on average and they
-// come in runs of about `tokens`.
-int tokens_of(int rows, int batch) { return ceil_div(rows, batch); }
+// columns, when the sequences have one and a half rows or more on average (16
+// heads a pair cost up to 1.4 times the time of 8 per byte, over fp8) and come in
+// runs of about `tokens`.
+int tokens_of(int rows, int batch) { return 2ll * rows < 3ll * batch ? 1 : ceil_div(rows, batch); }
 int merge_of(int group, int tokens) {
     const int most = 16 / group;
     return most < 2 || tokens < 2 ? 1 : ceil_div(tokens, ceil_div(tokens, most));

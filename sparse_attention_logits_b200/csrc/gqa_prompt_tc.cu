@@ -31,6 +31,7 @@
 // the prompt (they belong to other prompts, and 0 times their infinities
 // would not be 0).  Items are taken longest first.
 #include "common.cuh"
+#include "gqa_prompt.cuh"
 #include "launchers.h"
 #include "sm100.cuh"
 #include "tensor_map.h"
@@ -48,7 +49,6 @@ constexpr int THREADS = 384;
 constexpr int REGS_SOFTMAX = 216, REGS_REST = 72;
 static_assert(256 * REGS_SOFTMAX + 128 * REGS_REST <= 168 * THREADS, "register split exceeds launch");
 constexpr int TMEM_COLS = 512;
-constexpr int INLINE_SEQS = 32;     // prompts that a warp schedules without a list
 constexpr float RESCALE_LOG2 = 8.f;
 // Of 16 exponentials, how many run on the multiply-add pipe, and how many of
 // a tile's four 32-key pieces of P are announced together first.  Cycles per
@@ -86,53 +86,30 @@ struct Sched {                      // where the items come from
 
 // One warp's view of the items, longest first.
 struct Items {
-    int start, len, blocks;         // of prompt `lane` (inline scheduling)
+    PromptLanes lanes;              // without a list
     int entries;
 
     __device__ __forceinline__ void init(const PromptArgs& a, const Sched& s) {
-        const int lane = threadIdx.x & 31;
         if (s.list) {
             entries = *s.count;
-            return;
+        } else {
+            lanes.init(a, s.rows_per_block);
+            entries = lanes.at_least(1);
         }
-        start = len = 0;
-        if (lane < a.n_seqs) bounds(a, lane, start, len);
-        blocks = (len + s.rows_per_block - 1) / s.rows_per_block;
-        entries = at_least(1);
-    }
-    static __device__ __forceinline__ void bounds(const PromptArgs& a, int seq, int& start, int& len) {
-        start = a.cu_seqlens[seq];
-        len = a.cu_seqlens[seq + 1] - start;
-        if (start < 0 || len < 0 || (int64_t)start + len > a.total) {
-            record_error(a.err, DEV_ERR_BAD_INDEX);
-            start = len = 0;
-        }
-    }
-    // row blocks whose number (from 1) within their prompt is at least v
-    __device__ __forceinline__ int at_least(int v) const {
-        return (int)__reduce_add_sync(0xffffffffu, (unsigned)max(0, blocks - v + 1));
     }
     // Entry e: blocks in falling order of their number (their work); false past the end.
     __device__ __forceinline__ bool get(const PromptArgs& a, const Sched& s, int e, int& first, int& n, int& row0) const {
         if (e >= entries) return false;
+        int block;
         if (s.list) {
             const Entry x = s.list[e];
             first = a.cu_seqlens[x.seq];
             n = a.cu_seqlens[x.seq + 1] - first;
-            row0 = x.block * s.rows_per_block;
-            return true;
+            block = x.block;
+        } else {
+            lanes.get(e, first, n, block);
         }
-        int lo = 1, hi = (int)__reduce_max_sync(0xffffffffu, (unsigned)blocks) + 1;
-        while (hi - lo > 1) {                   // at_least(lo) > e >= at_least(hi)
-            const int mid = (lo + hi) >> 1;
-            if (at_least(mid) > e) lo = mid;
-            else hi = mid;
-        }
-        const unsigned have = __ballot_sync(0xffffffffu, blocks >= lo);
-        const int seq = (int)__fns(have, 0, e - at_least(lo + 1) + 1);
-        first = __shfl_sync(0xffffffffu, start, seq);
-        n = __shfl_sync(0xffffffffu, len, seq);
-        row0 = (lo - 1) * s.rows_per_block;
+        row0 = block * s.rows_per_block;
         return true;
     }
 };
@@ -238,7 +215,7 @@ __global__ void __launch_bounds__(1024) gqa_prompt_list_kernel(const PromptArgs 
     auto bin_of = [](int block) { return LIST_BINS - 1 - min(block, LIST_BINS - 1); };
     for (int s = warp; s < a.n_seqs; s += 32) {
         int start, len;
-        Items::bounds(a, s, start, len);
+        prompt_bounds(a, s, start, len);
         const int blocks = (len + rows_per_block - 1) / rows_per_block;
         for (int b = lane; b < blocks; b += 32) atomicAdd(&bins[bin_of(b)], 1);
     }
@@ -269,7 +246,7 @@ __global__ void __launch_bounds__(1024) gqa_prompt_list_kernel(const PromptArgs 
     __syncthreads();
     for (int s = warp; s < a.n_seqs; s += 32) {
         int start, len;
-        Items::bounds(a, s, start, len);
+        prompt_bounds(a, s, start, len);
         const int blocks = (len + rows_per_block - 1) / rows_per_block;
         for (int b = lane; b < blocks; b += 32) {
             const int at = atomicAdd(&bins[bin_of(b)], 1);
@@ -656,7 +633,7 @@ cudaError_t launch(const Launch& L, const PromptArgs& a, void* workspace) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const int most = max_entries(a.total, a.n_seqs);
-    if (a.n_seqs > INLINE_SEQS) {
+    if (a.n_seqs > LANE_SEQS) {
         s.count = (const int*)workspace;
         s.list = (const Entry*)((char*)workspace + 256);
         cfg.gridDim = dim3(1);
@@ -677,7 +654,7 @@ cudaError_t launch(const Launch& L, const PromptArgs& a, void* workspace) {
 }  // namespace
 
 size_t gqa_prompt_workspace_bytes(int total, int n_seqs, dsa_dtype_t dtype) {
-    if (dtype != DSA_BF16 || n_seqs <= INLINE_SEQS) return 0;
+    if (dtype != DSA_BF16 || n_seqs <= LANE_SEQS) return 0;
     return 256 + (size_t)max_entries(total, n_seqs) * sizeof(Entry);
 }
 

@@ -361,8 +361,8 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
     return r;
 }
 
-// Whole-cluster barrier (all threads of all CTAs).  Only used right after
-// launch, when every CTA of the cluster is resident by construction.
+// Whole-cluster barrier (all threads of all CTAs).  Every CTA of a cluster is
+// resident by construction; all of its threads must come here on every path.
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }

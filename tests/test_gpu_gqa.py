@@ -46,6 +46,11 @@ PROMPTS = {
     "many_short": ([(7 * i) % 23 for i in range(150)], 0, 0, 2, 2, 128, "bf16"),
     "fp32": ([1, 63, 64, 65, 0, 300], 2, 3, 6, 2, 64, "fp32"),
     "fp32_d128": ([200, 31], 0, 0, 4, 4, 128, "fp32"),
+    "fp32_some_tiles": ([31, 900, 400], 1, 0, 8, 4, 64, "fp32"),
+    "fp32_some_tiles_d128": ([900, 64, 3], 0, 2, 8, 2, 128, "fp32"),
+    "fp32_many_tiles": ([700, 33, 800, 600], 0, 0, 16, 4, 64, "fp32"),
+    "fp32_many_tiles_d128": ([129, 900], 0, 0, 16, 16, 128, "fp32"),
+    "fp32_many_prompts": ([(29 * i) % 140 for i in range(40)], 0, 0, 4, 1, 64, "fp32"),
 }
 DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
 
