@@ -48,7 +48,7 @@ constexpr int APPEND_ROWS = 32, APPEND_UNROLL = 2;
 // exact remainder, q <- q + r (x - q sc): by P. Markstein's theorem
 // ("Computation of elementary functions on the IBM RISC System/6000
 // processor", 1990) the second correction of a quotient within one unit gives
-// the correctly rounded one.  Five multiply-adds a value against about twelve
+// the correctly rounded one.  Five multiply-adds two values against about twelve
 // instructions of a division, which made the kernel issue-bound (52 us where
 // the loads and stores take 20).  Bits matter here: bf16 rows hold values that
 // fall exactly between two codes, about one in a hundred.  Below 2^-60 the
@@ -57,11 +57,15 @@ __device__ __forceinline__ uint4 e4m3_codes(const float (&x)[16], float sc) {
     float q[16];
     if (sc >= 0x1p-60f) {
         const float r = __frcp_rn(sc);
+        const float2 r2 = make_float2(r, r), m2 = make_float2(-sc, -sc), zero = make_float2(-0.f, -0.f);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            float y = x[e] * r;
-            y = fmaf(r, fmaf(-y, sc, x[e]), y);
-            q[e] = fmaf(r, fmaf(-y, sc, x[e]), y);
+        for (int e = 0; e < 16; e += 2) {                   // (two values an instruction, each rounded as one)
+            const float2 v = make_float2(x[e], x[e + 1]);
+            float2 y = fma2(v, r2, zero);
+            y = fma2(r2, fma2(y, m2, v), y);
+            y = fma2(r2, fma2(y, m2, v), y);
+            q[e] = y.x;
+            q[e + 1] = y.y;
         }
     } else {
 #pragma unroll
@@ -155,8 +159,22 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
                                                 bf16x2_bits(f[8 * i + 4], f[8 * i + 5]), bf16x2_bits(f[8 * i + 6], f[8 * i + 7]));
                     } else {
                         float amax = 0.f;
+                        if (F32_IN) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(f[e]));
+                            for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(f[e]));
+                        } else {                            // (bf16 numbers: their maximum is one of them)
+                            __nv_bfloat162 top = __float2bfloat162_rn(0.f);
+#pragma unroll
+                            for (int i = 0; i < W; ++i) {
+                                const uint32_t w[4] = {x[u][i].x, x[u][i].y, x[u][i].z, x[u][i].w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t a2 = w[e] & 0x7fff7fffu;
+                                    top = __hmax2(top, *(const __nv_bfloat162*)&a2);
+                                }
+                            }
+                            amax = fmaxf(__low2float(top), __high2float(top));
+                        }
 #pragma unroll
                         for (int m = LANES / 2; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(group, amax, m));
                         const float sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
