@@ -165,25 +165,32 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::BLOCKS) gqa_prompt_f32_kernel
     const int keys = w.row0 + rows;                     // the tile's last row sees this many
 
     float2 kx[LOADS], vx[LOADS];                        // the next tile's rows, on their way
+    // piece i of a thread: key KI i + tid / HALF, dims 2 (tid % HALF) and + 1 of K;
+    // keys KI i + 2 (tid / D) and + 1, dim tid % D of V
+    constexpr int KI = GROUP / HALF;
+    const int kr = tid / HALF, vr = tid / D, vd = tid % D;
+    const float* const k_from = kb + (int64_t)kr * a.ld_k + 2 * (tid % HALF);
+    const float* const v_from = vb + 2 * (int64_t)vr * a.ld_v + vd;
     auto request = [&](int k0) {
+        const float *kp = k_from + (int64_t)k0 * a.ld_k, *vp = v_from + (int64_t)k0 * a.ld_v;
+        const bool whole = k0 + BN <= keys;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
-            const int p = i * GROUP + tid;
-            const int key = k0 + p / HALF, d2 = p % HALF;
-            kx[i] = key < keys ? __ldg((const float2*)(kb + (int64_t)key * a.ld_k) + d2) : make_float2(0.f, 0.f);
-            const int key0 = k0 + 2 * (p / D), d = p % D;
-            vx[i].x = key0 < keys ? __ldg(vb + (int64_t)key0 * a.ld_v + d) : 0.f;
-            vx[i].y = key0 + 1 < keys ? __ldg(vb + (int64_t)(key0 + 1) * a.ld_v + d) : 0.f;
+            const int left = keys - k0 - i * KI;            // keys from the piece's first on
+            kx[i] = whole || kr < left ? __ldg((const float2*)kp) : make_float2(0.f, 0.f);
+            vx[i].x = whole || 2 * vr < left ? __ldg(vp) : 0.f;
+            vx[i].y = whole || 2 * vr + 1 < left ? __ldg(vp + a.ld_v) : 0.f;
+            kp += KI * a.ld_k;
+            vp += KI * a.ld_v;
         }
     };
+    uint4* const k_to = sk + kr * HALF + ((tid % HALF) ^ ((kr & 1) << 2));     // (KI is even)
     auto store = [&]() {
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
-            const int p = i * GROUP + tid;
-            const int key = p / HALF, d2 = p % HALF;
-            sk[key * HALF + (d2 ^ ((key & 1) << 2))] = split2(kx[i].x, kx[i].y);
-            const int pair = p / D, d = p % D;
-            sv[pair * D + (d ^ ((pair & 3) << 1))] = split2(vx[i].x, vx[i].y);
+            k_to[i * KI * HALF] = split2(kx[i].x, kx[i].y);
+            const int pair = i * (KI / 2) + vr;
+            sv[pair * D + (vd ^ ((pair & 3) << 1))] = split2(vx[i].x, vx[i].y);
         }
     };
     constexpr bool AHEAD = C::BLOCKS == 1;              // (two blocks an SM hide each other's loads)
@@ -200,6 +207,9 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::BLOCKS) gqa_prompt_f32_kernel
         for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     const int row = warp * 16 + r4;                     // this lane's rows of the tile: row, row + 8
+    const int odd = (r4 & 1) << 2;
+    const uint4 *const q_from = sq + row * HALF + c4, *const k_at = sk + r4 * HALF + c4;
+    const uint4* const v_at = sv + c4 * D + (r4 ^ (c4 << 1));
     const int last = w.row0 + min(rows, warp * 16 + 16) - 1;    // the warp's last row
     __syncthreads();                                    // the queries stand
     for (int k0 = walker * BN; k0 < keys; k0 += WALKERS * BN) {
@@ -217,14 +227,14 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::BLOCKS) gqa_prompt_f32_kernel
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[t][e] = small[t][e] = 0.f;
         // k-step kk: dims 8 kk + 2 c4 (k = c4) and 8 kk + 2 c4 + 1 (k = c4 + 4)
-#pragma unroll 2
+#pragma unroll 4
         for (int kk = 0; kk < D / 8; ++kk) {
-            const uint4 x = sq[row * HALF + ((4 * kk + c4) ^ ((row & 1) << 2))];
-            const uint4 y = sq[(row + 8) * HALF + ((4 * kk + c4) ^ ((row & 1) << 2))];
+            const int at = 4 * (kk & ~1) + ((kk & 1) ? 4 - odd : odd);      // (4 kk + c4) ^ 4 (row & 1), less c4
+            const uint4 x = q_from[at], y = q_from[8 * HALF + at];
             const uint32_t hi[4] = {x.x, y.x, x.z, y.z}, lo[4] = {x.y, y.y, x.w, y.w};
             uint4 b[ST];
 #pragma unroll
-            for (int t = 0; t < ST; ++t) b[t] = sk[(8 * t + r4) * HALF + ((4 * kk + c4) ^ ((r4 & 1) << 2))];
+            for (int t = 0; t < ST; ++t) b[t] = k_at[8 * t * HALF + at];
             mma_split<ST>(s, small, hi, lo, b);
         }
 #pragma unroll
@@ -232,19 +242,24 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::BLOCKS) gqa_prompt_f32_kernel
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[t][e] += small[t][e];
         // lane: rows row, row + 8; keys k0 + 8 t + 2 c4 + {0, 1}
+        if (k0 + BN - 1 > w.row0 + warp * 16) {             // some keys lie behind some rows
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int t = 0; t < ST; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (k0 + 8 * t + 2 * c4 + e > w.row0 + row + 8 * half) s[t][2 * half + e] = -INFINITY;
+        }
         float f[2];
         bool moved = false;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const int at = w.row0 + row + 8 * half;
             float top = -INFINITY;
 #pragma unroll
             for (int t = 0; t < ST; ++t)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (k0 + 8 * t + 2 * c4 + e > at) s[t][2 * half + e] = -INFINITY;
-                    top = fmaxf(top, s[t][2 * half + e]);
-                }
+                for (int e = 0; e < 2; ++e) top = fmaxf(top, s[t][2 * half + e]);
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             f[half] = 1.f;
@@ -289,7 +304,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::BLOCKS) gqa_prompt_f32_kernel
                 const uint32_t hi[4] = {x.x, y.x, x.z, y.z}, lo[4] = {x.y, y.y, x.w, y.w};
                 uint4 b[NB];
 #pragma unroll
-                for (int n = 0; n < NB; ++n) b[n] = sv[(4 * t + c4) * D + ((8 * (n0 + n) + r4) ^ (c4 << 1))];
+                for (int n = 0; n < NB; ++n) b[n] = v_at[4 * t * D + 8 * (n0 + n)];
                 mma_split<NB>(step, step, hi, lo, b);
             }
 #pragma unroll
