@@ -5,8 +5,8 @@
 // Every factor is split into two tf32 numbers, x = hi + lo (11 + 11 bits), and a
 // product is three tensor products hi hi + hi lo + lo hi; what is left out or
 // rounded is at most 3 x 2^-22 of |x y| a term, no more than a dot product of a
-// few fp32 terms.  1800 tokens in 3 prompts, 8 / 4 heads of 64: 61 us (fp32
-// multiply-adds on the CUDA cores: 121 us); 4000 in 8 prompts, 16 / 4 heads: 160 us.
+// few fp32 terms.  1800 tokens in 3 prompts, 8 / 4 heads of 64: 54 us (fp32
+// multiply-adds on the CUDA cores: 121 us); 4000 in 8 prompts, 16 / 4 heads: 146 us.
 //
 // A tile is 64 query rows of one head.  A block's two groups of 4 warps, 16 rows a
 // warp, and those of up to three more blocks of its cluster walk the tile's keys
@@ -18,8 +18,8 @@
 // neighbouring keys (V); which dims or keys a k-step takes is free as long as
 // both factors agree.  Two blocks an SM hide each
 // other's loads (head dim 128, one block: the next keys' rows are requested
-// before the present ones' products).  Bound by latencies: about 2000 instructions
-// a warp and 32 keys, a third of the issue slots in use.
+// before the present ones' products).  Bound by latencies and barriers between
+// the splitting of a tile and its products, at about half of the issue slots.
 #include "common.cuh"
 #include "gqa_prompt.cuh"
 #include "launchers.h"
@@ -370,9 +370,9 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::BLOCKS) gqa_prompt_f32_kernel
 
 // Blocks that share a tile.  A tile's time is its keys', so where there are few
 // tiles each is cut among more blocks, whose own start and end count otherwise.
-// us with 1 / 2 / 4 blocks: 16 tiles of head dim 128 79 / 44 / 28, 188 of them
-// 213 / 185 / 238, 264 of them 106 / 124 / 203; 76 tiles of head dim 64 60 / 42 / 30,
-// 112 of them 28 / 26 / 32, 232 of them 91 / 61 / 74, 564 of them 108 / 122 / 163.
+// us with 1 / 2 / 4 blocks: 16 tiles of head dim 128 65 / 37 / 24, 188 of them
+// 170 / 153 / 200, 264 of them 87 / 105 / 176; 76 tiles of head dim 64 56 / 38 / 28,
+// 112 of them 27 / 24 / 31, 232 of them 83 / 54 / 68, 564 of them 100 / 111 / 151.
 template <int D> int cluster_of(int64_t tiles, int sms) {
     return tiles * 3 <= 2 * sms ? 4 : tiles * 5 <= 7 * Cfg<D>::BLOCKS * sms ? 2 : 1;
 }
