@@ -1051,16 +1051,17 @@ __global__ void __launch_bounds__(128) gqa_combine_kernel(const DecodeArgs a, co
     me.y &= 0xffff;
     if (me.y <= 1) return;                                  // written whole
     // part 0 lies in the first block's "begins" place, the others in the
-    // "continues" places of the blocks behind it; four parts' numbers are
+    // "continues" places of the blocks behind it; eight parts' numbers are
     // requested together and joined like the steps of an online softmax
+    constexpr int BATCH = 8;
     float m = -INFINITY, l = 0.f, o[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) o[v] = 0.f;
-    for (int i0 = 0; i0 < me.y; i0 += 4) {
-        float2 ml[4];
-        float po[4][VEC];
+    for (int i0 = 0; i0 < me.y; i0 += BATCH) {
+        float2 ml[BATCH];
+        float po[BATCH][VEC];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < BATCH; ++k) {
             const int i = min(i0 + k, me.y - 1);
             const int64_t at = (int64_t)(2 * (me.x + i) + (i == 0)) * GT + h;
             ml[k] = parts.ml[at];
@@ -1068,7 +1069,9 @@ __global__ void __launch_bounds__(128) gqa_combine_kernel(const DecodeArgs a, co
             else *(float2*)po[k] = *(const float2*)(parts.o + at * D + lane * VEC);
             if (i0 + k >= me.y) ml[k].x = -INFINITY;
         }
-        const float top = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m);
+        float top = m;
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) top = fmaxf(top, ml[k].x);
         if (top == -INFINITY) continue;                     // parts without a visible key
         const float f = fast_exp2(m - top);
         m = top;
@@ -1076,7 +1079,7 @@ __global__ void __launch_bounds__(128) gqa_combine_kernel(const DecodeArgs a, co
 #pragma unroll
         for (int v = 0; v < VEC; ++v) o[v] *= f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < BATCH; ++k) {
             const float g = fast_exp2(ml[k].x - top);
             l = fmaf(g, ml[k].y, l);
 #pragma unroll
