@@ -459,7 +459,8 @@ DSA_API dsa_status_t gqa_decode_attention(const void* q, int64_t ld_q, dsa_dtype
                                   int rows, int n_heads, int n_kv_heads, int head_dim, float scale, void* out,
                                   float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes gqa_prompt_attention needs for these sizes (0 = none). */
+/* Workspace bytes gqa_prompt_attention needs for these sizes on the current
+ * device (0 = none). */
 DSA_API size_t gqa_prompt_attention_workspace_size(int total, int n_seqs, int n_heads, int head_dim,
                                            dsa_dtype_t dtype);
 
@@ -504,7 +505,8 @@ DSA_API dsa_status_t gqa_prompt_attention(const void* q, int64_t ld_q, const voi
  * list's order, so results are deterministic.  An entry that cannot be served
  * changes nothing and is reported by dsa_get_device_error: DSA_ERR_INVALID_ARG for
  * a sequence, length or page out of range and, except by kv_pages_free, for one
- * listed twice; DSA_ERR_OUT_OF_PAGES for want of free pages.  Calls on one pool must be in order on one stream.
+ * listed twice; DSA_ERR_OUT_OF_PAGES for want of free pages.  Calls on one
+ * pool must be in order on one stream.
  * The functions serve any paged cache of the library, the latent cache of
  * dsa_sparse_mla among them: a cache is a pointer and the bytes of its pages.
  */

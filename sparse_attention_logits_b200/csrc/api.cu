@@ -610,7 +610,10 @@ dsa_status_t gqa_decode_attention(const void* q, int64_t ld_q, dsa_dtype_t dtype
 
 size_t gqa_prompt_attention_workspace_size(int total, int n_seqs, int n_heads, int head_dim, dsa_dtype_t dtype) {
     if (total <= 0 || n_seqs <= 0 || n_heads <= 0 || !kv_head_dim(head_dim)) return 0;
-    return dsa::gqa_prompt_workspace_bytes(total, n_seqs, dtype);
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        sms = 1024;  // no device: size for a large GPU
+    return dsa::gqa_prompt_workspace_bytes(total, n_seqs, n_heads, head_dim, dtype, sms);
 }
 
 dsa_status_t gqa_prompt_attention(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
@@ -635,7 +638,7 @@ dsa_status_t gqa_prompt_attention(const void* q, int64_t ld_q, const void* k, in
     if (tiles * n_heads > ((int64_t)1 << 31) - 2) return fail(DSA_ERR_UNSUPPORTED, "%s: too many rows and heads", name);
     dsa::Launch L;
     if ((st = make_launch(stream, &L)) != DSA_OK) return st;
-    const size_t need = dsa::gqa_prompt_workspace_bytes(total, n_seqs, dtype);
+    const size_t need = dsa::gqa_prompt_workspace_bytes(total, n_seqs, n_heads, head_dim, dtype, L.num_sms);
     if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
         return fail(DSA_ERR_INVALID_ARG, "%s: a 256-byte aligned workspace of %zu bytes is needed", name, need);
     dsa::PromptArgs a;

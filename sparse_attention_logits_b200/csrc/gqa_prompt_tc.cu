@@ -30,6 +30,10 @@
 // memory; 9: TMA loads; 10: zeroes the rows of a last V tile that lie behind
 // the prompt (they belong to other prompts, and 0 times their infinities
 // would not be 0).  Items are taken longest first.
+//
+// Few heads and long prompts (a model's heads dealt to several GPUs) leave fewer
+// items than the longest one's time lets hide: there the keys of an item are cut
+// into up to four parts, whose unnormalised fp32 sums a second kernel joins.
 #include "common.cuh"
 #include "gqa_prompt.cuh"
 #include "launchers.h"
@@ -50,6 +54,7 @@ constexpr int REGS_SOFTMAX = 216, REGS_REST = 72;
 static_assert(256 * REGS_SOFTMAX + 128 * REGS_REST <= 168 * THREADS, "register split exceeds launch");
 constexpr int TMEM_COLS = 512;
 constexpr float RESCALE_LOG2 = 8.f;
+constexpr int MAX_CHUNKS = 4;       // parts of an item's keys
 // Of 16 exponentials, how many run on the multiply-add pipe, and how many of
 // a tile's four 32-key pieces of P are announced together first.  Cycles per
 // 128 keys of both tiles: 0 -> 3440, 2 -> 3280, 3 -> 3256, 4 -> 3370 (three
@@ -82,26 +87,41 @@ struct Sched {                      // where the items come from
     int pairs;                      // items per row block: head pairs (even groups) or heads
     int rows_per_block;             // 128 (even groups) or 256
     bool two_heads;
+    // split items: key tiles of one, their largest number, and what they leave:
+    // [part, row, head] sums of p v and (maximum in base 2, sum of p)
+    int chunk, chunks;
+    float* part_o;
+    float2* part_ml;
 };
 
 // One warp's view of the items, longest first.
-struct Items {
+template <bool SPLIT> struct Items {
     PromptLanes lanes;              // without a list
     int entries;
 
+    // row blocks that reach into part c of their keys
+    __device__ __forceinline__ int reaching(const Sched& s, int c) const {
+        return lanes.at_least(c * (s.chunk * BN / s.rows_per_block) + 1);
+    }
     __device__ __forceinline__ void init(const PromptArgs& a, const Sched& s) {
-        if (s.list) {
+        if (!SPLIT && s.list) {
             entries = *s.count;
         } else {
             lanes.init(a, s.rows_per_block);
             entries = lanes.at_least(1);
+            if (SPLIT)
+                for (int c = 1; c < s.chunks; ++c) entries += reaching(s, c);
         }
     }
-    // Entry e: blocks in falling order of their number (their work); false past the end.
-    __device__ __forceinline__ bool get(const PromptArgs& a, const Sched& s, int e, int& first, int& n, int& row0) const {
+    // Entry e: blocks in falling order of their number (their work), part by
+    // part of their keys; false past the end.
+    __device__ __forceinline__ bool get(const PromptArgs& a, const Sched& s, int e, int& first, int& n, int& row0, int& part) const {
         if (e >= entries) return false;
         int block;
-        if (s.list) {
+        part = 0;
+        if (SPLIT)
+            for (int left = reaching(s, 0); e >= left; left = reaching(s, ++part)) e -= left;
+        if (!SPLIT && s.list) {
             const Entry x = s.list[e];
             first = a.cu_seqlens[x.seq];
             n = a.cu_seqlens[x.seq + 1] - first;
@@ -118,22 +138,32 @@ struct Item {
     int first, len;                 // the prompt's first packed row, and its length
     int head[2], row0[2], n[2];     // per tile: query head, first row in the prompt, key tiles (0: no tile)
     int kvh, n_max;
+    int part, tile0;                // split items: number, first key tile
+    bool diagonal[2], whole[2];     // split items: whether the last tile is the diagonal one; whether this is all
 };
 
 // The block's r-th item; odd rounds run backwards over the blocks, so that
 // neither end of the grid collects the longer ones.
-__device__ __forceinline__ bool get_item(const PromptArgs& a, const Sched& s, const Items& items, int round, Item& w) {
+template <bool SPLIT>
+__device__ __forceinline__ bool get_item(const PromptArgs& a, const Sched& s, const Items<SPLIT>& items, int round, Item& w) {
     const int g = gridDim.x, b = blockIdx.x;
     const int64_t i = (int64_t)round * g + ((round & 1) ? g - 1 - b : b);
     const int64_t e = i / s.pairs;
     const int p = (int)(i - e * s.pairs);
     int row0;
-    if (e > 0x7fffffff || !items.get(a, s, (int)e, w.first, w.len, row0)) return false;
+    if (e > 0x7fffffff || !items.get(a, s, (int)e, w.first, w.len, row0, w.part)) return false;
+    w.tile0 = SPLIT ? w.part * s.chunk : 0;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         w.head[t] = s.two_heads ? 2 * p + t : p;
         w.row0[t] = s.two_heads ? row0 : row0 + t * BM;
         w.n[t] = w.row0[t] < w.len ? w.row0[t] / BN + 1 : 0;
+        w.diagonal[t] = w.whole[t] = true;
+        if (SPLIT) {
+            w.whole[t] = w.n[t] <= s.chunk;
+            w.diagonal[t] = w.n[t] - w.tile0 <= s.chunk;
+            w.n[t] = max(0, min(w.n[t] - w.tile0, s.chunk));
+        }
     }
     w.kvh = w.head[0] / (a.n_heads / a.n_kv_heads);
     w.n_max = max(w.n[0], w.n[1]);
@@ -238,7 +268,7 @@ __global__ void __launch_bounds__(1024) gqa_prompt_list_kernel(const PromptArgs 
     }
 }
 
-template <int D>
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1) gqa_prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                                                                    const __grid_constant__ CUtensorMap k_map,
                                                                    const __grid_constant__ CUtensorMap v_map,
@@ -284,7 +314,7 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prompt_tc_kernel(const __grid_
     const uint32_t tmem = bars->tmem;
     pdl_wait();
     pdl_launch_dependents();
-    Items items;
+    Items<SPLIT> items;
     Item w;
     items.init(a, sched);
 
@@ -312,7 +342,7 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prompt_tc_kernel(const __grid_
                 tmem_ld_wait();
                 tmem_ld32(s_col + 64, s[2]);                        // (these arrive under the first half's weights)
                 tmem_ld32(s_col + 96, s[3]);
-                if (j == n - 1) {                                   // the diagonal tile: keys up to the row's own
+                if (j == n - 1 && (!SPLIT || w.diagonal[t])) {      // the diagonal tile: keys up to the row's own
                     tmem_ld_wait();
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
@@ -407,6 +437,32 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prompt_tc_kernel(const __grid_
             const int64_t row0 = (int64_t)w.first + w.row0[t] + (warp & 3) * 32;
             const float inv = l == 0.f ? 0.f : 1.f / l;
             uint8_t* stage = obuf + warp * OUT_STAGE;
+            if (SPLIT && !w.whole[t]) {
+                // a part of the keys: the sums as they are, in fp32, 32 dims at a time
+                const int64_t part_row = (int64_t)w.part * a.total + row0;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float v[32];
+                    tmem_ld32(o_col + c * 32, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        st_shared_v4(stage + lane * 128 + ((e ^ (lane & 7)) << 4), __float_as_uint(v[4 * e]),
+                                     __float_as_uint(v[4 * e + 1]), __float_as_uint(v[4 * e + 2]), __float_as_uint(v[4 * e + 3]));
+                    __syncwarp();
+                    float* out = sched.part_o + (part_row * a.n_heads + w.head[t]) * D + c * 32 + (lane & 7) * 4;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int k = i * 4 + (lane >> 3);
+                        const uint4 x = ld_shared_v4(stage + k * 128 + (((lane & 7) ^ (k & 7)) << 4));
+                        if (k < rows) *(uint4*)(out + (int64_t)k * a.n_heads * D) = x;
+                    }
+                    __syncwarp();
+                }
+                if (lane < rows) sched.part_ml[(part_row + lane) * a.n_heads + w.head[t]] = make_float2(m, l);
+                tc_fence_before();
+                continue;
+            }
 #pragma unroll 1
             for (int c = 0; c < D / 64; ++c) {
 #pragma unroll
@@ -473,7 +529,7 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prompt_tc_kernel(const __grid_
                     for (int j = 0; j < w.n_max && ok; ++j) {
                         const uint32_t vslot = slot + 2 * j + 1, kslot = vslot + 1;
                         ok = wait_kv(vslot);
-                        if (ok && (j + 1) * BN > w.len) {
+                        if (ok && (w.tile0 + j + 1) * BN > w.len) {
                             mbar_arrive(&bars->to_zero);        // the tile has landed
                             ok = mbar_wait(&bars->zeroed, n_z & 1, a.err, DEV_ERR_TIMEOUT_PEER, abort_flag);
                             ++n_z;
@@ -545,7 +601,7 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prompt_tc_kernel(const __grid_
                         ++q_loads;
                     }
                     for (int j = 0; j < w.n_max && ok; ++j)
-                        ok = load(&k_map, w.kvh * D, w.first + j * BN) && load(&v_map, w.kvh * D, w.first + j * BN);
+                        ok = load(&k_map, w.kvh * D, w.first + (w.tile0 + j) * BN) && load(&v_map, w.kvh * D, w.first + (w.tile0 + j) * BN);
                 }
                 ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, __ffs(__ballot_sync(0xffffffffu, leader)) - 1) != 0;
                 if (!ok) break;
@@ -560,7 +616,7 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prompt_tc_kernel(const __grid_
             // ----------------------------- rows of V behind a prompt's end ----
             uint32_t slot = 0, n_z = 0;
             for (int round = 0; get_item(a, sched, items, round, w); ++round) {
-                const int left = w.len - (w.n_max - 1) * BN;            // rows of the last key tile
+                const int left = w.len - (w.tile0 + w.n_max - 1) * BN;  // rows of the last key tile
                 if (left < BN) {
                     const uint32_t i = slot + 2 * (w.n_max - 1) + 1;
                     const bool ok = __all_sync(0xffffffffu, mbar_wait(&bars->to_zero, n_z & 1, a.err, DEV_ERR_TIMEOUT_PEER,
@@ -587,9 +643,79 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prompt_tc_kernel(const __grid_
     }
 }
 
+// The parts of split items joined: a warp per (row, head).
+template <int D>
+__global__ void __launch_bounds__(128) gqa_prompt_join_kernel(const PromptArgs a, const Sched s) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t item = blockIdx.x * 4ll + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (item >= (int64_t)a.total * a.n_heads) return;
+    const int row = (int)(item / a.n_heads);
+    int start = 0, len = 0;
+    if (lane < a.n_seqs) prompt_bounds(a, lane, start, len);
+    const unsigned mine = __ballot_sync(0xffffffffu, row >= start && row - start < len);
+    if (!mine) return;                                      // outside every prompt
+    const int tiles = (row - __shfl_sync(0xffffffffu, start, __ffs(mine) - 1)) / BN + 1;
+    if (tiles <= s.chunk) return;                           // written whole
+    const int parts = (tiles - 1) / s.chunk + 1;
+    float2 ml[MAX_CHUNKS], o[MAX_CHUNKS][D / 64];
+#pragma unroll
+    for (int c = 0; c < MAX_CHUNKS; ++c) {
+        const int64_t at = (int64_t)min(c, parts - 1) * a.total * a.n_heads + item;
+        ml[c] = s.part_ml[at];
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) o[c][k] = *(const float2*)(s.part_o + at * D + k * 64 + 2 * lane);
+        if (c >= parts) ml[c] = make_float2(-INFINITY, 0.f);
+    }
+    float top = ml[0].x, l = 0.f;
+#pragma unroll
+    for (int c = 1; c < MAX_CHUNKS; ++c) top = fmaxf(top, ml[c].x);
+    const float base = top > -INFINITY ? top : 0.f;
+    float2 sum[D / 64] = {};
+#pragma unroll
+    for (int c = 0; c < MAX_CHUNKS; ++c) {
+        if (c >= parts) break;
+        const float f = fast_exp2(ml[c].x - base);
+        l = fmaf(f, ml[c].y, l);
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) sum[k] = fma2(make_float2(f, f), o[c][k], sum[k]);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k)
+        *(uint32_t*)((__nv_bfloat16*)a.out + item * D + k * 64 + 2 * lane) = bf16x2_bits(sum[k].x * inv, sum[k].y * inv);
+    if (lane == 0) a.lse[item] = l == 0.f ? -INFINITY : (top + log2f(l)) * LN2;
+}
+
 namespace {
 
 int max_entries(int total, int n_seqs) { return total / BM + (n_seqs < total ? n_seqs : total); }
+
+// Key tiles of a split item, or 0: items stay whole.  `pairs` items share a
+// block of rows.  A block's time is its longest item, so items are cut where
+// the longest (taking prompts to differ by up to twice their average) is well
+// above a block's share of all work; cutting costs the parts' way through
+// memory and a second kernel, which three tiles saved must pay for.  One prompt,
+// heads of 128, whole / cut: 8192 tokens, 4 heads 115 / 87 us, 1 head 110 / 41;
+// 4096 tokens, 4 heads 60 / 44, 8 heads 62 / 60; 2048 tokens, 4 heads 33 / 21.
+int chunk_of(int total, int n_seqs, int pairs, int rows_per_block, int sms) {
+    if (n_seqs > LANE_SEQS) return 0;
+    const int64_t longest = total < 2 * ((int64_t)total / n_seqs + 1) ? total : 2 * ((int64_t)total / n_seqs + 1);
+    const int64_t tiles = (longest + BN - 1) / BN, blocks = ((int64_t)total + rows_per_block - 1) / rows_per_block;
+    const int64_t share = pairs * blocks * tiles / (2 * sms);
+    const int64_t all = ((int64_t)total + BN - 1) / BN;
+    int64_t chunk = share * 7 / 10 > 4 ? share * 7 / 10 : 4;        // (less than a share: blocks take unequal numbers of items)
+    if (chunk * MAX_CHUNKS < all) chunk = (all + MAX_CHUNKS - 1) / MAX_CHUNKS;
+    chunk += chunk & 1;
+    return tiles >= chunk + 3 && 2 * tiles > 3 * share ? (int)chunk : 0;
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+size_t parts_bytes(int total, int n_heads, int head_dim) {
+    const size_t rows = (size_t)MAX_CHUNKS * total * n_heads;
+    return up256(rows * 8) + rows * head_dim * 4;
+}
 
 template <int D>
 cudaError_t launch(const Launch& L, const PromptArgs& a, void* workspace) {
@@ -607,8 +733,13 @@ cudaError_t launch(const Launch& L, const PromptArgs& a, void* workspace) {
     s.rows_per_block = s.two_heads ? BM : 2 * BM;
     s.list = nullptr;
     s.count = nullptr;
-    static std::atomic<int> done[kMaxDevices];
-    cudaError_t e = allow_smem(done, gqa_prompt_tc_kernel<D>, C::SMEM);
+    s.chunk = chunk_of(a.total, a.n_seqs, s.pairs, s.rows_per_block, L.num_sms);
+    s.chunks = s.chunk ? ceil_div(ceil_div(a.total, BN), s.chunk) : 1;
+    s.part_ml = (float2*)workspace;
+    s.part_o = (float*)((char*)workspace + up256((size_t)MAX_CHUNKS * a.total * a.n_heads * 8));
+    static std::atomic<int> done[2][kMaxDevices];
+    const auto kern = s.chunk ? gqa_prompt_tc_kernel<D, true> : gqa_prompt_tc_kernel<D, false>;
+    cudaError_t e = allow_smem(done[s.chunk != 0], kern, C::SMEM);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1] = {pdl_attr()};
@@ -625,20 +756,30 @@ cudaError_t launch(const Launch& L, const PromptArgs& a, void* workspace) {
         count_launch();
         if (e != cudaSuccess) return e;
     }
-    const int64_t items = (int64_t)most * s.pairs;
+    const int64_t items = (int64_t)most * s.pairs * s.chunks;
     cfg.gridDim = dim3((unsigned)(items < L.num_sms ? items : L.num_sms));
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
-    e = cudaLaunchKernelEx(&cfg, gqa_prompt_tc_kernel<D>, q_map, k_map, v_map, a, s);
+    e = cudaLaunchKernelEx(&cfg, kern, q_map, k_map, v_map, a, s);
+    count_launch();
+    if (e != cudaSuccess || !s.chunk) return e;
+    cfg.gridDim = dim3((unsigned)(((int64_t)a.total * a.n_heads + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, gqa_prompt_join_kernel<D>, a, s);
     count_launch();
     return e;
 }
 
 }  // namespace
 
-size_t gqa_prompt_workspace_bytes(int total, int n_seqs, dsa_dtype_t dtype) {
-    if (dtype != DSA_BF16 || n_seqs <= LANE_SEQS) return 0;
-    return 256 + (size_t)max_entries(total, n_seqs) * sizeof(Entry);
+// (The number of kv heads is not asked for: enough for either kind of item.)
+size_t gqa_prompt_workspace_bytes(int total, int n_seqs, int n_heads, int head_dim, dsa_dtype_t dtype, int sms) {
+    if (dtype != DSA_BF16) return 0;
+    if (n_seqs > LANE_SEQS) return 256 + (size_t)max_entries(total, n_seqs) * sizeof(Entry);
+    return chunk_of(total, n_seqs, n_heads / 2, BM, sms) || chunk_of(total, n_seqs, n_heads, 2 * BM, sms)
+               ? parts_bytes(total, n_heads, head_dim)
+               : 0;
 }
 
 cudaError_t launch_gqa_prompt_tc(const Launch& L, const PromptArgs& a, int head_dim, void* workspace) {

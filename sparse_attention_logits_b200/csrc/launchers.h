@@ -185,7 +185,7 @@ struct PromptArgs {
     float* lse;                 // [total, n_heads]
     unsigned* err;
 };
-size_t gqa_prompt_workspace_bytes(int total, int n_seqs, dsa_dtype_t dtype);
+size_t gqa_prompt_workspace_bytes(int total, int n_seqs, int n_heads, int head_dim, dsa_dtype_t dtype, int num_sms);
 cudaError_t launch_gqa_prompt_f32(const Launch& L, const PromptArgs& a, int head_dim);                     // fp32
 cudaError_t launch_gqa_prompt_tc(const Launch& L, const PromptArgs& a, int head_dim, void* workspace);      // bf16
 }  // namespace dsa

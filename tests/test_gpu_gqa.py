@@ -44,6 +44,11 @@ PROMPTS = {
     "one_long": ([2049], 0, 0, 4, 1, 128, "bf16"),
     "long_and_short": ([1500, 3, 900, 1, 1, 1], 0, 0, 4, 2, 64, "bf16"),
     "many_short": ([(7 * i) % 23 for i in range(150)], 0, 0, 2, 2, 128, "bf16"),
+    # few heads and long prompts: a row's keys in parts
+    "parts": ([1500], 3, 9, 4, 1, 128, "bf16"),
+    "parts_odd_group": ([1400, 300], 0, 0, 3, 1, 128, "bf16"),
+    "parts_edges": ([768, 769, 513, 0, 1537], 2, 0, 2, 1, 64, "bf16"),
+    "parts_one_head": ([130, 2600], 0, 1, 1, 1, 64, "bf16"),
     "fp32": ([1, 63, 64, 65, 0, 300], 2, 3, 6, 2, 64, "fp32"),
     "fp32_d128": ([200, 31], 0, 0, 4, 4, 128, "fp32"),
     "fp32_some_tiles": ([31, 900, 400], 1, 0, 8, 4, 64, "fp32"),
@@ -104,6 +109,27 @@ def test_prompt_large_and_peaked_scores(cuda_device, dtype):
     q[::3] *= -3
     out, lse = dsa.gqa_prompt_attention(q, k, v, torch.tensor([0, n], dtype=torch.int32, device="cuda"), 0.3)
     _prompt_check(out, lse, q, k, v, [0, n], 0.3, 0, n)
+
+
+@pytest.mark.parametrize("group", [1, 2])
+def test_prompt_parts_of_peaked_scores(cuda_device, group):
+    """Rows whose keys are taken in parts: maxima that rise and fall from part to part, a prompt
+    beside rows of NaN, the caller's workspace full of NaN."""
+    g = _gen(8)
+    n, D, cu = 1700, 128, [70, 1770]
+    q, k, v = (_randn((n + 80, h, D), g, torch.bfloat16) for h in (2 * group, 2, 2))
+    k[70:1770] *= (3.2 + 3 * torch.sin(torch.arange(n, device="cuda") / 150))[:, None, None].to(torch.bfloat16)
+    for x in (q, k, v):
+        x[:70] = NAN
+        x[1770:] = math.inf
+    need = dsa.gqa_prompt_attention_workspace_size(n + 80, 1, 2 * group, D, torch.bfloat16)
+    assert need > 0
+    ws = torch.full((need // 4,), NAN, device="cuda")
+    out, lse = dsa.gqa_prompt_attention(q, k, v, _i32(cu), 0.3, workspace=ws.view(torch.uint8))
+    assert dsa.get_device_error(cuda_device) == dsa.DSA_OK
+    _prompt_check(out, lse, q, k, v, cu, 0.3, *cu)
+    again = dsa.gqa_prompt_attention(q, k, v, _i32(cu), 0.3)
+    assert torch.equal(out[70:1770], again[0][70:1770]) and torch.equal(lse[70:1770], again[1][70:1770])
 
 
 @pytest.mark.parametrize("dtype,D,H,Hkv", [("bf16", 128, 4, 2), ("bf16", 64, 3, 1), ("fp32", 64, 2, 2)])
