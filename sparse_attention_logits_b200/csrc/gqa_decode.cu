@@ -5,14 +5,14 @@
 // so the cache's bytes at the HBM rate are the floor.  32 sequences of up to
 // 32K tokens, 8 / 32 heads of 128, bf16: 514 us, 6.36 TB/s (a plain copy runs at
 // 6.5); 64 of them, 8 / 64 heads, fp8: 570 us, 5.9 TB/s.  One row of 777 tokens
-// takes 7.7 us, a chain of latencies: rows, pages, cache, joining of the parts.
+// takes 7.2 us, a chain of latencies: rows, pages, cache, joining of the parts.
 //
 // Rows of one sequence that stand beside each other (several tokens verified
 // at once) share its reads too: a bunch is up to `merge` such rows, whose heads
 // fill the 16 columns of the products together; past a row's last key its
 // columns are masked.  Against a pair for every row: 8 sequences of up to 16K
-// tokens, 4 rows each, 8 / 32 heads: 272 -> 82 us in bf16, 122 -> 69 in fp8; one
-// sequence of 777 tokens 9.5 -> 10.8 us.
+// tokens, 4 rows each, 8 / 32 heads: 264 -> 82 us in bf16, 126 -> 68 in fp8; 16
+// of up to 100 tokens 13.9 -> 10.7; one of 777 tokens 9.9 -> 10.3 us.
 //
 // Work split.  A pair is (bunch of rows, kv head, tile of the group's heads); its keys
 // are cut into units of KT (128, in fp32 64).  All pairs' units form
