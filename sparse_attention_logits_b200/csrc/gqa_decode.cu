@@ -1,8 +1,8 @@
 // Grouped-query attention of single query rows over a paged key-value cache:
 //   z_s    = scale * q[t,h,:] . k_s          s <= row_pos[t], kv head h / group
 //   out    = sum_s softmax_s(z) v_s,   lse = log sum_s exp(z_s)
-// Every visible key and value row is read once for all heads of its group,
-// so the cache's bytes at the HBM rate are the floor.  32 sequences of up to
+// Every visible key and value row is read once for all heads of its group (for
+// each 16 of them, in larger groups), so the cache's bytes at the HBM rate are the floor.  32 sequences of up to
 // 32K tokens, 8 / 32 heads of 128, bf16: 514 us, 6.36 TB/s (a plain copy runs at
 // 6.5); 64 of them, 8 / 64 heads, fp8: 570 us, 5.9 TB/s.  One row of 777 tokens
 // takes 7.2 us, a chain of latencies: rows, pages, cache, joining of the parts.
@@ -16,8 +16,8 @@
 //
 // Work split.  A pair is (bunch of rows, kv head, tile of the group's heads); its keys
 // are cut into units of KT (128, in fp32 64).  All pairs' units form
-// one line, and block i of the grid takes the i-th equal stretch of it, whatever the rows' lengths:
-// ragged batches load every SM alike, and one long row uses the whole GPU.
+// one line, and block i of the grid takes the i-th equal stretch of it,
+// whatever the rows' lengths: ragged batches load every SM alike, and one long row uses the whole GPU.
 // Lengths are read on the device (nothing about them is known to the host),
 // so a captured call serves growing sequences.  A stretch that holds a whole
 // pair writes its output; a pair cut between blocks leaves fp32 partials
@@ -138,7 +138,8 @@ struct LocateShared {
 // whole block takes part.  `per_block` units at least, so that short lines
 // are not cut finer than is worth joining.
 template <int KT, bool MANY>
-__device__ __forceinline__ void locate(const DecodeArgs& a, int tiles, int per_block, LocateShared& sh, RowsShared& held, Walk<KT, MANY>& w,
+__device__ __forceinline__ void locate(const DecodeArgs& a, int tiles, int per_block, LocateShared& sh,
+                                       RowsShared& held, Walk<KT, MANY>& w,
                                        int64_t& begin, int64_t& end, int64_t& stretch) {
     const int hvs = a.n_kv_heads * tiles;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -539,7 +540,9 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D, GT>::BLOCKS)) gqa_deco
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int x = 8 * g + 2 * c4 + e;
-                sees[g][e] = bunch ? (x < heads ? keys_of(a, row_at(a, held, w.row + a.by_group.div(x)).x, w.batch) : w.least) : w.keys;
+                sees[g][e] = !bunch      ? w.keys
+                             : x < heads ? keys_of(a, row_at(a, held, w.row + a.by_group.div(x)).x, w.batch)
+                                         : w.least;
             }
         // O^T: tile t, rows (dims) r4 and r4 + 8, columns (heads) 8 g + 2 c4 + {0, 1}
         float o[KS][NG][4];
@@ -740,7 +743,8 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D, GT>::BLOCKS)) gqa_deco
                                     if (!MANY || !partly || key0 + 8 * t + r4 < sees[g][e]) top = fmaxf(top, fabsf(vs[t]));
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                                top = fmaxf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)), 1e-30f);   // its reciprocal is finite
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                                top = fmaxf(top, 1e-30f);               // its reciprocal is finite
                                 all_top = top;
                             }
                             if (top > vref[g][e]) {
@@ -999,7 +1003,8 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D, GT>::BLOCKS)) gqa_deco
                 if (begins && ends) {
                     const float inv = ll == 0.f ? 0.f : 1.f / ll;
                     const int hr = bunch ? a.by_group.div(h) : 0;
-                    const int64_t to_head = (int64_t)(w.row + hr) * a.n_heads + h0 + h - hr * group, to = to_head * D + lane * VEC;
+                    const int64_t to_head = (int64_t)(w.row + hr) * a.n_heads + h0 + h - hr * group;
+                    const int64_t to = to_head * D + lane * VEC;
 #pragma unroll
                     for (int v = 0; v < VEC; v += 2) {
                         if (FP32) *(float2*)((float*)a.out + to + v) = make_float2(acc[v] * inv, acc[v + 1] * inv);

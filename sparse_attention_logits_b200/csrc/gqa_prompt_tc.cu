@@ -115,7 +115,8 @@ template <bool SPLIT> struct Items {
     }
     // Entry e: blocks in falling order of their number (their work), part by
     // part of their keys; false past the end.
-    __device__ __forceinline__ bool get(const PromptArgs& a, const Sched& s, int e, int& first, int& n, int& row0, int& part) const {
+    __device__ __forceinline__ bool get(const PromptArgs& a, const Sched& s, int e, int& first, int& n, int& row0,
+                                        int& part) const {
         if (e >= entries) return false;
         int block;
         part = 0;
@@ -601,7 +602,8 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prompt_tc_kernel(const __grid_
                         ++q_loads;
                     }
                     for (int j = 0; j < w.n_max && ok; ++j)
-                        ok = load(&k_map, w.kvh * D, w.first + (w.tile0 + j) * BN) && load(&v_map, w.kvh * D, w.first + (w.tile0 + j) * BN);
+                        ok = load(&k_map, w.kvh * D, w.first + (w.tile0 + j) * BN) &&
+                             load(&v_map, w.kvh * D, w.first + (w.tile0 + j) * BN);
                 }
                 ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, __ffs(__ballot_sync(0xffffffffu, leader)) - 1) != 0;
                 if (!ok) break;

@@ -382,6 +382,55 @@ def test_decode_rows_never_see_later_tokens(cuda_device, kind, n):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "fp32"])
+def test_decode_bad_rows_that_share_a_sequence(cuda_device, kind):
+    """Rows of sequences out of range beside each other, and a page out of range that only the later rows reach."""
+    c = Paged([300, 100], 2, 64, 16, kind, 27)
+    table = c.table.clone()
+    table[0, 18] = 10 ** 6                                  # tokens 288 .. 299
+    batch, pos = [0, 0, 0, 9, 9, 9, 1, 1, 1, -1, -1], [285, 287, 299, 1, 2, 3, 97, 98, 99, 5, 6]
+    q = _randn((len(pos), 6, 64), _gen(28), torch.float32 if kind == "fp32" else torch.bfloat16)
+    out, lse = dsa.gqa_decode_attention(q, c.k, c.v, table, _i32(batch), _i32(pos), 0.15, c.k_scale, c.v_scale)
+    with pytest.raises(dsa.DSAError) as e:
+        dsa.get_device_error(cuda_device)
+    assert e.value.status == dsa.DSA_ERR_INVALID_ARG
+    _decode_check(c, q, out, lse, [max(b, 0) if b < 2 else 0 for b in batch],
+                  [p if b in (0, 1) else -1 for b, p in zip(batch, [285, 287, 287, *pos[3:]])], 0.15)
+    assert dsa.get_device_error(cuda_device) == dsa.DSA_OK
+
+
+def test_captured_rows_and_prompts_change_between_replays(cuda_device):
+    """One captured graph of a decode of several rows a sequence and of prompts in parts; the rows'
+    sequences and lengths, and the prompts' bounds, are others at each replay."""
+    c = Paged([700, 260, 90], 1, 64, 16, "bf16", 29)
+    n = 1300
+    q, x = _randn((8, 4, 64), _gen(30), torch.bfloat16), _randn((n, 6, 64), _gen(31), torch.bfloat16)
+    batch, pos, cu = _i32([0] * 8), _i32([-1] * 8), _i32([0, n])
+    pq, pk, pv = x[:, :4], x[:, 4:5], x[:, 5:]
+
+    def step():
+        return (dsa.gqa_decode_attention(q, c.k, c.v, c.table, batch, pos, 0.15),
+                dsa.gqa_prompt_attention(pq, pk, pv, cu, 0.15))
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        (out, lse), (pout, plse) = step()
+    for b, p, first in (([0] * 4 + [1] * 4, [696, 697, 698, 699, 40, 41, 42, 43], 0),
+                        ([2, 2, 0, 1, 1, 1, 1, 0], [89, -1, 650, 256, 257, 258, 259, 0], 511),
+                        ([1, 0, 1, 0, 2, 2, 2, 2], [5, 6, 7, 8, 80, 85, 60, 89], 1290)):
+        batch.copy_(_i32(b))
+        pos.copy_(_i32(p))
+        cu.copy_(_i32([first, n]))
+        graph.replay()
+        torch.cuda.synchronize()
+        _decode_check(c, q, out, lse, b, p, 0.15)
+        _prompt_check(pout, plse, pq, pk, pv, [first, n], 0.15, first, n)
+    assert dsa.get_device_error(cuda_device) == dsa.DSA_OK
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp32"])
 def test_decode_large_scores(cuda_device, kind):
     """Scores of a few hundred that grow along the sequence: every slice moves the maximum."""
     c = Paged([3000], 1, 128, 64, kind, 31)
