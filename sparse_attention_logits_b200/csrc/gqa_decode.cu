@@ -270,17 +270,27 @@ __device__ __forceinline__ int cache_row(const DecodeArgs& a, Place p) {
 // output is summed from zero and added to the running one in fp32.
 // WK: keys of a warp's slice; BLOCKS per SM, with STAGES slices in flight per
 // warp; Q_BYTES: the query fragments, where the registers have no room for them.
+//
+// More blocks of one slice a warp hide each other's products and joining better
+// than fewer blocks of several slices, as far as registers allow (us, fewer blocks
+// or more slices -> as here; 8 kv heads, 4 heads each, or as said):
+//   bf16, 128: 128 sequences of up to 500 54.6 -> 43.4, 32 of up to 32K 511.6 -> 510.3,
+//              one of 32K 31.4 -> 32.6;  64: 128 of up to 500 28.7 -> 25.7
+//   fp8, 128:  64 of up to 32K, 8 heads each, 579 -> 532;  64: two slices and four
+//              blocks, 32 of up to 16K 80.7 -> 78.3, with one slice 82.2; 16 heads a
+//              pair: two slices, 32 of up to 16K 222 -> 202 (128), and with three blocks,
+//              whose registers spill, 332
+//   fp32, 128: 16 of up to 8K 179 -> 144 (6.0 TB/s);  64: two slices 68.3, one 77.1, three 68.8
 template <typename KV, int D, int GT> struct MmaCfg;
 template <int D, int GT> struct MmaCfg<__nv_bfloat16, D, GT> {
-    static constexpr int WK = 32, STAGES = 2, BLOCKS = D == 64 ? 2 : 1, Q_BYTES = 0;
+    static constexpr int WK = 32, STAGES = 1, BLOCKS = D == 64 ? 3 : 2, Q_BYTES = 0;
 };
-// 16 heads of 128: 32 sequences of up to 16K, 8 / 128 heads, take 202 us with two
-// blocks and 332 us with three, whose registers spill.
 template <int D, int GT> struct MmaCfg<__nv_fp8_e4m3, D, GT> {
-    static constexpr int WK = 32, STAGES = 2, BLOCKS = D == 64 || GT == 8 ? 3 : 2, Q_BYTES = GT == 16 ? D / 16 * 512 : 0;
+    static constexpr int WK = 32, STAGES = D == 128 && GT == 8 ? 1 : 2, BLOCKS = (D == 64 ? 4 : 3) - (GT == 16 ? 1 : 0);
+    static constexpr int Q_BYTES = GT == 16 ? D / 16 * 512 : 0;
 };
 template <int D, int GT> struct MmaCfg<float, D, GT> {
-    static constexpr int WK = 16, STAGES = D == 64 ? 3 : 2, BLOCKS = D == 64 ? 2 : 1, Q_BYTES = GT == 16 ? D / 8 * 1024 : 0;
+    static constexpr int WK = 16, STAGES = D == 64 ? 2 : 1, BLOCKS = 2, Q_BYTES = GT == 16 ? D / 8 * 1024 : 0;
 };
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
