@@ -3,16 +3,17 @@
 //   out    = sum_s softmax_s(z) v_s,   lse = log sum_s exp(z_s)
 // Every visible key and value row is read once for all heads of its group (for
 // each 16 of them, in larger groups), so the cache's bytes at the HBM rate are the floor.  32 sequences of up to
-// 32K tokens, 8 / 32 heads of 128, bf16: 514 us, 6.36 TB/s (a plain copy runs at
-// 6.5); 64 of them, 8 / 64 heads, fp8: 570 us, 5.9 TB/s.  One row of 777 tokens
+// 32K tokens, 8 / 32 heads of 128, bf16: 512 us, 6.4 TB/s (a plain copy runs at
+// 6.5); 64 of them, 8 / 64 heads, fp8: 523 us, 6.4 TB/s.  One row of 777 tokens
 // takes 7.2 us, a chain of latencies: rows, pages, cache, joining of the parts.
 //
 // Rows of one sequence that stand beside each other (several tokens verified
 // at once) share its reads too: a bunch is up to `merge` such rows, whose heads
 // fill the 16 columns of the products together; past a row's last key its
 // columns are masked.  Against a pair for every row: 8 sequences of up to 16K
-// tokens, 4 rows each, 8 / 32 heads: 264 -> 82 us in bf16, 126 -> 68 in fp8; 16
-// of up to 100 tokens 13.9 -> 10.7; one of 777 tokens 9.9 -> 10.3 us.
+// tokens, 4 rows each, 8 / 32 heads: 258 -> 80 us in bf16, 124 -> 68 in fp8; 4
+// of up to 5K in fp32 90 -> 50; 16 of up to 100 tokens 10.3 -> 11.3; one of 777
+// tokens 9.3 -> 10.8 us.
 //
 // Work split.  A pair is (bunch of rows, kv head, tile of the group's heads); its keys
 // are cut into units of KT (128, in fp32 64).  All pairs' units form
@@ -399,7 +400,7 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D, GT>::BLOCKS)) gqa_deco
     constexpr bool Q_SHARED = MANY && ES != 2;      // query fragments in shared memory, for want of registers
     constexpr int VG = MANY ? NG : 1, VE = MANY ? 2 : 1;    // references of the value scales: per head, or one
     static_assert(!FP8 || WK == 32, "a lane per key's scales");
-    static_assert(2 * SLICE >= 8 * D * 4, "the outputs of 8 heads are exchanged in a slot");
+    static_assert(2 * SLICE >= GT * D * 4, "the outputs of a pair's heads are exchanged in a slot");
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ LocateShared sh;
     __shared__ RowsShared held;             // (MANY only)
@@ -976,61 +977,59 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D, GT>::BLOCKS)) gqa_deco
         const int place = 2 * blockIdx.x + (begins ? 1 : 0);
         float* mine = (float*)(ring + st * SLOT);
 #pragma unroll
-        for (int half = 0; half < NG; ++half) {
+        for (int half = 0; half < NG; ++half)
 #pragma unroll
             for (int t = 0; t < KS; ++t)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float carry = FP8 ? vref[half % VG][e % VE] : 1.f;
                     if (ES == 2) {
-                        mine[exch_at<D>(2 * c4 + e, 16 * t + r4)] = o[t][half][e];
-                        mine[exch_at<D>(2 * c4 + e, 16 * t + r4 + 8)] = o[t][half][2 + e];
+                        mine[exch_at<D>(8 * half + 2 * c4 + e, 16 * t + r4)] = o[t][half][e];
+                        mine[exch_at<D>(8 * half + 2 * c4 + e, 16 * t + r4 + 8)] = o[t][half][2 + e];
                     } else if ((t & 1) == 0) {
-                        *(float4*)(mine + exch_at<D>(2 * c4 + e, (D / 8) * r4 + 2 * t)) =
+                        *(float4*)(mine + exch_at<D>(8 * half + 2 * c4 + e, (D / 8) * r4 + 2 * t)) =
                             make_float4(o[t][half][e] * carry, o[t][half][2 + e] * carry, o[t + 1][half][e] * carry,
                                         o[t + 1][half][2 + e] * carry);
                     }
                 }
-            __syncthreads();
-            constexpr int VEC = D / 32;
-            for (int r = warp; r < 8 && r + 8 * half < heads; r += WARPS) {
-                const int h = r + 8 * half;
-                float mm = -INFINITY, ll = 0.f;
+        __syncthreads();
+        constexpr int VEC = D / 32;
+        for (int h = warp; h < heads; h += WARPS) {
+            float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-                for (int i = 0; i < WARPS; ++i) mm = fmaxf(mm, s_ml[i][h].x);
-                float acc[VEC];
+            for (int i = 0; i < WARPS; ++i) mm = fmaxf(mm, s_ml[i][h].x);
+            float acc[VEC];
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) acc[v] = 0.f;
+            for (int v = 0; v < VEC; ++v) acc[v] = 0.f;
 #pragma unroll
-                for (int i = 0; i < WARPS; ++i) {
-                    const float2 ml = s_ml[i][h];
-                    const float g = mm == -INFINITY ? 0.f : fast_exp2(ml.x - mm);
-                    ll += g * ml.y;
-                    const float* from = (const float*)(smem + (i * STAGES + st) * SLOT) + exch_at<D>(r, lane * VEC);
+            for (int i = 0; i < WARPS; ++i) {
+                const float2 ml = s_ml[i][h];
+                const float g = mm == -INFINITY ? 0.f : fast_exp2(ml.x - mm);
+                ll += g * ml.y;
+                const float* from = (const float*)(smem + (i * STAGES + st) * SLOT) + exch_at<D>(h, lane * VEC);
 #pragma unroll
-                    for (int v = 0; v < VEC; ++v) acc[v] = fmaf(g, from[v], acc[v]);
-                }
-                if (begins && ends) {
-                    const float inv = ll == 0.f ? 0.f : 1.f / ll;
-                    const int hr = bunch ? a.by_group.div(h) : 0;
-                    const int64_t to_head = (int64_t)(w.row + hr) * a.n_heads + h0 + h - hr * group;
-                    const int64_t to = to_head * D + lane * VEC;
-#pragma unroll
-                    for (int v = 0; v < VEC; v += 2) {
-                        if (FP32) *(float2*)((float*)a.out + to + v) = make_float2(acc[v] * inv, acc[v + 1] * inv);
-                        else *(uint32_t*)((__nv_bfloat16*)a.out + to + v) = pack2<false>(acc[v] * inv, acc[v + 1] * inv);
-                    }
-                    if (lane == 0)
-                        a.lse[to_head] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * LN2;
-                } else {
-                    float* po = parts.o + ((int64_t)place * GT + h) * D + lane * VEC;
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) po[v] = acc[v];
-                    if (lane == 0) parts.ml[place * GT + h] = make_float2(mm, ll);
-                }
+                for (int v = 0; v < VEC; ++v) acc[v] = fmaf(g, from[v], acc[v]);
             }
-            __syncthreads();
+            if (begins && ends) {
+                const float inv = ll == 0.f ? 0.f : 1.f / ll;
+                const int hr = bunch ? a.by_group.div(h) : 0;
+                const int64_t to_head = (int64_t)(w.row + hr) * a.n_heads + h0 + h - hr * group;
+                const int64_t to = to_head * D + lane * VEC;
+#pragma unroll
+                for (int v = 0; v < VEC; v += 2) {
+                    if (FP32) *(float2*)((float*)a.out + to + v) = make_float2(acc[v] * inv, acc[v + 1] * inv);
+                    else *(uint32_t*)((__nv_bfloat16*)a.out + to + v) = pack2<false>(acc[v] * inv, acc[v + 1] * inv);
+                }
+                if (lane == 0)
+                    a.lse[to_head] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * LN2;
+            } else {
+                float* po = parts.o + ((int64_t)place * GT + h) * D + lane * VEC;
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) po[v] = acc[v];
+                if (lane == 0) parts.ml[place * GT + h] = make_float2(mm, ll);
+            }
         }
+        __syncthreads();
         if (begins && tid < (MANY ? w.rows : 1)) {
             const int64_t last = (at + w.units - 1) / stretch;      // block of the pair's last unit
             parts.meta[((int64_t)(w.row + tid) * a.n_kv_heads + w.kvh) * tiles + w.tile] =
@@ -1112,7 +1111,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Rows of one sequence that share a pair: as many as fill the products' 16
 // columns, when the sequences have one and a half rows or more on average (16
-// heads a pair cost up to 1.4 times the time of 8 per byte, over fp8) and come in
+// heads a pair cost up to 1.5 times the time of 8 per byte, over fp8) and come in
 // runs of about `tokens`.
 int tokens_of(int rows, int batch) { return 2ll * rows < 3ll * batch ? 1 : ceil_div(rows, batch); }
 int merge_of(int group, int tokens) {
