@@ -1086,15 +1086,17 @@ __global__ void __launch_bounds__(128) gqa_combine_kernel(const DecodeArgs a, co
         float top = m;
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) top = fmaxf(top, ml[k].x);
-        if (top == -INFINITY) continue;                     // parts without a visible key
-        const float f = fast_exp2(m - top);
+        // a part without a visible key has zero sums; one whose scores are all
+        // NaN has no maximum either, and NaN sums, which must not be passed over
+        const float base = top > -INFINITY ? top : 0.f;
+        const float f = fast_exp2(m - base);
         m = top;
         l *= f;
 #pragma unroll
         for (int v = 0; v < VEC; ++v) o[v] *= f;
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-            const float g = fast_exp2(ml[k].x - top);
+            const float g = fast_exp2(ml[k].x - base);
             l = fmaf(g, ml[k].y, l);
 #pragma unroll
             for (int v = 0; v < VEC; ++v) o[v] = fmaf(g, po[k][v], o[v]);

@@ -442,6 +442,25 @@ def test_decode_large_scores(cuda_device, kind):
     _decode_check(c, q, out, lse, [0], [2999], 1.0)
 
 
+@pytest.mark.parametrize("group", [4, 12])
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp32"])
+def test_decode_nan_shows_at_any_length(cuda_device, kind, group):
+    """A row of a NaN query, and one whose first half of keys is NaN, are NaN whether a block holds the whole row or
+    many blocks hold parts of it; the rows beside them stand."""
+    lens = [50, 777, 20000, 20000, 300, 30]
+    c = Paged(lens, 2, 64, 16, kind, 37)
+    q = _randn((6, 2 * group, 64), _gen(38), torch.float32 if kind == "fp32" else torch.bfloat16)
+    for r in (0, 1, 2):
+        q[r, :, 11] = NAN
+    (c.k_scale if kind == "fp8" else c.k)[c.table[3, :625].long()] = NAN
+    pos = [n - 1 for n in lens]
+    out, lse = dsa.gqa_decode_attention(q, c.k, c.v, c.table, _i32(range(6)), _i32(pos), 0.15, c.k_scale, c.v_scale)
+    assert dsa.get_device_error(cuda_device) == dsa.DSA_OK
+    for r in range(4):
+        assert bool(torch.isnan(out[r]).all()) and bool(torch.isnan(lse[r]).all()), r
+    _decode_check(c, q[4:], out[4:], lse[4:], [4, 5], pos[4:], 0.15)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "fp32"])
 def test_decode_bad_indexes_are_reported(cuda_device, kind):
     lens = [200, 100]
