@@ -314,12 +314,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// tf32 parts of an fp32 number: hi = x rounded to 11 bits, lo = x - hi, each
-// as the tensor core reads it (it ignores the low 13 bits).
-__device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
-    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-    lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
-}
 // C += A B on tf32: lane (r4, c4) gives A's rows r4 and r4 + 8 at k = c4 (a[0],
 // a[1]) and c4 + 4 (a[2], a[3]), and B's column r4 at k = c4 and c4 + 4.
 __device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -368,10 +362,9 @@ template <int ES, int RB, bool IS_V> __device__ __forceinline__ uint32_t piece_a
     return r * RB + ((RB == 128 ? c ^ ((r & 1) << 2) : c) << 4);
 }
 
-// Whether a word of cache values holds one that is, or in the products becomes,
-// infinite or NaN.
+// Whether a word of cache values holds one that is infinite or NaN.
 template <int ES> __device__ __forceinline__ bool not_finite(uint32_t x) {
-    if (ES == 4) return (x & 0x7fffffffu) >= 0x7f7ff000u;       // (its hi part is rounded up)
+    if (ES == 4) return (x & 0x7f800000u) == 0x7f800000u;
     if (ES == 2) return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
     return __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0u;
 }
@@ -493,10 +486,10 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D, GT>::BLOCKS)) gqa_deco
                     const float4 v = on ? __ldg((const float4*)((const float*)a.q + at_q + 16 * kk + 4 * c4))
                                         : make_float4(0.f, 0.f, 0.f, 0.f);
                     uint32_t y[8];
-                    split(v.x, y[0], y[4]);
-                    split(v.y, y[1], y[5]);
-                    split(v.z, y[2], y[6]);
-                    split(v.w, y[3], y[7]);
+                    tf32_split(v.x, y[0], y[4]);
+                    tf32_split(v.y, y[1], y[5]);
+                    tf32_split(v.z, y[2], y[6]);
+                    tf32_split(v.w, y[3], y[7]);
                     if (Q_SHARED) {
                         st_shared_v4(q_at(2 * kk, g), y[0], y[1], y[4], y[5]);
                         st_shared_v4(q_at(2 * kk + 1, g), y[2], y[3], y[6], y[7]);
@@ -612,10 +605,10 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D, GT>::BLOCKS)) gqa_deco
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 uint32_t hi[4], lo[4];
-                                split(__uint_as_float(xs[2 * i]), hi[0], lo[0]);
-                                split(__uint_as_float(ys[2 * i]), hi[1], lo[1]);
-                                split(__uint_as_float(xs[2 * i + 1]), hi[2], lo[2]);
-                                split(__uint_as_float(ys[2 * i + 1]), hi[3], lo[3]);
+                                tf32_split(__uint_as_float(xs[2 * i]), hi[0], lo[0]);
+                                tf32_split(__uint_as_float(ys[2 * i]), hi[1], lo[1]);
+                                tf32_split(__uint_as_float(xs[2 * i + 1]), hi[2], lo[2]);
+                                tf32_split(__uint_as_float(ys[2 * i + 1]), hi[3], lo[3]);
 #pragma unroll
                                 for (int g = 0; g < NG; ++g) {
                                     uint4 y = make_uint4(qf[kk][2 * i], qf[kk][2 * i + 1], qf[kk][2 * i + 4], qf[kk][2 * i + 5]);
@@ -815,7 +808,7 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D, GT>::BLOCKS)) gqa_deco
                                     const int from = (2 * c4 + e) * 4 + (r4 >> 1);
                                     const float even = __shfl_sync(0xffffffffu, s[ti / 2][g][2 * (ti & 1)], from);
                                     const float odd = __shfl_sync(0xffffffffu, s[ti / 2][g][2 * (ti & 1) + 1], from);
-                                    split((r4 & 1) ? odd : even, ph[ti][g][e], pl[ti][g][e]);
+                                    tf32_split((r4 & 1) ? odd : even, ph[ti][g][e], pl[ti][g][e]);
                                 }
 #pragma unroll
                         for (int n4 = 0; n4 < RUN / 4; ++n4) {
@@ -837,10 +830,10 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D, GT>::BLOCKS)) gqa_deco
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) {
                                     uint32_t hi[4], lo[4];
-                                    split(__uint_as_float(xs[2 * k]), hi[0], lo[0]);
-                                    split(__uint_as_float(xs[2 * k + 1]), hi[1], lo[1]);
-                                    split(__uint_as_float(ys[2 * k]), hi[2], lo[2]);
-                                    split(__uint_as_float(ys[2 * k + 1]), hi[3], lo[3]);
+                                    tf32_split(__uint_as_float(xs[2 * k]), hi[0], lo[0]);
+                                    tf32_split(__uint_as_float(xs[2 * k + 1]), hi[1], lo[1]);
+                                    tf32_split(__uint_as_float(ys[2 * k]), hi[2], lo[2]);
+                                    tf32_split(__uint_as_float(ys[2 * k + 1]), hi[3], lo[3]);
 #pragma unroll
                                     for (int g = 0; g < NG; ++g) {
                                         mma1688(step[k][g], lo, ph[ti][g][0], ph[ti][g][1]);

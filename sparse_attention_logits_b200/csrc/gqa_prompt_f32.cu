@@ -88,14 +88,11 @@ __device__ __forceinline__ bool find_tile(const PromptArgs& a, int t, Tile& w, i
 }
 
 
-// tf32 parts of an fp32 number: hi = x rounded to 11 bits, lo = x - hi, each
-// as the tensor core reads it (it ignores the low 13 bits).
+// The tf32 parts of two numbers: (hi, lo, hi, lo).
 __device__ __forceinline__ uint4 split2(float x, float y) {
     uint4 r;
-    r.x = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-    r.y = __float_as_uint(x - __uint_as_float(r.x)) + 0x1000u;
-    r.z = (__float_as_uint(y) + 0x1000u) & 0xffffe000u;
-    r.w = __float_as_uint(y - __uint_as_float(r.z)) + 0x1000u;
+    tf32_split(x, r.x, r.y);
+    tf32_split(y, r.z, r.w);
     return r;
 }
 __device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {

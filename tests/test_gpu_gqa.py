@@ -162,6 +162,42 @@ def test_prompt_nan_queries_stay_in_their_rows(cuda_device):
     assert bool(torch.isnan(out[~rows]).all())
 
 
+# An fp32 NaN as torch fills it in, and as GPU arithmetic makes it.
+NAN_BITS = {"filled": 0x7FC00000, "computed": 0x7FFFFFFF, "negative": -1}
+
+
+def _nan(which):
+    return _i32([NAN_BITS[which]]).view(torch.float32)[0]
+
+
+@pytest.mark.parametrize("which", list(NAN_BITS))
+@pytest.mark.parametrize("D", [64, 128])
+def test_fp32_prompt_nan_queries_show_and_stay_in_their_rows(cuda_device, D, which):
+    q, k, v = (_randn((300, 2, D), _gen(8)) for _ in range(3))
+    clean = dsa.gqa_prompt_attention(q, k, v, _i32([0, 300]), 0.1)
+    bad = [5, 130, 299]
+    q = q.clone()
+    q[bad, :, 7] = _nan(which)                              # one element of a row is enough
+    out, lse = dsa.gqa_prompt_attention(q, k, v, _i32([0, 300]), 0.1)
+    rows = torch.ones(300, dtype=torch.bool, device="cuda")
+    rows[bad] = False
+    assert torch.equal(out[rows], clean[0][rows]) and torch.equal(lse[rows], clean[1][rows])
+    assert bool(torch.isnan(out[~rows]).all()) and bool(torch.isnan(lse[~rows]).all())
+
+
+def test_fp32_prompt_largest_numbers(cuda_device):
+    """Keys and values next to the largest fp32 number: their parts must not round up to infinity."""
+    top, near = torch.finfo(torch.float32).max, float.fromhex("0x1.FFEp127")
+    g, n = _gen(9), 40
+    q, k, v = (_randn((n, 2, 64), g) for _ in range(3))
+    q[:, :, 3] = 0
+    k[:, 0, 3], k[:, 1, 3] = top, -top
+    v[0, 0, 5], v[0, 1, 6] = near, -near                      # row 0 sees itself alone
+    out, lse = dsa.gqa_prompt_attention(q, k, v, _i32([0, 1, n]), 0.1)
+    for a, b in ((0, 1), (1, n)):
+        _prompt_check(out, lse, q, k, v, None, 0.1, a, b)
+
+
 def test_prompt_row_strides_past_32_bits(cuda_device):
     """Rows 2.5 MB apart: the last lie more than 2^31 elements behind the first."""
     n, wide = 1800, 1250000
@@ -440,6 +476,57 @@ def test_decode_large_scores(cuda_device, kind):
         c.k64 = c.k.double() * c.k_scale.double()[..., None]
     out, lse = dsa.gqa_decode_attention(q, c.k, c.v, c.table, _i32([0]), _i32([2999]), 1.0, c.k_scale, c.v_scale)
     _decode_check(c, q, out, lse, [0], [2999], 1.0)
+
+
+@pytest.mark.parametrize("which", list(NAN_BITS))
+@pytest.mark.parametrize("H,Hkv,D", [(8, 2, 64), (8, 2, 128), (24, 2, 64)])
+def test_fp32_decode_nan_is_not_lost(cuda_device, H, Hkv, D, which):
+    """A NaN in a query, or in a visible key or value, shows in everything that it takes part in, and there alone."""
+    lens, g = [50, 777], H // Hkv
+    c = Paged(lens, Hkv, D, 16, "fp32", 33)
+    q = _randn((2, H, D), _gen(34))
+
+    def run(q):
+        return dsa.gqa_decode_attention(q, c.k, c.v, c.table, _i32([0, 1]), _i32([49, 776]), 0.15)
+    clean = run(q)
+    bad = q.clone()
+    bad[1, 3, 7] = _nan(which)
+    out, lse = run(bad)
+    hit = torch.zeros(2, H, dtype=torch.bool, device="cuda")
+    hit[1, 3] = True
+    assert bool(torch.isnan(out[hit]).all()) and bool(torch.isnan(lse[hit]).all())
+    assert torch.equal(out[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
+    for b, at in ((0, 0), (0, 49), (1, 401)):
+        hit = torch.zeros(2, H, dtype=torch.bool, device="cuda")
+        hit[b, g:] = True                                   # (kv head 1)
+        for cache in (c.k, c.v):
+            place = cache[int(c.table[b, at // 16]), 1, at % 16]
+            was = place[9].clone()
+            place[9] = _nan(which)
+            out, lse = run(q)
+            place[9] = was
+            assert torch.equal(out[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
+            if cache is c.k:
+                assert bool(torch.isnan(out[hit]).all()) and bool(torch.isnan(lse[hit]).all())
+            else:
+                dims = torch.arange(D, device="cuda") == 9
+                assert bool(torch.isnan(out[hit][:, dims]).all()) and torch.equal(lse[hit], clean[1][hit])
+                assert torch.equal(out[hit][:, ~dims], clean[0][hit][:, ~dims])
+
+
+def test_fp32_decode_largest_numbers(cuda_device):
+    """Keys and values next to the largest fp32 number: their parts must not round up to infinity."""
+    top, near = torch.finfo(torch.float32).max, float.fromhex("0x1.FFEp127")
+    c = Paged([1, 90], 2, 64, 16, "fp32", 35)
+    q = _randn((2, 4, 64), _gen(36))
+    q[:, :, 3] = 0
+    for b, n in ((0, 1), (1, 90)):
+        for at in range(n):
+            c.k[int(c.table[b, at // 16]), :, at % 16, 3] = top if at % 2 else -top
+    c.v[int(c.table[0, 0]), 0, 0, 5], c.v[int(c.table[0, 0]), 1, 0, 6] = near, -near      # (sequence 0 has one token)
+    c.k64, c.v64 = c.k.double(), c.v.double()
+    out, lse = dsa.gqa_decode_attention(q, c.k, c.v, c.table, _i32([0, 1]), _i32([0, 89]), 0.15)
+    _decode_check(c, q, out, lse, [0, 1], [0, 89], 0.15)
 
 
 @pytest.mark.parametrize("group", [4, 12])
