@@ -38,6 +38,9 @@ namespace {
 constexpr int THREADS = 128;
 constexpr int WARPS = THREADS / 32;
 constexpr float LN2 = 0.6931471805599453f;
+// fp8: what a weight at the reference becomes; the reference's range, in which
+// WEIGHT_ONE / reference is a normal number.
+constexpr float WEIGHT_ONE = 8192.f, VREF_LEAST = 1e-30f, VREF_MOST = 0x1p126f;
 
 // 2^x on the MUFU unit: relative error ~2^-22, -inf -> +0.
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -260,9 +263,14 @@ __device__ __forceinline__ int cache_row(const DecodeArgs& a, Place p) {
 //
 // fp8: codes are widened to f16 (exact) on the way into the product.  The
 // query row is first brought to [1, 2) by a power of two, so that f16 holds
-// it (a value below 2^-14 of the row's largest loses bits below 2^-25 of it);
-// P is taken times the value scale relative to the largest scale met so far,
-// which the output carries like the running maximum.
+// it (a value below 2^-14 of the row's largest loses bits below 2^-25 of it).
+// The second product's weights are p v_scale, as f16 too, relative to the
+// largest of them that the warp has met for the head: a reference of its own
+// beside the running maximum, since a large scale may belong to a key of next to
+// no weight.  It stands at 2^13 of f16's 2^-24 .. 2^16, so that a weight down to
+// 2^-27 of the largest keeps all 11 bits, and no weight is off by more than 2^-38
+// of it.  Rows of zero codes do not count: their scale says nothing about the
+// others' (the writer's is 1).
 //
 // fp32: every factor is split into two tf32 numbers, x = hi + lo (11 + 11
 // bits), and a product is three tensor products hi hi + hi lo + lo hi, the
@@ -391,7 +399,6 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D, GT>::BLOCKS)) gqa_deco
     constexpr int KS = D / 16, MT = WK / 16, NG = GT / 8;   // k-steps; tiles of 16 keys, of 8 heads
     constexpr bool MANY = GT == 16;                 // pairs of several rows
     constexpr bool Q_SHARED = MANY && ES != 2;      // query fragments in shared memory, for want of registers
-    constexpr int VG = MANY ? NG : 1, VE = MANY ? 2 : 1;    // references of the value scales: per head, or one
     static_assert(!FP8 || WK == 32, "a lane per key's scales");
     static_assert(2 * SLICE >= GT * D * 4, "the outputs of a pair's heads are exchanged in a slot");
     extern __shared__ __align__(128) uint8_t smem[];
@@ -556,17 +563,13 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D, GT>::BLOCKS)) gqa_deco
             for (int g = 0; g < NG; ++g)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[t][g][e] = 0.f;
-        float m[NG][2], l[NG][2], vref[VG][VE], vinv[VG][VE];
-#pragma unroll
-        for (int g = 0; g < VG; ++g)
-#pragma unroll
-            for (int e = 0; e < VE; ++e) vref[g][e] = vinv[g][e] = 0.f;
+        float m[NG][2], l[NG][2], vref[NG][2];      // (vref: fp8)
 #pragma unroll
         for (int g = 0; g < NG; ++g)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 m[g][e] = -INFINITY;
-                l[g][e] = 0.f;
+                l[g][e] = vref[g][e] = 0.f;
             }
 
         for (int u = 0; u < n; ++u) {
@@ -706,7 +709,7 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D, GT>::BLOCKS)) gqa_deco
                             for (int e = 0; e < 2; ++e)
                                 if (key0 + 8 * t + r4 >= sees[g][e]) s[t / 2][g][2 * (t & 1) + e] = -INFINITY;
                 }
-                // running maximum (scores times zs; zs > 0), and the output brought to it
+                // running maximum (scores times zs; zs > 0), and the output brought to it (fp8: below)
                 float f[NG][2];
                 bool moved = false;
 #pragma unroll
@@ -727,45 +730,13 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D, GT>::BLOCKS)) gqa_deco
                             moved = true;
                         }
                     }
-                float vmove[VG][VE], all_top = 0.f;
-#pragma unroll
-                for (int g = 0; g < VG; ++g)
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) vmove[g][e] = 1.f;
-                if (FP8) {
-                    // the largest value scale (MANY: of the keys that a head sees)
-#pragma unroll
-                    for (int g = 0; g < VG; ++g)
-#pragma unroll
-                        for (int e = 0; e < VE; ++e) {
-                            float top = 0.f;
-                            if (MANY && !partly && g + e > 0) {
-                                top = all_top;
-                            } else {
-#pragma unroll
-                                for (int t = 0; t < WK / 8; ++t)
-                                    if (!MANY || !partly || key0 + 8 * t + r4 < sees[g][e]) top = fmaxf(top, fabsf(vs[t]));
-                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                                top = fmaxf(top, 1e-30f);               // its reciprocal is finite
-                                all_top = top;
-                            }
-                            if (top > vref[g][e]) {
-                                vmove[g][e] = vref[g][e] / top;
-                                vref[g][e] = top;
-                                vinv[g][e] = 1.f / top;
-                                moved = true;
-                            }
-                        }
-                }
-                if (__any_sync(0xffffffffu, moved)) {
+                if (!FP8 && __any_sync(0xffffffffu, moved)) {
 #pragma unroll
                     for (int t = 0; t < KS; ++t)
 #pragma unroll
                         for (int g = 0; g < NG; ++g)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) o[t][g][e] *= f[g][e & 1] * vmove[g % VG][e % VE];
+                            for (int e = 0; e < 4; ++e) o[t][g][e] *= f[g][e & 1];
                 }
 #pragma unroll
                 for (int g = 0; g < NG; ++g)
@@ -778,10 +749,82 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D, GT>::BLOCKS)) gqa_deco
                             for (int i = 0; i < 2; ++i) {
                                 const float p = fast_exp2(fmaf(s[t][g][2 * i + e], zs[g][e], -base));
                                 l[g][e] += p;
-                                s[t][g][2 * i + e] = FP8 ? p * (vs[2 * t + i] * vinv[g % VG][e % VE]) : p;
+                                s[t][g][2 * i + e] = FP8 ? p * vs[2 * t + i] : p;
                                 if (FP8 && MANY && partly && key0 + 16 * t + 8 * i + r4 >= sees[g][e]) s[t][g][2 * i + e] = 0.f;
                             }
                     }
+                if constexpr (FP8) {
+                    // the weights p v_scale relative to vref, which follows the largest of them at a distance of 2;
+                    // vref too is relative to the running maximum, so that the output need not move with it
+                    auto largest = [&](int g, int e) {
+                        float top = 0.f;
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) top = fmaxf(top, fmaxf(fabsf(s[t][g][e]), fabsf(s[t][g][2 + e])));
+                        return top;
+                    };
+                    bool grows = false;
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            vref[g][e] *= f[g][e];
+                            grows = grows || largest(g, e) > 2.f * vref[g][e] || vref[g][e] < VREF_LEAST;
+                        }
+                    if (__any_sync(0xffffffffu, grows)) {
+                        // rows whose codes are all zero weigh nothing, whatever their scale: where one of a
+                        // row's pieces is zero, the rows are looked at whole
+                        constexpr int READS = WK * PIECES / 32, PER = 32 / PIECES;     // rows a read covers
+                        auto codes = [&](int r, int c) {
+                            const uint4 x = ld_shared_v4(slot + SLICE + piece_at<ES, RB, true>(r, c));
+                            return (x.x | x.y | x.z | x.w) & 0x7f7f7f7fu;
+                        };
+                        if (__any_sync(0xffffffffu, codes(lane, lane % PIECES) == 0u && ((valid >> lane) & 1u))) {
+                            uint32_t some[READS];
+#pragma unroll
+                            for (int i = 0; i < READS; ++i)
+                                some[i] = __ballot_sync(0xffffffffu, codes(i * PER + lane / PIECES, lane % PIECES) != 0u);
+#pragma unroll
+                            for (int t = 0; t < WK / 8; ++t) {
+                                const uint32_t rows8 = PER == 8 ? some[t % READS] : (r4 & 4) ? some[(2 * t + 1) % READS] : some[2 * t % READS];
+                                if ((rows8 >> (r4 % PER * PIECES) & ((1u << PIECES) - 1u)) == 0u) {
+#pragma unroll
+                                    for (int g = 0; g < NG; ++g)
+#pragma unroll
+                                        for (int e = 0; e < 2; ++e) s[t / 2][g][2 * (t & 1) + e] *= 0.f;    // (NaN stays)
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            float move[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float top = largest(g, e);
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                                const float was = vref[g][e];
+                                if (top > 2.f * was) vref[g][e] = top;
+                                vref[g][e] = fminf(fmaxf(vref[g][e], VREF_LEAST), VREF_MOST);
+                                move[e] = __fdividef(was, vref[g][e]);
+                            }
+#pragma unroll
+                            for (int t = 0; t < KS; ++t)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) o[t][g][e] *= move[e & 1];
+                        }
+                    }
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float inv = __fdividef(WEIGHT_ONE, vref[g][e]);
+#pragma unroll
+                            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) s[t][g][2 * i + e] *= inv;
+                        }
+                }
                 // O^T += V^T P^T.  Zero times a value that a row may not see need not be zero: where some
                 // such value is infinite or NaN, the product is formed once per row (ONE: the row of `sees`
                 // = n_keys) with the values behind its keys set to zero, for its columns alone.
@@ -975,7 +1018,7 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D, GT>::BLOCKS)) gqa_deco
             for (int t = 0; t < KS; ++t)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float carry = FP8 ? vref[half % VG][e % VE] : 1.f;
+                    const float carry = FP8 ? vref[half][e] * (1.f / WEIGHT_ONE) : 1.f;
                     if (ES == 2) {
                         mine[exch_at<D>(8 * half + 2 * c4 + e, 16 * t + r4)] = o[t][half][e];
                         mine[exch_at<D>(8 * half + 2 * c4 + e, 16 * t + r4 + 8)] = o[t][half][2 + e];

@@ -548,6 +548,56 @@ def test_decode_nan_shows_at_any_length(cuda_device, kind, group):
     _decode_check(c, q[4:], out[4:], lse[4:], [4, 5], pos[4:], 0.15)
 
 
+@pytest.mark.parametrize("H,Hkv,D,per", [(8, 2, 128, 1), (8, 2, 64, 1), (24, 2, 64, 1), (16, 1, 128, 1), (4, 2, 64, 3), (8, 2, 128, 2)])
+@pytest.mark.parametrize("size", [1.0, 1e-2, 1e-3, 1e-4, 1e-6])
+def test_decode_fp8_zero_rows_beside_small_values(cuda_device, size, H, Hkv, D, per):
+    """All-zero value rows (codes +0 or -0) have the scale 1, however small the others' values are; beside them rows that
+    are zero but for a few dims, and count."""
+    lens = [9000, 200]
+    c = Paged(lens, Hkv, D, 16, "fp8", 39)
+    c.v_scale *= size
+    zero = torch.arange(c.v.shape[0] * Hkv * 16, device="cuda").reshape(c.v.shape[:3]) % 13 == 4
+    zero &= ~torch.isnan(c.v_scale)
+    codes = c.v.view(torch.uint8)
+    codes[zero] = torch.where(torch.arange(D, device="cuda") % 3 == 0, 0x80, 0).to(torch.uint8)
+    c.v_scale[zero] = 1.0
+    few = torch.arange(zero.numel(), device="cuda").reshape(zero.shape) % 13 == 9
+    codes[..., :D - 5][few & ~torch.isnan(c.v_scale)] = 0
+    c.v64 = c.v.double() * c.v_scale.double()[..., None]
+    batch = [b for b in range(2) for _ in range(per)]
+    pos = [n - per + i for n in lens for i in range(per)]
+    q = _randn((2 * per, H, D), _gen(40), torch.bfloat16)
+    out, lse = dsa.gqa_decode_attention(q, c.k, c.v, c.table, _i32(batch), _i32(pos), 0.15, c.k_scale, c.v_scale)
+    _decode_check(c, q, out, lse, batch, pos, 0.15)
+
+
+@pytest.mark.parametrize("group", [1, 9])
+@pytest.mark.parametrize("ratio", [1e3, 1e8])
+def test_decode_fp8_value_scales_far_apart(cuda_device, ratio, group):
+    """A token of next to no weight whose value scale is far above the others', one token that holds most of the weight,
+    and thousands that share the rest.  300 rows over the same pages, so that a block meets a row's keys one after another."""
+    n, D, rows = 5000, 128, 300
+    c = Paged([n], 1, D, 16, "fp8", 41)
+    q1 = _randn((D,), _gen(42), torch.bfloat16)
+    q = q1.expand(rows, group, D).contiguous()
+    scale, unit = 0.1, q1.float() / float((q1.float() ** 2).sum())
+
+    def put(at, z, v_scale):                                # a key of score z; its value's scale
+        page, slot = int(c.table[0, at // 16]), at % 16
+        codes, s = e4m3_rows((unit * (z / scale))[None])
+        c.k.view(torch.uint8)[page, 0, slot], c.k_scale[page, 0, slot] = codes.view(torch.uint8)[0], s[0]
+        c.v_scale[page, 0, slot] *= v_scale
+    c.k_scale *= 1e-3                                       # scores of nearly 0
+    put(3, 11.5, 1e-3)
+    put(17, -2.0 * math.log(ratio), ratio)
+    put(3333, -60.0, ratio)
+    c.k64, c.v64 = (x.double() * s.double()[..., None] for x, s in ((c.k, c.k_scale), (c.v, c.v_scale)))
+    table = c.table.expand(rows, -1).contiguous()
+    out, lse = dsa.gqa_decode_attention(q, c.k, c.v, table, _i32(range(rows)), _i32([n - 1] * rows), scale, c.k_scale, c.v_scale)
+    for r in (0, 1, 2, 137, rows - 1):
+        _decode_check(c, q[r:r + 1], out[r:r + 1], lse[r:r + 1], [0], [n - 1], scale)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "fp32"])
 def test_decode_bad_indexes_are_reported(cuda_device, kind):
     lens = [200, 100]
