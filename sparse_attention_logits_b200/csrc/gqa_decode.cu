@@ -27,6 +27,7 @@
 #include "launchers.h"
 #include "sm100.cuh"
 
+#include <cfloat>
 #include <type_traits>
 
 namespace dsa {
@@ -528,7 +529,8 @@ __global__ void __launch_bounds__(THREADS, (MmaCfg<KV, D, GT>::BLOCKS)) gqa_deco
                 // 2^e <= top < 2^(e + 1), e kept where 2^-e is a normal number
                 const int e = min(max((int)(__float_as_uint(top) >> 23), 1), 253) - 127;
                 const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-                const float up = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);     // of head r4
+                // of head r4; a normal number, so that a hidden key's score (-inf times it) stays -inf
+                const float up = fminf(fmaxf(a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23), FLT_MIN), FLT_MAX);
 #pragma unroll
                 for (int kk = 0; kk < KS; ++kk)
 #pragma unroll

@@ -598,6 +598,16 @@ def test_decode_fp8_value_scales_far_apart(cuda_device, ratio, group):
         _decode_check(c, q[r:r + 1], out[r:r + 1], lse[r:r + 1], [0], [n - 1], scale)
 
 
+@pytest.mark.parametrize("group", [4, 12])
+@pytest.mark.parametrize("scale", [1e-7, 1e-9, 1e-30])
+def test_decode_fp8_zero_query_and_small_scale(cuda_device, scale, group):
+    """Queries of zeros (padding) see the mean of the values at any scale."""
+    c = Paged([45, 300], 1, 64, 16, "fp8", 43)
+    q = torch.zeros((2, group, 64), dtype=torch.bfloat16, device="cuda")
+    out, lse = dsa.gqa_decode_attention(q, c.k, c.v, c.table, _i32([0, 1]), _i32([44, 299]), scale, c.k_scale, c.v_scale)
+    _decode_check(c, q, out, lse, [0, 1], [44, 299], scale)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "fp32"])
 def test_decode_bad_indexes_are_reported(cuda_device, kind):
     lens = [200, 100]
