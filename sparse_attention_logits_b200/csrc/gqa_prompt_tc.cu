@@ -178,9 +178,10 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
+// The largest of three; NaN where one is NaN.
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 
@@ -351,15 +352,20 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prompt_tc_kernel(const __grid_
                         for (int e = 0; e < 32; ++e)
                             if (c * 32 + e > r) s[c][e] = -INFINITY;
                 }
+                // The tile's largest score.  Where it is NaN or +inf, so is the row's sum from here on: the
+                // weights alone would not show it, as exp2_fma gives 0 for a NaN.
                 auto largest = [&]() {
                     float mx[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) mx[c] = fmaxf(s[c][0], s[c][1]);
+                    for (int c = 0; c < 4; ++c) mx[c] = max3(s[c][0], s[c][1], s[c][2]);
 #pragma unroll
-                    for (int e = 2; e < 32; e += 2)
+                    for (int e = 3; e < 31; e += 2)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) mx[c] = max3(mx[c], s[c][e], s[c][e + 1]);
-                    return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale_log2;
+                    const float top = max3(max3(mx[0], mx[1], s[0][31]), max3(mx[2], mx[3], s[1][31]),
+                                           max3(s[2][31], s[3][31], mx[0])) * a.scale_log2;
+                    if (!(top < INFINITY)) l = __uint_as_float(0x7fffffffu);
+                    return top;
                 };
                 const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
                 float2 sum[2], neg;

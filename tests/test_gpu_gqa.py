@@ -198,6 +198,23 @@ def test_fp32_prompt_largest_numbers(cuda_device):
         _prompt_check(out, lse, q, k, v, None, 0.1, a, b)
 
 
+@pytest.mark.parametrize("H,Hkv,D,n,places", [
+    (4, 2, 128, 200, [*range(34), 63, 100, 127, 128, 140, 199]), (3, 1, 64, 300, [0, 1, 12, 13, 22, 23, 250, 258]),
+    (1, 1, 64, 1800, [0, 13, 900, 1300])])                  # (the last: a row's keys in parts)
+def test_prompt_nan_and_infinite_scores_show_at_any_place(cuda_device, H, Hkv, D, n, places):
+    """A key that gives some row a NaN or an infinite score leaves NaN in that row, whichever key it is."""
+    q, k, v = (_randn((n, h, D), _gen(10), torch.bfloat16) for h in (H, Hkv, Hkv))
+    q[:, :, 5] = q[:, :, 5].abs() + 0.5
+    clean = dsa.gqa_prompt_attention(q, k, v, _i32([0, n]), 0.1)
+    for at in places:
+        for bad in (NAN, math.inf):
+            x = k.clone()
+            x[at, :, 5] = bad
+            out, lse = dsa.gqa_prompt_attention(q, x, v, _i32([0, n]), 0.1)
+            assert bool(torch.isnan(out[at:]).all()) and bool(torch.isnan(lse[at:]).all()), (at, bad)
+            assert torch.equal(out[:at], clean[0][:at]) and torch.equal(lse[:at], clean[1][:at]), (at, bad)
+
+
 def test_prompt_row_strides_past_32_bits(cuda_device):
     """Rows 2.5 MB apart: the last lie more than 2^31 elements behind the first."""
     n, wide = 1800, 1250000
