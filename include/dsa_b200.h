@@ -504,9 +504,11 @@ DSA_API dsa_status_t gqa_prompt_attention(const void* q, int64_t ld_q, const voi
  * its first place.  Fresh pages are the lowest-numbered free ones, in the
  * list's order, so results are deterministic.  An entry that cannot be served
  * changes nothing and is reported by dsa_get_device_error: DSA_ERR_INVALID_ARG for
- * a sequence, length or page out of range and, except by kv_pages_free, for one
- * listed twice; DSA_ERR_OUT_OF_PAGES for want of free pages.  Calls on one
- * pool must be in order on one stream.
+ * a sequence or length out of range, for a parent that holds a page out of range
+ * and, except by kv_pages_free, for a sequence listed twice; DSA_ERR_OUT_OF_PAGES
+ * for want of free pages.  (kv_pages_free drops a sequence in every case; it passes
+ * over pages that are out of range or free already and reports them.)  Calls on
+ * one pool must be in order on one stream.
  * The functions serve any paged cache of the library, the latent cache of
  * dsa_sparse_mla among them: a cache is a pointer and the bytes of its pages.
  */

@@ -411,6 +411,8 @@ kv_assign_kernel(const BooksArgs a, int words_per_cta) {
     int* len = start + a.n + 1;                         // [n] extend: new length; fork: the parent's; -1: not served
     int* what = len + a.n;                              // [n] sequence (fork: child)
     int* entry = what + a.n;                            // [n] table entry of the item's page of rank 0
+    int* bad_row = entry + a.n;                         // [n] fork: whether a page of the parent is out of range, said by
+                                                        // block i % 8 for item i and read by the others
     const int rank = (int)cluster_ctarank(), tid = threadIdx.x;
     auto place = [&](int w) { return (w / RUN_WORDS * BOOK_CTAS + rank) * RUN_WORDS + w % RUN_WORDS; };
     const int32_t* list = FORK ? a.children : a.seqs;
@@ -460,6 +462,28 @@ kv_assign_kernel(const BooksArgs a, int words_per_cta) {
         start[i] = need;
         need_sum += need;
     }
+    const int lane = tid & 31;
+    if (FORK) {
+        // a branch shares all of its parent's pages or none: the parents' rows, dealt to the cluster's warps
+        __syncthreads();
+        for (int i = rank + BOOK_CTAS * (tid >> 5); i < a.n; i += BOOK_CTAS * BOOK_WARPS) {
+            const int pages = pages_of(len[i], a.page_size);
+            const int32_t* row = a.page_table + (pages > 0 ? (int64_t)a.parents[i] * a.max_pages : 0);
+            bool out = false;
+            for (int j = lane; j < pages; j += 32) out |= row[j] < 0 || row[j] >= a.num_pages;
+            out = __any_sync(0xffffffffu, out);
+            if (lane == 0) bad_row[i] = out;
+        }
+        __syncwarp();
+        cluster_sync_all();
+        for (int i = i0; i < i1; ++i)
+            if (ld_cluster_s32(bad_row + i, i % BOOK_CTAS)) {
+                bad = true;
+                len[i] = -1;
+                need_sum -= start[i];
+                start[i] = 0;
+            }
+    }
     if (bad && rank == 0) record_error(a.err, DEV_ERR_BAD_INDEX);
     int total_need;
     int run = block_scan(need_sum, sh.warp_sum[0], &total_need);
@@ -487,7 +511,7 @@ kv_assign_kernel(const BooksArgs a, int words_per_cta) {
 
     // the free pages to the items that they fall to: a page per lane; a warp's
     // words follow one another, so that a lane's item is mostly its last one's
-    const int lane = tid & 31, wper = (words_per_cta + BOOK_WARPS - 1) / BOOK_WARPS;
+    const int wper = (words_per_cta + BOOK_WARPS - 1) / BOOK_WARPS;
     const int w0 = min(words_per_cta, (tid >> 5) * wper), w1 = min(words_per_cta, w0 + wper);
     int lo = 0;
     for (int w = w0; w < w1; ++w) {
@@ -526,11 +550,10 @@ kv_assign_kernel(const BooksArgs a, int words_per_cta) {
             const int full = served ? len[i] / a.page_size : 0;
             const int32_t* from = a.page_table + (served ? (int64_t)a.parents[i] * a.max_pages : 0);
             int32_t* to = a.page_table + (served ? (int64_t)what[i] * a.max_pages : 0);
-            for (int j = lane; j < full; j += 32) {
+            for (int j = lane; j < full; j += 32) {         // (all in range)
                 const int p = from[j];
                 to[j] = p;
-                if (p >= 0 && p < a.num_pages) atomicAdd(a.ref_count + p, 1);
-                else record_error(a.err, DEV_ERR_BAD_INDEX);
+                atomicAdd(a.ref_count + p, 1);
             }
             if (lane == 0) {
                 a.pair_src[i] = served && need ? from[full] : -1;
@@ -656,7 +679,7 @@ constexpr int words_per_assign_cta(int num_pages) {
     return ceil_div(words_per_book_cta(num_pages), RUN_WORDS) * RUN_WORDS;
 }
 constexpr int books_smem(int num_pages, int n) {
-    return (words_per_assign_cta(num_pages) / RUN_WORDS * (RUN_WORDS + 2) + 4 * n + 1) * 4;
+    return (words_per_assign_cta(num_pages) / RUN_WORDS * (RUN_WORDS + 2) + 5 * n + 1) * 4;
 }
 constexpr int BOOK_SMEM_MAX = books_smem(DSA_KV_PAGES_MAX_POOL, DSA_KV_PAGES_MAX_LIST);
 constexpr int PLAN_SMEM_MAX = 3 * 4 * words_per_book_cta(DSA_KV_PAGES_MAX_POOL);

@@ -239,3 +239,64 @@ def test_captured_turnover(cuda_device):
         p.moved(p.plain.fork([2], [4]))
         p.same()
     assert dsa.get_device_error(cuda_device) == dsa.DSA_OK
+
+
+def _pool_of(lens, page, width, num_pages):
+    """Books for sequences of these lengths, extended in one call."""
+    p = Both(len(lens) + 2, width, page, num_pages, ((page * 16,),))
+    p.extend(list(range(len(lens))), lens)
+    assert _status() == dsa.DSA_OK
+    p.same()
+    return p
+
+
+@pytest.mark.parametrize("at,bad", [(0, -1), (1, 12), (1, 10 ** 6), (2, -1), (2, -7), (2, 12)])
+@pytest.mark.parametrize("tail", [1, 4])
+def test_fork_of_a_parent_with_a_bad_page_changes_nothing(cuda_device, tail, at, bad):
+    """A parent one of whose pages (a full one, or the last) is out of range: its branch is refused whole, the others of
+    the same call are served, and a page that the refused one would have taken goes to the next."""
+    p = _pool_of([8 + tail, 7], 4, 4, 12)               # parent 0: two full pages and one of `tail` tokens
+    was = int(p.table[0, at])
+    p.table[0, at] = bad
+    before = [x.clone() for x in (p.table, p.length, p.count, *p.caches)]
+    dsa.kv_pages_fork(p.table, p.length, p.count, _i32([0]), _i32([2]), 4, p.caches)
+    assert _status() == dsa.DSA_ERR_INVALID_ARG
+    assert all(torch.equal(a, b) for a, b in zip(before, (p.table, p.length, p.count, *p.caches)))
+    dsa.kv_pages_fork(p.table, p.length, p.count, _i32([0, 1]), _i32([2, 3]), 4, p.caches)
+    assert _status() == dsa.DSA_ERR_INVALID_ARG
+    p.table[0, at] = was
+    p.moved(p.plain.fork([1], [3]))
+    p.same()
+
+
+def test_many_forks_with_bad_pages_among_them(cuda_device):
+    """More entries than the cluster's blocks have warps, every seventh parent with a page out of range."""
+    n, page, width = 600, 4, 70
+    r = random.Random(6)
+    lens = [r.randint(1, page * width) for _ in range(n)]
+    p = Both(2 * n, width, page, sum(-(-x // page) for x in lens) + n, ())
+    p.extend(list(range(n)), lens)
+    kept = p.table.clone()
+    for q in range(0, n, 7):
+        p.table[q, r.randrange(-(-lens[q] // page))] = r.choice([-1, -3, p.count.numel(), 2 ** 31 - 1])
+    broken = p.table.clone()
+    dsa.kv_pages_fork(p.table, p.length, p.count, _i32(list(range(n))), _i32(list(range(n, 2 * n))), page, ())
+    assert _status() == dsa.DSA_ERR_INVALID_ARG
+    assert torch.equal(p.table[:n], broken[:n])
+    p.table[:n] = kept[:n]
+    good = [q for q in range(n) if q % 7]
+    p.plain.fork(good, [n + q for q in good])
+    p.same()
+
+
+@pytest.mark.parametrize("bad", [-1, -5, 12, 2 ** 31 - 1])
+def test_free_of_a_sequence_with_a_bad_page(cuda_device, bad):
+    """Dropped all the same: the page out of range is passed over and reported, the others are given back."""
+    p = _pool_of([9, 7], 4, 4, 12)
+    page = int(p.table[0, 1])
+    p.table[0, 1] = bad
+    dsa.kv_pages_free(p.table, p.length, p.count, _i32([0]), 4)
+    assert _status() == dsa.DSA_ERR_INVALID_ARG
+    p.plain.free([0])
+    p.plain.count[page] = 1                                 # nobody's any more, and not given back
+    p.same()
