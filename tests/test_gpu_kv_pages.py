@@ -300,3 +300,82 @@ def test_free_of_a_sequence_with_a_bad_page(cuda_device, bad):
     p.plain.free([0])
     p.plain.count[page] = 1                                 # nobody's any more, and not given back
     p.same()
+
+
+@pytest.mark.parametrize("seed", [2, 3, 4])
+def test_random_lives_report_what_was_refused(cuda_device, seed):
+    """After each action the device status is the one that the plain books give: entries out of range first, then
+    want of pages, else none."""
+    batch, width, page, pages = 12, 6, 4, 14
+    r = random.Random(seed)
+    p = Both(batch, width, page, pages, ((16,),), seed)
+    met = set()
+    for _ in range(60):
+        act, some = r.choice(["extend", "extend", "free", "fork"]), r.sample(range(batch), r.randint(1, 3))
+        free, length = p.plain.count.count(0), list(p.plain.length)
+        asked, invalid, short = 0, False, False
+
+        def want(n):
+            nonlocal asked, short
+            asked += n
+            short |= n > 0 and asked > free
+        if act == "extend":
+            add = [-1 if r.random() < 0.1 else r.randint(0, page * width) for _ in some]
+            for q, a in zip(some, add):
+                if a < 0 or length[q] + a > page * width:
+                    invalid = True
+                else:
+                    want(p.plain.up(length[q] + a) - p.plain.up(length[q]))
+            p.extend(some, add)
+        elif act == "free":
+            p.free(some)
+        else:
+            parents = [r.randrange(batch) for _ in some]
+            for a, b in zip(parents, some):
+                if length[b]:
+                    invalid = True
+                else:
+                    want(length[a] % page > 0)
+            p.fork(parents, some)
+        code = dsa.DSA_ERR_INVALID_ARG if invalid else dsa.DSA_ERR_OUT_OF_PAGES if short else dsa.DSA_OK
+        met.add(code)
+        assert _status() == code, act
+        p.same()
+    assert len(met) == 3
+
+
+@pytest.mark.parametrize("dtype,d,heads", [(torch.bfloat16, 576, 128), (torch.float32, 64, 8)])
+def test_pool_serves_the_latent_cache_of_sparse_attention(cuda_device, dtype, d, heads):
+    """dsa_sparse_mla over pages that the pool handed out, branched and drew together, against the same rows in a
+    contiguous cache (a table as wide as the context, -1 behind each sequence)."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    page, ctx, batch, pages, d_v = 64, 512, 3, 24, 512 if d == 576 else d
+    table = torch.full((batch, ctx // page), -1, dtype=torch.int32, device="cuda")
+    length, count = torch.zeros(batch, dtype=torch.int32, device="cuda"), torch.zeros(pages, dtype=torch.int32, device="cuda")
+    cache = torch.zeros((pages, page, d), dtype=dtype, device="cuda")
+    whole = torch.randn((batch, ctx, d), generator=g, device="cuda").to(dtype)
+    count[[0, 2, 5, 9]] = 1                                 # pages held by someone else
+    lens = [200, 300]
+    dsa.kv_pages_extend(table, length, count, _i32([0, 1]), _i32(lens), page)
+    for b, n in enumerate(lens):
+        for j in range(-(-n // page)):
+            cache[int(table[b, j]), :min(page, n - j * page)] = whole[b, j * page:min(n, (j + 1) * page)]
+    dsa.kv_pages_fork(table, length, count, _i32([1]), _i32([2]), page, [cache])
+    whole[2, :lens[1]] = whole[1, :lens[1]]
+    lens.append(lens[1])
+    count[[0, 2, 5, 9]] = 0
+    dsa.kv_pages_compact(table, count, [cache], table_out=table, ref_out=count)
+    dsa.kv_pages_extend(table, length, count, _i32([2]), _i32([1]), page)
+    lens[2] += 1
+    cache[int(table[2, 300 // page]), 300 % page] = whole[2, 300]
+    idx = torch.full((batch, 256), -1, dtype=torch.int32)
+    for b, n in enumerate(lens):
+        some = torch.randperm(n - 1)[:min(n - 1, 255)].to(torch.int32)
+        idx[b, :len(some)] = some
+        idx[b, len(some)] = n - 1
+    idx, rows = idx.cuda(), _i32([0, 1, 2])
+    q = torch.randn((batch, heads, d), generator=g, device="cuda").to(dtype)
+    out, lse = dsa.sparse_mla(q, cache, idx, rows, 0.05, d_v, ctx, page_table=table)
+    ref, ref_lse = dsa.sparse_mla(q, whole, idx, rows, 0.05, d_v, ctx)
+    assert dsa.get_device_error(cuda_device) == dsa.DSA_OK
+    assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
