@@ -837,3 +837,37 @@ def test_prompt_then_decode_over_the_cache(cuda_device, kind):
             check(o[b][:, None], l[b][:, None], ref, ref_lse, A, d, n, u)
     assert dsa.get_device_error(cuda_device) == dsa.DSA_OK
     assert length.tolist() == [57, 110, 110]
+
+
+def test_calls_without_rows(cuda_device):
+    """Empty batches: nothing is launched, outputs are empty, what the caches hold stays."""
+    kc, vc = (torch.ones((4, 2, 16, 64), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    table, none = _i32([[0, 1]]), _i32([])
+    x = torch.empty((0, 6, 64), dtype=torch.bfloat16, device="cuda")
+    before = dsa.launch_count()
+    dsa.kv_cache_append(x[:, :2], x[:, 2:4], none, none, table, kc, vc)
+    for out, lse in (dsa.gqa_decode_attention(x, kc, vc, table, none, none, 0.1),
+                     dsa.gqa_prompt_attention(x, x[:, :2], x[:, :2], _i32([0, 0]), 0.1)):
+        assert out.shape == (0, 6, 64) and lse.shape == (0, 6)
+    y = torch.ones((3, 6, 64), dtype=torch.bfloat16, device="cuda")
+    kept = torch.full_like(y, 7.0)
+    dsa.gqa_prompt_attention(y, y[:, :2], y[:, :2], _i32([0]), 0.1, out=kept)
+    assert bool((kept == 7).all()) and bool((kc == 1).all()) and bool((vc == 1).all())
+    assert dsa.launch_count() == before
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_fp8_caches_as_bytes(cuda_device, D):
+    """A uint8 cache holds the codes of a float8 one: written and read alike."""
+    g, n = _gen(73), 90
+    table = _i32([[3, 0, 5, 1, 2, 4]])
+    k, v = (_randn((n, 2, D), g, torch.bfloat16) for _ in "kv")
+    batch, pos, q = _i32([0] * n), torch.arange(n, device="cuda", dtype=torch.int32), _randn((1, 8, D), g, torch.bfloat16)
+    got = []
+    for dt in (torch.float8_e4m3fn, torch.uint8):
+        caches = [torch.zeros((6, 2, 16, D), dtype=torch.uint8, device="cuda").view(dt) for _ in "kv"]
+        scales = [torch.zeros((6, 2, 16), device="cuda") for _ in "kv"]
+        dsa.kv_cache_append(k, v, batch, pos, table, *caches, *scales)
+        got.append([x.view(torch.uint8) for x in caches] + scales +
+                   list(dsa.gqa_decode_attention(q, *caches, table, _i32([0]), _i32([n - 1]), 0.1, *scales)))
+    assert all(torch.equal(a, b) for a, b in zip(*got))

@@ -208,6 +208,27 @@ def test_large_pool_and_long_lists(cuda_device):
     p.same()
 
 
+def test_largest_pool_and_list(cuda_device):
+    """As many pages and list entries as a call takes: the books fill the cluster's shared memory."""
+    n, pages, page = 4096, 1 << 22, 4
+    r = random.Random(5)
+    p = Both(2 * n, 9, page, pages, ())
+    held = torch.arange(0, pages, 3, device="cuda")         # a third of the pool is someone else's
+    p.count[held] = 1
+    for i in held.tolist():
+        p.plain.count[i] = 1
+    p.extend(r.sample(range(n), n), [r.randint(0, 9 * page) for _ in range(n)])
+    p.fork([r.randrange(n) for _ in range(n)], r.sample(range(n, 2 * n), n))
+    assert _status() == dsa.DSA_OK
+    p.same()
+    p.free(list(range(n)))
+    p.compact(True)
+    assert _status() == dsa.DSA_OK
+    p.same()
+    with pytest.raises(dsa.DSAError):
+        dsa.kv_pages_free(p.table, p.length, p.count, _i32([0] * (n + 1)), page)
+
+
 def test_captured_turnover(cuda_device):
     """free + extend + fork captured once and replayed: the books follow without a host read."""
     p = Both(6, 8, 4, 40, ((32,),))
