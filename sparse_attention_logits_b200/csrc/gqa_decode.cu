@@ -275,7 +275,7 @@ __device__ __forceinline__ int cache_row(const DecodeArgs& a, Place p) {
 //
 // fp32: every factor is split into two tf32 numbers, x = hi + lo (11 + 11
 // bits), and a product is three tensor products hi hi + hi lo + lo hi, the
-// small ones summed apart.  What is left out or rounded is at most 3 x 2^-22
+// small ones summed apart.  What is left out or rounded is at most 4.5 x 2^-22
 // of |x y| a term.  The tensor core's sums round toward zero, so each slice's
 // output is summed from zero and added to the running one in fp32.
 // WK: keys of a warp's slice; BLOCKS per SM, with STAGES slices in flight per
