@@ -436,7 +436,8 @@ DSA_API size_t gqa_decode_attention_workspace_size(int rows, int n_heads, int n_
  * One row per sequence decodes one token; several rows of a sequence (at
  * successive positions) verify several tokens or run a piece of a prompt.
  * Rows of one sequence beside each other share the reads of its cache as far
- * as their heads fill 16 columns, when rows >= 1.5 * batch.
+ * as their heads fill 16 columns, when rows >= 1.5 * batch (batch is the
+ * page table's number of rows, empty sequences among them).
  *   q          [rows, n_heads, head_dim] of dtype, rows ld_q elements apart, 16-byte
  *              aligned rows; n_heads a multiple of n_kv_heads
  *   row_pos    [rows] int32: last visible token; < 0: none (out = 0, lse = -inf), as
@@ -450,7 +451,13 @@ DSA_API size_t gqa_decode_attention_workspace_size(int rows, int n_heads, int n_
  * sequence is out of range has no visible token; tokens past the table's
  * width (row_pos >= max_pages * page_size) or in a page out of range are left
  * out; each is reported by dsa_get_device_error.  Sums are fp32; results do
- * not depend on the order in which blocks run.
+ * not depend on the order in which blocks run.  Products: over a bf16 cache the
+ * weights exp(z - max) are rounded to bf16.  Over an fp8 cache q is taken as f16 relative
+ * to its row's largest number (bits below 2^-25 of that are lost) and the weights times
+ * v_scale as f16 relative to the head's largest (off by 2^-11 of themselves and
+ * 2^-38 of that at most).  fp32 products are three tf32 ones, off by at most 4.5 x 2^-22
+ * of |x y| a term, for numbers up to 3.402e38.  A NaN in q or in a visible place
+ * shows in what it takes part in.
  */
 DSA_API dsa_status_t gqa_decode_attention(const void* q, int64_t ld_q, dsa_dtype_t dtype, const void* k_cache,
                                   const void* v_cache, dsa_dtype_t kv_dtype, const float* k_scale,
@@ -484,8 +491,9 @@ DSA_API size_t gqa_prompt_attention_workspace_size(int total, int n_seqs, int n_
  * k and v must be finite within a prompt (a later row's infinity or NaN may
  * reach earlier rows of its own prompt); prompts never reach one another.  A
  * prompt whose bounds descend or leave [0, total] is skipped and reported by
- * dsa_get_device_error.  bf16 runs on the tensor cores (P is rounded to bf16),
- * fp32 on the CUDA cores; sums are fp32.
+ * dsa_get_device_error.  Both types run on the tensor cores: bf16 with the weights
+ * exp(z - max) rounded to bf16, fp32 as three tf32 products each (see
+ * gqa_decode_attention); sums are fp32.  A NaN in q shows in its row.
  */
 DSA_API dsa_status_t gqa_prompt_attention(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
                                   int64_t ld_v, dsa_dtype_t dtype, const int32_t* cu_seqlens, int n_seqs, int total,
@@ -519,7 +527,9 @@ DSA_API dsa_status_t gqa_prompt_attention(const void* q, int64_t ld_q, const voi
  * kv_pages_extend -- room for add[i] more tokens in sequence seqs[i]: fresh
  * pages (each with count 1) until the new length fits, seq_len += add.  An
  * entry is served when the pages asked for up to and with it are free.  A
- * sequence that would pass max_pages * page_size tokens is refused.
+ * sequence that would pass max_pages * page_size tokens is refused, and so is
+ * add[i] < 0: sequences are not shortened (with seq_len lowered by hand, the
+ * pages behind it would stay counted and their entries be written over).
  */
 DSA_API dsa_status_t kv_pages_extend(int32_t* page_table, int batch, int max_pages, int page_size, int32_t* seq_len,
                              int32_t* ref_count, int num_pages, const int32_t* seqs, const int32_t* add, int n,

@@ -4,16 +4,17 @@
 // Every visible key and value row is read once for all heads of its group (for
 // each 16 of them, in larger groups), so the cache's bytes at the HBM rate are the floor.  32 sequences of up to
 // 32K tokens, 8 / 32 heads of 128, bf16: 512 us, 6.4 TB/s (a plain copy runs at
-// 6.5); 64 of them, 8 / 64 heads, fp8: 523 us, 6.4 TB/s.  One row of 777 tokens
-// takes 7.2 us, a chain of latencies: rows, pages, cache, joining of the parts.
+// 6.5); 64 of them, 8 / 64 heads, fp8: 530 us, 6.3 TB/s in a short run, and 562,
+// 6.0 TB/s, back to back, where the clock falls under the power limit.  One row of
+// 777 tokens takes 7.3 us, a chain of latencies: rows, pages, cache, joining of the parts.
 //
 // Rows of one sequence that stand beside each other (several tokens verified
 // at once) share its reads too: a bunch is up to `merge` such rows, whose heads
 // fill the 16 columns of the products together; past a row's last key its
 // columns are masked.  Against a pair for every row: 8 sequences of up to 16K
-// tokens, 4 rows each, 8 / 32 heads: 258 -> 80 us in bf16, 124 -> 68 in fp8; 4
-// of up to 5K in fp32 90 -> 50; 16 of up to 100 tokens 10.3 -> 11.3; one of 777
-// tokens 9.3 -> 10.8 us.
+// tokens, 4 rows each, 8 / 32 heads: 258 -> 80 us in bf16, 124 -> 66 in fp8; 4
+// of up to 5K in fp32 90 -> 50; 16 of up to 100 tokens 10.3 -> 11.4; one of 777
+// tokens 9.3 -> 10.9 us.
 //
 // Work split.  A pair is (bunch of rows, kv head, tile of the group's heads); its keys
 // are cut into units of KT (128, in fp32 64).  All pairs' units form
@@ -280,6 +281,9 @@ __device__ __forceinline__ int cache_row(const DecodeArgs& a, Place p) {
 // output is summed from zero and added to the running one in fp32.
 // WK: keys of a warp's slice; BLOCKS per SM, with STAGES slices in flight per
 // warp; Q_BYTES: the query fragments, where the registers have no room for them.
+//
+// Spills: 16 bytes a thread in fp8 with head dim 128 and 8 heads, 4 in fp32 with
+// head dim 128 and 16 heads; none elsewhere.
 //
 // More blocks of one slice a warp hide each other's products and joining better
 // than fewer blocks of several slices, as far as registers allow (us, fewer blocks

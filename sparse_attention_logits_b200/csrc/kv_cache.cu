@@ -40,7 +40,7 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
 // per row walks the chain, while all groups already load the data of their
 // first vectors, which does not depend on it.  64 rows of 8 heads of 128, bf16:
 // 2 us on the GPU; the 20,996 rows of a batch of prompts into an fp8 cache: 29 us,
-// 4.5 TB/s of reads and writes.
+// 4.5 TB/s of reads and writes, into a bf16 one 36 us, 5.2 TB/s, fp32 86 us, 4.7.
 constexpr int APPEND_ROWS = 32, APPEND_UNROLL = 2;
 
 // Codes of sixteen values over their scale.  All share the divisor, so its
